@@ -370,6 +370,115 @@ int ft_host_experts(const void* x, int32_t T, int32_t d, int32_t d_ff, int32_t f
                     const void* const* records, const int32_t* use_off, const int32_t* use_t,
                     const float* use_g, int32_t n_exp, int32_t threads, float* partial);
 
+/* ---- dense operators (stateless) ------------------------------------------------
+ * What a layer has beside its routed experts: a dense gated feed-forward block (a
+ * shared expert, or the dense layers of a stack) with its backward pass, activations
+ * kept in 8 bits between the two, and products with 4-bit weights.  All pointers
+ * are device pointers on the current device, 16-byte aligned unless said otherwise; `ld*`
+ * are row strides in elements (>= the row's length, multiples of 8, at most 2^21).
+ * Streams are ordered as usual: a call reads its inputs and writes its outputs and
+ * its workspace in stream order, keeps nothing afterwards and allocates nothing, so it
+ * may be captured into a HIP graph (a workspace then belongs to that graph's replays
+ * alone).  No output may overlap an input, another output or the workspace, except a
+ * residual given as the output itself (same pointer and stride).  A workspace is
+ * 256-byte aligned; FT_ENOMEM when smaller than its size query says (0 from a query:
+ * bad sizes).  Results do not depend on timing: equal calls give equal bits.
+ * Values that are not finite pass through the sums as IEEE arithmetic has it. */
+typedef enum { FT_T_BF16 = 0, FT_T_FP16 = 1, FT_T_FP32 = 2 } ft_dtype;
+typedef enum { FT_ACT_SILU = 0, FT_ACT_GELU_TANH = 1 } ft_act;
+typedef enum { FT_SAVE_NONE = 0, FT_SAVE_16 = 1, FT_SAVE_MX8 = 2 } ft_save;
+
+/* Gated feed-forward block:
+ *   a = x w_gate^T, u = x w_up^T, h = act(a) * u, y = h w_down^T (+ residual)
+ * x [T, d]; w_gate, w_up [d_ff, d]; w_down [d, d_ff] (contiguous; a bf16 expert record
+ * holds them one after the other); all of `dtype` (bf16 or fp16).  y [T, d] and
+ * residual (may be NULL) of y_dtype: `dtype` or FT_T_FP32.  Sums, the activation and the
+ * residual's addition are fp32; h is rounded to `dtype` between the two products.
+ * d, d_ff multiples of 8; T >= 0, any number of rows (from one token on).
+ * save_fmt keeps a and u for ft_gated_ffn_bwd in `saved`
+ * (ft_gated_ffn_saved_bytes bytes):
+ *   FT_SAVE_NONE  nothing (saved may be NULL)
+ *   FT_SAVE_16    a [T, d_ff] then u [T, d_ff], rounded to `dtype`
+ *   FT_SAVE_MX8   codes of a [T, d_ff], codes of u [T, d_ff], scales of a
+ *                 [T, d_ff / 32], scales of u (see ft_act8_pack); d_ff % 32 == 0.
+ * workspace: ft_gated_ffn_workspace_bytes(T, d, d_ff). */
+size_t ft_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t d_ff);
+size_t ft_gated_ffn_saved_bytes(int32_t T, int32_t d_ff, int32_t save_fmt);
+int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff, int32_t dtype,
+                 int32_t act, const void* w_gate, const void* w_up, const void* w_down,
+                 const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
+                 void* saved, int32_t save_fmt, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/* Its backward pass for dy [T, d] (the residual's gradient is dy itself):
+ *   dh = dy w_down, du = dh act(a), da = dh u act'(a), h = act(a) u
+ *   dx = da w_gate + du w_up, dw_gate = da^T x, dw_up = du^T x, dw_down = dy^T h
+ * dy, dx and the weights' gradients (contiguous, shaped as the weights) are of
+ * `dtype`.  h, da and du are rounded to `dtype` before the products that read them;
+ * sums are fp32.  Gradients are written, not added to.  dx may be NULL (not wanted),
+ * and so may the three weight gradients together.  With T = 0 the weights' gradients
+ * are zeros.
+ * saved, save_fmt: a and u as the forward call kept them; FT_SAVE_NONE computes them
+ * again from x (4 T d d_ff more operations), rounded to `dtype`.
+ * x: `dtype` [T, d], or with x_scales not NULL MX8 codes [T, d] (contiguous, ldx = d,
+ * d % 32 == 0) with their scales [T, d / 32].  Scales and MX8 saves need no alignment
+ * beyond 16 bytes.
+ * workspace: ft_gated_ffn_bwd_workspace_bytes(T, d, d_ff, save_fmt, x_scales != NULL). */
+size_t ft_gated_ffn_bwd_workspace_bytes(int32_t T, int32_t d, int32_t d_ff, int32_t save_fmt,
+                                        int32_t x_mx8);
+int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_t T, int32_t d,
+                     int32_t d_ff, int32_t dtype, int32_t act, const void* w_gate,
+                     const void* w_up, const void* w_down, const void* saved, int32_t save_fmt,
+                     const void* dy, int64_t lddy, void* dx, int64_t lddx, void* dw_gate,
+                     void* dw_up, void* dw_down, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* An activation kept in 8 bits (MX8) and brought back.  src, dst: `dtype` (bf16 or
+ * fp16) [rows, n], n % 32 == 0; codes: E4M3 uint8 [rows, n]; scales: uint8
+ * [rows, n / 32], no alignment needed.  A block of 32 consecutive elements of a row has the scale
+ * 2^e, stored as e + 127, with the least e >= -127 such that its largest finite
+ * magnitude is at most 448 * 2^e: nothing saturates, and an element is off by at most
+ * 2^-4 of itself (or 2^(e - 10)).  Rounding to nearest even; infinities and NaN become
+ * NaN and leave the block's scale to the others; a block of zeros has scale byte 0.  (The MXFP8
+ * conversion of the experts' prefill form takes its exponent from the largest
+ * element alone and clamps.)  Unpacking is exact in bf16 and rounds in fp16, where
+ * magnitudes past 65504 become 65504. */
+int ft_act8_pack(const void* src, int64_t ld, int32_t rows, int32_t n, int32_t dtype,
+                 uint8_t* codes, uint8_t* scales, void* stream);
+int ft_act8_unpack(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t n,
+                   int32_t dtype, void* dst, int64_t ld, void* stream);
+
+/* A matrix [N, K] of 4-bit weights with group scales along K:
+ *   w[n, k] = (code[n, k] - zero[n, k / group]) * scale[n, k / group]
+ * codes: uint8 [N, K / 2], unsigned codes 0..15, the lower k in the low nibble;
+ * scales: [N, K / group] of the activations' dtype; zeros: uint8 [N, K / group], 0..15
+ * (larger values are undefined), or NULL for 8 everywhere.  group 32, 64 or 128;
+ * K % group == 0; any N.  scales need 2-byte alignment, zeros none. */
+typedef struct {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  int32_t N, K, group;
+} ft_w4_matrix;
+
+/* y = x w^T (+ residual): x `dtype` [T, K] (bf16 or fp16), y [T, N] and residual (may
+ * be NULL) of y_dtype, `dtype` or FT_T_FP32.  Weights are applied as the exact
+ * integers code - zero, scaled per group in fp32; fp32 sums.  The decode form: the
+ * weights stream once per 64 tokens; T >= 0.  ldy and ldr are any strides >= N, and y and
+ * residual need their element's alignment only. */
+int ft_w4_gemv(const void* x, int64_t ldx, int32_t T, int32_t dtype, const ft_w4_matrix* w,
+               const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
+               void* stream);
+
+/* The gated block of ft_gated_ffn on 4-bit weights: gate and up [d_ff, d], down
+ * [d, d_ff], one group size or several.  h is rounded to `dtype` between the products.
+ * workspace: ft_w4_gated_ffn_workspace_bytes(T, d_ff). */
+size_t ft_w4_gated_ffn_workspace_bytes(int32_t T, int32_t d_ff);
+int ft_w4_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_t act,
+                    const ft_w4_matrix* gate, const ft_w4_matrix* up, const ft_w4_matrix* down,
+                    const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- expert cache -------------------------------------------------------------- */
 
 /* Decisions of one decode call for routed ids idx_host (host int32 [T, k]):

@@ -32,7 +32,10 @@ HOST_FLAGS = ["-x", "c++", "-D__HIP_PLATFORM_AMD__", f"-I{os.path.join(ROCM, 'in
 SOURCES = [
     ("kernels.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("kernels_mx.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
+    ("kernels_dense.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
+    ("kernels_w4.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("api.cpp", CXX, HOST_FLAGS),
+    ("api_dense.cpp", CXX, HOST_FLAGS),
     ("cache.cpp", CXX, HOST_FLAGS),
     ("qstar.cpp", CXX, HOST_FLAGS),
     ("bwprofile.cpp", CXX, HOST_FLAGS),

@@ -138,6 +138,57 @@ int launch_mx_ffn_mfma(const uint16_t* x, int T, int d, int d_ff, int k, const u
 int launch_combine(const float* out, const int32_t* inv, const float* gates,
                    const float* cpu_partial, int T, int k, int d, float* y, void* stream);
 
+// ---- dense operators (kernels_dense.hip) -----------------------------------------
+// A gated block with its tensors checked and its workspace laid out.
+struct DenseFfn {
+  const uint16_t *x, *wg, *wu, *wd;
+  int64_t ldx;
+  int T, d, d_ff, dtype, act;
+  // forward: null y computes a and u alone
+  const void* res;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int y_f32;
+  // a and u: 16 bits, or MX8 codes with their scales (sca, scu not null)
+  int save_fmt;
+  void *sa, *su;
+  uint8_t *sca, *scu;
+  uint16_t* h;  // [T, d_ff]
+};
+struct DenseGrad {
+  const uint16_t* dy;
+  int64_t lddy;
+  uint16_t* dx;  // null: not wanted
+  int64_t lddx;
+  uint16_t *dwg, *dwu, *dwd;  // all or none
+  uint16_t* dag;              // [T, 2 d_ff]: da, du
+};
+int launch_gated_ffn(const DenseFfn& F, void* stream);
+int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream);
+int launch_act8_pack(const uint16_t* src, int64_t ld, int rows, int n, bool half, uint8_t* codes, uint8_t* scales,
+                     void* stream);
+int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, uint16_t* dst,
+                       int64_t ld, void* stream);
+
+// ---- products with 4-bit weights (kernels_w4.hip) ----------------------------------
+struct W4Args {
+  const uint16_t* x;
+  int64_t ldx;
+  int T, K, N, G, act;
+  bool half;
+  const uint8_t *codes, *codes2;    // codes2, scales2, zeros2: the up matrix of a gate/up product
+  const uint16_t *scales, *scales2;
+  const uint8_t *zeros, *zeros2;    // null: 8
+  uint16_t* h;                      // gate/up: [T, N]
+  const void* res;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int y_f32;
+};
+int launch_w4(const W4Args& A, bool gate_up, void* stream);
+
 // ---- host expert kernel (cpu_exec.cpp) ----------------------------------------
 // One batch of CPU-branch work: experts `n_exp`, each with a record pointer and a
 // list of (token, gate) uses.  Computes partial[t] += sum gate * FFN_e(x[t]).

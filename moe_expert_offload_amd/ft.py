@@ -27,6 +27,14 @@ FT_WOVERLAP_OFF = 1
 FT_PLAN_CAP = 512
 FT_W_BF16 = 0
 FT_W_MXFP4 = 1
+FT_T_BF16 = 0
+FT_T_FP16 = 1
+FT_T_FP32 = 2
+FT_ACT_SILU = 0
+FT_ACT_GELU_TANH = 1
+FT_SAVE_NONE = 0
+FT_SAVE_16 = 1
+FT_SAVE_MX8 = 2
 FT_PLACE_LRU = 0
 FT_PLACE_HOTSET = 1
 FT_PLACE_STATIC = 2
@@ -44,6 +52,9 @@ EXPORTED = [
     "ft_bw_profile_path", "ft_bw_profile_save", "ft_bw_profile_load", "ft_expert_cache_prefill_on_demand",
     "ft_replay_placement", "ft_layer_routing", "ft_decode_graph_create",
     "ft_decode_graph_launch", "ft_decode_graph_status", "ft_decode_graph_destroy", "ft_permute_noalloc", "ft_permute_noalloc_max_scratch_bytes",
+    "ft_gated_ffn_workspace_bytes", "ft_gated_ffn_saved_bytes", "ft_gated_ffn", "ft_gated_ffn_bwd_workspace_bytes",
+    "ft_gated_ffn_bwd", "ft_act8_pack", "ft_act8_unpack", "ft_w4_gemv", "ft_w4_gated_ffn_workspace_bytes",
+    "ft_w4_gated_ffn",
 ]
 
 
@@ -102,6 +113,11 @@ class ft_profile(C.Structure):
                 ("flops_down", C.c_double)]
 
 
+class ft_w4_matrix(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("zeros", C.c_void_p), ("N", C.c_int32),
+                ("K", C.c_int32), ("group", C.c_int32)]
+
+
 class FtError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn} failed: {status} ({msg})")
@@ -111,6 +127,8 @@ class FtError(RuntimeError):
 _lib = None
 P = C.c_void_p
 I = C.c_int32
+L64 = C.c_int64
+Z = C.c_size_t
 
 
 def lib():
@@ -155,6 +173,17 @@ def lib():
             "ft_grouped_ffn": (C.c_int, [P, I, I, I, I, P, P, P, P, I, I, I, I, P, P, I, P]),
             "ft_grouped_ffn_mx_workspace_bytes": (C.c_size_t, [I, I, I, I]),
             "ft_grouped_ffn_mx": (C.c_int, [P, I, I, I, I, P, P, P, P, I, I, I, I, I, P, C.c_size_t, P, I, P]),
+            "ft_gated_ffn_workspace_bytes": (Z, [I, I, I]),
+            "ft_gated_ffn_saved_bytes": (Z, [I, I, I]),
+            "ft_gated_ffn": (C.c_int, [P, L64, I, I, I, I, I, P, P, P, P, L64, P, L64, I, P, I, P, Z, P]),
+            "ft_gated_ffn_bwd_workspace_bytes": (Z, [I, I, I, I, I]),
+            "ft_gated_ffn_bwd": (C.c_int, [P, L64, P, I, I, I, I, I, P, P, P, P, I, P, L64, P, L64, P, P, P, P, Z, P]),
+            "ft_act8_pack": (C.c_int, [P, L64, I, I, I, P, P, P]),
+            "ft_act8_unpack": (C.c_int, [P, P, I, I, I, P, L64, P]),
+            "ft_w4_gemv": (C.c_int, [P, L64, I, I, C.POINTER(ft_w4_matrix), P, L64, P, L64, I, P]),
+            "ft_w4_gated_ffn_workspace_bytes": (Z, [I, I]),
+            "ft_w4_gated_ffn": (C.c_int, [P, L64, I, I, I, C.POINTER(ft_w4_matrix), C.POINTER(ft_w4_matrix),
+                                          C.POINTER(ft_w4_matrix), P, L64, P, L64, I, P, Z, P]),
             "ft_combine": (C.c_int, [P, P, P, P, I, I, I, P, P]),
             "ft_expert_cache_lookup": (C.c_int, [P, I, P, I, C.POINTER(ft_plan)]),
             "ft_expert_cache_fill": (C.c_int, [P, C.POINTER(ft_plan), P, P, P]),
@@ -390,6 +419,64 @@ def ft_grouped_ffn_mx(x, T, d, d_ff, k, slots, group_slot, offsets, perm, n_grou
     return _check("ft_grouped_ffn_mx", lib().ft_grouped_ffn_mx(
         _ptr(x), T, d, d_ff, k, _ptr(slots), _ptr(group_slot), _ptr(offsets), _ptr(perm), n_groups, g_begin,
         g_end, max_rows_per_group, n_rows, _ptr(workspace), workspace_bytes, _ptr(out), form, _stream(stream)))
+
+
+def ft_gated_ffn_workspace_bytes(T, d, d_ff):
+    return lib().ft_gated_ffn_workspace_bytes(T, d, d_ff)
+
+
+def ft_gated_ffn_saved_bytes(T, d_ff, save_fmt):
+    return lib().ft_gated_ffn_saved_bytes(T, d_ff, save_fmt)
+
+
+def ft_gated_ffn(x, ldx, T, d, d_ff, dtype, act, w_gate, w_up, w_down, residual, ldr, y, ldy, y_dtype, saved, save_fmt,
+                 workspace, workspace_bytes, stream=None):
+    return _check("ft_gated_ffn", lib().ft_gated_ffn(
+        _ptr(x), ldx, T, d, d_ff, dtype, act, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(residual), ldr, _ptr(y),
+        ldy, y_dtype, _ptr(saved), save_fmt, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ft_gated_ffn_bwd_workspace_bytes(T, d, d_ff, save_fmt, x_mx8):
+    return lib().ft_gated_ffn_bwd_workspace_bytes(T, d, d_ff, save_fmt, 1 if x_mx8 else 0)
+
+
+def ft_gated_ffn_bwd(x, ldx, x_scales, T, d, d_ff, dtype, act, w_gate, w_up, w_down, saved, save_fmt, dy, lddy, dx,
+                     lddx, dw_gate, dw_up, dw_down, workspace, workspace_bytes, stream=None):
+    return _check("ft_gated_ffn_bwd", lib().ft_gated_ffn_bwd(
+        _ptr(x), ldx, _ptr(x_scales), T, d, d_ff, dtype, act, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(saved),
+        save_fmt, _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def ft_act8_pack(src, ld, rows, n, dtype, codes, scales, stream=None):
+    return _check("ft_act8_pack", lib().ft_act8_pack(_ptr(src), ld, rows, n, dtype, _ptr(codes), _ptr(scales),
+                                                     _stream(stream)))
+
+
+def ft_act8_unpack(codes, scales, rows, n, dtype, dst, ld, stream=None):
+    return _check("ft_act8_unpack", lib().ft_act8_unpack(_ptr(codes), _ptr(scales), rows, n, dtype, _ptr(dst), ld,
+                                                         _stream(stream)))
+
+
+def make_w4_matrix(codes, scales, zeros, N, K, group):
+    """A 4-bit matrix of device tensors (or addresses); the caller keeps them alive."""
+    return ft_w4_matrix(_ptr(codes), _ptr(scales), _ptr(zeros), N, K, group)
+
+
+def ft_w4_gemv(x, ldx, T, dtype, w, residual, ldr, y, ldy, y_dtype, stream=None):
+    return _check("ft_w4_gemv", lib().ft_w4_gemv(_ptr(x), ldx, T, dtype, C.byref(w), _ptr(residual), ldr, _ptr(y), ldy,
+                                                 y_dtype, _stream(stream)))
+
+
+def ft_w4_gated_ffn_workspace_bytes(T, d_ff):
+    return lib().ft_w4_gated_ffn_workspace_bytes(T, d_ff)
+
+
+def ft_w4_gated_ffn(x, ldx, T, dtype, act, gate, up, down, residual, ldr, y, ldy, y_dtype, workspace, workspace_bytes,
+                    stream=None):
+    return _check("ft_w4_gated_ffn", lib().ft_w4_gated_ffn(
+        _ptr(x), ldx, T, dtype, act, C.byref(gate), C.byref(up), C.byref(down), _ptr(residual), ldr, _ptr(y), ldy,
+        y_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def ft_combine(out, inv, gates, cpu_partial, T, k, d, y, stream=None):
