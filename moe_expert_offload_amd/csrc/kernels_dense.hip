@@ -57,7 +57,8 @@ __device__ __forceinline__ float fit16(float v) {
 // A block computes a BM x BN tile with WM x WN waves of (BM / WM) x 64.  K runs in stages of
 // 64: both operands go straight from memory into one of two LDS buffers, one stage ahead.
 //   - An operand along k: LDS rows of 64 elements (128 bytes), the 16-byte piece p of row r at
-//     place p ^ (r & 7), so that the 8 lanes of a read phase hit 8 different pieces.
+//     place p ^ (r / 2 & 7): the 16 rows of a read phase then use all 16 pieces of two rows'
+//     banks once (p ^ (r & 7) put rows r and r + 8 on the same banks: twice the LDS cycles).
 //   - A transposed operand: LDS rows are the 64 k of the stage, each BM (or BN) elements,
 //     piece p of row k at p ^ ((k & 3) << 2); fragments come through the transposing LDS read
 //     (16 lanes read 4 rows of k and get one column of 4 k each), whose 4 rows then fall
@@ -105,6 +106,185 @@ __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
   b = r.y;
 }
 
+// What becomes of one 32-row piece of a wave's result: c0 and c1 are its 32x32 results at columns
+// nb0 and nb1 (kGateUp: a and u of the same columns).  The lane holds row m, and in quad q the
+// columns 8 q + 4 hi + 0..3 of each.
+template <int MODE, bool H>
+__device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16_t& c0, const f32x16_t& c1, int m, int nb0,
+                                         int nb1, int hi) {
+  const bool mok = m < p.M;
+  if constexpr (MODE == kGateUp) {
+    const int nb = nb0;  // the 32 columns of a, u and h
+    if (p.sca) {
+      // whole blocks of 32 (N % 32 == 0): this lane and its other half hold one block of row m
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float am = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) am = fmaxf(am, fin_abs((j ? c1 : c0)[e]));
+        am = fmaxf(am, __shfl_xor(am, 32, WAVE));
+        const int sc = mx8_scale(am);
+        uint8_t* cd = static_cast<uint8_t*>(j ? p.su : p.sa) + (int64_t)m * p.N + nb;
+        if (mok && nb < p.N) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint32_t*>(cd + 8 * q + 4 * hi) = mx8_codes4(
+                (j ? c1 : c0)[4 * q], (j ? c1 : c0)[4 * q + 1], (j ? c1 : c0)[4 * q + 2], (j ? c1 : c0)[4 * q + 3], sc);
+          if (hi == 0) (j ? p.scu : p.sca)[(int64_t)m * (p.N >> 5) + (nb >> 5)] = (uint8_t)sc;
+        }
+      }
+    } else if (p.sa) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint16_t* dst = static_cast<uint16_t*>(j ? p.su : p.sa) + (int64_t)m * p.N;
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack2<H>((j ? c1 : c0)[4 * q + 2 * e], (j ? c1 : c0)[4 * q + 2 * e + 1]);
+          swap_halves(w[0], w[2]);
+          swap_halves(w[1], w[3]);
+          const int n = nb + 8 * q + 8 * hi;
+          if (mok && n < p.N) *reinterpret_cast<uint4*>(dst + n) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (p.h) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 4 * q + 2 * e;
+          w[e] = pack2<H>(act_f(c0[k], p.act) * c1[k], act_f(c0[k + 1], p.act) * c1[k + 1]);
+        }
+        swap_halves(w[0], w[2]);
+        swap_halves(w[1], w[3]);
+        const int n = nb + 8 * q + 8 * hi;
+        if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  } else if constexpr (MODE == kDh) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int nb = j ? nb1 : nb0;
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const int n = nb + 8 * q + 8 * hi;  // after the exchange this lane holds n .. n + 7
+        const bool ok = mok && n < p.N;
+        const int64_t at = (int64_t)m * p.N + n;
+        float g[8], a[8], u[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t x = __float_as_uint((j ? c1 : c0)[4 * q + e]), y = __float_as_uint((j ? c1 : c0)[4 * q + 4 + e]);
+          swap_halves(x, y);
+          g[e] = __uint_as_float(x);
+          g[4 + e] = __uint_as_float(y);
+        }
+        if (p.sca) {
+          uint2 ca = make_uint2(0, 0), cu = ca;
+          int ea = 0, eu = 0;
+          if (ok) {
+            ca = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.sa) + at);
+            cu = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.su) + at);
+            ea = p.sca[(int64_t)m * (p.N >> 5) + (nb >> 5)];
+            eu = p.scu[(int64_t)m * (p.N >> 5) + (nb >> 5)];
+          }
+          mx8_values4(ca.x, ea, a);
+          mx8_values4(ca.y, ea, a + 4);
+          mx8_values4(cu.x, eu, u);
+          mx8_values4(cu.y, eu, u + 4);
+        } else {
+          uint4 va = make_uint4(0, 0, 0, 0), vu = va;
+          if (ok) {
+            va = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.sa) + at);
+            vu = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.su) + at);
+          }
+          const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[2 * e] = lo16<H>(wa[e]);
+            a[2 * e + 1] = hi16<H>(wa[e]);
+            u[2 * e] = lo16<H>(wu[e]);
+            u[2 * e + 1] = hi16<H>(wu[e]);
+          }
+        }
+        uint32_t oh[4], oa[4], ou[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const ActD f0 = act_df(a[2 * e], p.act), f1 = act_df(a[2 * e + 1], p.act);
+          oh[e] = pack2<H>(f0.f * u[2 * e], f1.f * u[2 * e + 1]);
+          oa[e] = pack2<H>(g[2 * e] * u[2 * e] * f0.df, g[2 * e + 1] * u[2 * e + 1] * f1.df);
+          ou[e] = pack2<H>(g[2 * e] * f0.f, g[2 * e + 1] * f1.f);
+        }
+        if (ok) {
+          *reinterpret_cast<uint4*>(p.h + at) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+          uint16_t* dg = p.dag + 2 * (int64_t)m * p.N + n;
+          *reinterpret_cast<uint4*>(dg) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+          *reinterpret_cast<uint4*>(dg + p.N) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int nb = j ? nb1 : nb0;
+      if (MODE == kOut && p.c_f32) {
+        float* c = static_cast<float*>(p.c) + (int64_t)m * p.ldc;
+        const float* r = static_cast<const float*>(p.res) + (int64_t)m * p.ldr;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = nb + 8 * q + 4 * hi;
+          if (mok && n < p.N) {
+            float4 v = make_float4((j ? c1 : c0)[4 * q], (j ? c1 : c0)[4 * q + 1], (j ? c1 : c0)[4 * q + 2], (j ? c1 : c0)[4 * q + 3]);
+            if (p.res) {
+              const float4 o = *reinterpret_cast<const float4*>(r + n);
+              v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+            *reinterpret_cast<float4*>(c + n) = v;
+          }
+        }
+      } else {
+        uint16_t* c = static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc;
+        if (MODE == kDw && m >= p.split) c = static_cast<uint16_t*>(p.c2) + (int64_t)(m - p.split) * p.ldc;
+        const uint16_t* r = static_cast<const uint16_t*>(p.res) + (int64_t)m * p.ldr;
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          const int n = nb + 8 * q + 8 * hi;
+          const bool ok = mok && n < p.N;
+          if (MODE == kOut && p.res) {
+            // the sum in fp32, then one rounding
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x = __float_as_uint((j ? c1 : c0)[4 * q + e]), y = __float_as_uint((j ? c1 : c0)[4 * q + 4 + e]);
+              swap_halves(x, y);
+              v[e] = __uint_as_float(x);
+              v[4 + e] = __uint_as_float(y);
+            }
+            if (ok) {
+              const uint4 o = *reinterpret_cast<const uint4*>(r + n);
+              const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<H>(v[2 * e] + lo16<H>(ow[e]), v[2 * e + 1] + hi16<H>(ow[e]));
+              *reinterpret_cast<uint4*>(c + n) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack2<H>((j ? c1 : c0)[4 * q + 2 * e], (j ? c1 : c0)[4 * q + 2 * e + 1]);
+            swap_halves(w[0], w[2]);
+            swap_halves(w[1], w[3]);
+            if (ok) *reinterpret_cast<uint4*>(c + n) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int MODE, bool H, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs p) {
   constexpr bool AT = MODE == kDw;
@@ -131,7 +311,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
   for (int j = 0; j < LA; ++j) {
     const int q = (wave * LA + j) * 64 + lane;
     if constexpr (!AT) {
-      const int r = q >> 3, pc = (q & 7) ^ (r & 7);
+      const int r = q >> 3, pc = (q & 7) ^ ((r >> 1) & 7);
       kA[j] = pc * 8;
       offA[j] = m0 + r < p.M ? (uint32_t)(r * p.lda * 2 + pc * 16) : kOOB;
     } else {
@@ -145,7 +325,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
   for (int j = 0; j < LB; ++j) {
     const int q = (wave * LB + j) * 64 + lane;
     if constexpr (!BT) {
-      const int r = q >> 3, pc = (q & 7) ^ (r & 7);
+      const int r = q >> 3, pc = (q & 7) ^ ((r >> 1) & 7);
       const int n = MODE == kGateUp ? (r >> 6) * 32 + (r & 31) : r;
       kB[j] = pc * 8;
       offB[j] = n0 + n < p.N ? (uint32_t)(n * p.ldb * 2 + pc * 16) : kOOB;
@@ -192,9 +372,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 
   // ---- fragments ----
   const int hi = lane >> 5, l31 = lane & 31;
-  // along k: row l31 of the subtile, piece (2 slice + hi) ^ (row & 7)
+  // along k: row l31 of the subtile, piece (2 slice + hi) ^ (row / 2 & 7)
   auto frag_k = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
-    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ (l31 & 7)) << 4));
+    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
   };
   // transposed: rows k = 16 slice + 8 hi + {0, 4} + kk, columns 16 ((lane >> 4) & 1) + 4 (lane & 3)
   const int kk = (lane >> 2) & 3;
@@ -240,181 +420,205 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
-  // ---- epilogues: lane holds row m, quads q of n = 8 q + 4 hi + 0..3 ----
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int m = m0 + wm * TM + i * 32 + l31;
-    const bool mok = m < p.M;
-    if constexpr (MODE == kGateUp) {
-      const int nb = n0 + wn * 32;  // the wave's 32 columns of a, u and h
-      if (p.sca) {
-        // whole blocks of 32 (N % 32 == 0): this lane and its other half hold one block of row m
+    const int nb = n0 + wn * (MODE == kGateUp ? 32 : 64);
+    epilogue<MODE, H>(p, acc[i][0], acc[i][1], m0 + wm * TM + i * 32 + l31, nb, nb + 32, hi);
+  }
+}
+
+// The same product on 256 x 256 tiles, for results large enough to fill the chip with them.
+// 8 waves, two per SIMD; each computes 64 rows and 32 columns of every 128 x 128 quarter.  A
+// stage of 64 k is four regions of 16 KB (the two halves of A's rows and of B's), two stages
+// in LDS.  A stage is four steps, one per quarter: a read section (fragments from LDS, loads
+// into regions that everyone has read) and a multiply section (8 MFMAs), each closed by a
+// barrier.  The waves 4..7 run one section behind the waves 0..3, so on every SIMD one
+// wave multiplies while the other reads.  With sections t = 0..7 of a stage for the first
+// group:
+//   t  first group                              second group (one section later)
+//   0  read A0, B0                              -
+//   1  A0 x B0                                  read A0, B0
+//   2  read B1; load A0, B0 of stage s + 2      A0 x B0
+//   3  A0 x B1                                  read B1; load A0, B0 of s + 2
+//   4  read A1; load B1 of s + 2                A0 x B1
+//   5  A1 x B1                                  read A1; load B1 of s + 2
+//   6  load A1 of s + 2; wait for A0, B0, B1 of s + 1
+//   7  A1 x B0                                  load A1 of s + 2; wait
+// A region is loaded again two sections after the first group read it, one after the
+// second did (both end a read section with their reads done), and is waited for, by both groups, at least one
+// barrier before its first read; between the two lie 1.5 stages or more.  Loads past the last stage are
+// masked (they write zeros nobody reads), which keeps the counts of the waits.
+template <int MODE, bool H>
+__global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
+  constexpr bool AT = MODE == kDw;
+  constexpr bool BT = MODE == kDh || MODE == kDx || MODE == kDw;
+  constexpr int REG = 16384;
+  enum { A0 = 0, B0 = REG, B1 = 2 * REG, A1 = 3 * REG, STAGE = 4 * REG };
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[2 * STAGE];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+
+  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int per = 8 * p.tiles_n, grp = lb / per, first = grp * 8;
+  const int rows = min(8, p.tiles_m - first), in = lb - grp * per;
+  const int m0 = (first + in % rows) * 256, n0 = (in / rows) * (MODE == kGateUp ? 128 : 256);
+
+  // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
+  uint32_t offA[2][2], offB[2][2];  // [half][chunk]
+  int kA[2], kB[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float am = 0.0f;
+  for (int j = 0; j < 2; ++j) {
+    const int c = wave * 2 + j;
+    const int r = c * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);       // along k
+    const int kt = c * 4 + (lane >> 4), pt = (lane & 15) ^ ((lane >> 4) << 2);  // transposed
+    kA[j] = AT ? kt : pk * 8;
+    kB[j] = BT ? kt : pk * 8;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) am = fmaxf(am, fin_abs(acc[i][j][e]));
-          am = fmaxf(am, __shfl_xor(am, 32, WAVE));
-          const int sc = mx8_scale(am);
-          uint8_t* cd = static_cast<uint8_t*>(j ? p.su : p.sa) + (int64_t)m * p.N + nb;
-          if (mok && nb < p.N) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint32_t*>(cd + 8 * q + 4 * hi) = mx8_codes4(
-                  acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3], sc);
-            if (hi == 0) (j ? p.scu : p.sca)[(int64_t)m * (p.N >> 5) + (nb >> 5)] = (uint8_t)sc;
-          }
-        }
-      } else if (p.sa) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint16_t* dst = static_cast<uint16_t*>(j ? p.su : p.sa) + (int64_t)m * p.N;
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack2<H>(acc[i][j][4 * q + 2 * e], acc[i][j][4 * q + 2 * e + 1]);
-            swap_halves(w[0], w[2]);
-            swap_halves(w[1], w[3]);
-            const int n = nb + 8 * q + 8 * hi;
-            if (mok && n < p.N) *reinterpret_cast<uint4*>(dst + n) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      if (p.h) {
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 4 * q + 2 * e;
-            w[e] = pack2<H>(act_f(acc[i][0][k], p.act) * acc[i][1][k], act_f(acc[i][0][k + 1], p.act) * acc[i][1][k + 1]);
-          }
-          swap_halves(w[0], w[2]);
-          swap_halves(w[1], w[3]);
-          const int n = nb + 8 * q + 8 * hi;
-          if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    } else if constexpr (MODE == kDh) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int nb = n0 + wn * 64 + j * 32;
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          const int n = nb + 8 * q + 8 * hi;  // after the exchange this lane holds n .. n + 7
-          const bool ok = mok && n < p.N;
-          const int64_t at = (int64_t)m * p.N + n;
-          float g[8], a[8], u[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t x = __float_as_uint(acc[i][j][4 * q + e]), y = __float_as_uint(acc[i][j][4 * q + 4 + e]);
-            swap_halves(x, y);
-            g[e] = __uint_as_float(x);
-            g[4 + e] = __uint_as_float(y);
-          }
-          if (p.sca) {
-            uint2 ca = make_uint2(0, 0), cu = ca;
-            int ea = 0, eu = 0;
-            if (ok) {
-              ca = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.sa) + at);
-              cu = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.su) + at);
-              ea = p.sca[(int64_t)m * (p.N >> 5) + (nb >> 5)];
-              eu = p.scu[(int64_t)m * (p.N >> 5) + (nb >> 5)];
-            }
-            mx8_values4(ca.x, ea, a);
-            mx8_values4(ca.y, ea, a + 4);
-            mx8_values4(cu.x, eu, u);
-            mx8_values4(cu.y, eu, u + 4);
-          } else {
-            uint4 va = make_uint4(0, 0, 0, 0), vu = va;
-            if (ok) {
-              va = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.sa) + at);
-              vu = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.su) + at);
-            }
-            const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              a[2 * e] = lo16<H>(wa[e]);
-              a[2 * e + 1] = hi16<H>(wa[e]);
-              u[2 * e] = lo16<H>(wu[e]);
-              u[2 * e + 1] = hi16<H>(wu[e]);
-            }
-          }
-          uint32_t oh[4], oa[4], ou[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const ActD f0 = act_df(a[2 * e], p.act), f1 = act_df(a[2 * e + 1], p.act);
-            oh[e] = pack2<H>(f0.f * u[2 * e], f1.f * u[2 * e + 1]);
-            oa[e] = pack2<H>(g[2 * e] * u[2 * e] * f0.df, g[2 * e + 1] * u[2 * e + 1] * f1.df);
-            ou[e] = pack2<H>(g[2 * e] * f0.f, g[2 * e + 1] * f1.f);
-          }
-          if (ok) {
-            *reinterpret_cast<uint4*>(p.h + at) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-            uint16_t* dg = p.dag + 2 * (int64_t)m * p.N + n;
-            *reinterpret_cast<uint4*>(dg) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-            *reinterpret_cast<uint4*>(dg + p.N) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int nb = n0 + wn * 64 + j * 32;
-        if (MODE == kOut && p.c_f32) {
-          float* c = static_cast<float*>(p.c) + (int64_t)m * p.ldc;
-          const float* r = static_cast<const float*>(p.res) + (int64_t)m * p.ldr;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = nb + 8 * q + 4 * hi;
-            if (mok && n < p.N) {
-              float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-              if (p.res) {
-                const float4 o = *reinterpret_cast<const float4*>(r + n);
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-              }
-              *reinterpret_cast<float4*>(c + n) = v;
-            }
-          }
-        } else {
-          uint16_t* c = static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc;
-          if (MODE == kDw && m >= p.split) c = static_cast<uint16_t*>(p.c2) + (int64_t)(m - p.split) * p.ldc;
-          const uint16_t* r = static_cast<const uint16_t*>(p.res) + (int64_t)m * p.ldr;
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            const int n = nb + 8 * q + 8 * hi;
-            const bool ok = mok && n < p.N;
-            if (MODE == kOut && p.res) {
-              // the sum in fp32, then one rounding
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t x = __float_as_uint(acc[i][j][4 * q + e]), y = __float_as_uint(acc[i][j][4 * q + 4 + e]);
-                swap_halves(x, y);
-                v[e] = __uint_as_float(x);
-                v[4 + e] = __uint_as_float(y);
-              }
-              if (ok) {
-                const uint4 o = *reinterpret_cast<const uint4*>(r + n);
-                const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = pack2<H>(v[2 * e] + lo16<H>(ow[e]), v[2 * e + 1] + hi16<H>(ow[e]));
-                *reinterpret_cast<uint4*>(c + n) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack2<H>(acc[i][j][4 * q + 2 * e], acc[i][j][4 * q + 2 * e + 1]);
-              swap_halves(w[0], w[2]);
-              swap_halves(w[1], w[3]);
-              if (ok) *reinterpret_cast<uint4*>(c + n) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (AT)
+        offA[h][j] = m0 + h * 128 + pt * 8 < p.M ? (uint32_t)(kt * p.lda * 2 + pt * 16) : kOOB;
+      else
+        offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda * 2 + pk * 16) : kOOB;
+      const int nh = n0 + (MODE == kGateUp ? 0 : h * 128);
+      if constexpr (BT)
+        offB[h][j] = nh + pt * 8 < p.N ? (uint32_t)(kt * p.ldb * 2 + pt * 16) : kOOB;
+      else
+        offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.ldb * 2 + pk * 16) : kOOB;
     }
+  }
+  const int per_seg = (p.K + 63) >> 6;
+  const int stages = MODE == kDx ? 2 * per_seg : per_seg;
+  const uint32_t sm0 = lds_addr(sm) + wave * 2048;
+
+  auto load_a = [&](int s, int h) {
+    int k0 = s << 6;
+    const uint16_t* pa = p.a;
+    if (MODE == kDx && s >= per_seg) {
+      k0 = (s - per_seg) << 6;
+      pa = p.a + p.K;
+    }
+    const int left = p.K - k0;
+    const auto rs = rsrc_of(AT ? pa + k0 * p.lda + m0 + h * 128 : pa + (int64_t)(m0 + h * 128) * p.lda + k0);
+    const uint32_t dst = sm0 + (s & 1) * STAGE + (h ? A1 : A0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) lds_load16(rs, kA[j] < left ? offA[h][j] : kOOB, 0, dst + j * 1024);
+  };
+  auto load_b = [&](int s, int h) {
+    int k0 = s << 6;
+    const uint16_t* pb = p.b;
+    if (MODE == kDx && s >= per_seg) {
+      k0 = (s - per_seg) << 6;
+      pb = p.b2;
+    }
+    int nh = n0 + h * 128;
+    if (MODE == kGateUp) {
+      nh = n0;
+      pb = h ? p.b2 : p.b;
+    }
+    const int left = p.K - k0;
+    const auto rs = rsrc_of(BT ? pb + k0 * p.ldb + nh : pb + (int64_t)nh * p.ldb + k0);
+    const uint32_t dst = sm0 + (s & 1) * STAGE + (h ? B1 : B0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) lds_load16(rs, kB[j] < left ? offB[h][j] : kOOB, 0, dst + j * 1024);
+  };
+
+  // ---- fragments of a region: 32 rows (or columns) from `row`, slice of 16 k ----
+  const int hi = lane >> 5, l31 = lane & 31, kk = (lane >> 2) & 3;
+  auto frag_k = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
+  };
+  auto frag_t = [&](const uint8_t* base, int col, int slice) -> i32x4_t {
+    const int pc = ((col >> 3) ^ (kk << 2)) + ((lane >> 3) & 2) + ((lane >> 1) & 1);
+    const uint8_t* q = base + (16 * slice + 8 * hi + kk) * 256 + pc * 16 + (lane & 1) * 8;
+    typedef __attribute__((address_space(3))) s16x4_t* lp;
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)q));
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(q + 1024)));
+    return i32x4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
+  };
+
+  f32x16_t acc[4][2];  // [2 half + 32-row piece][half of the columns]
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
+  i32x4_t fa[2][4], fb0[4], fb1[4];
+
+  auto read_a = [&](const uint8_t* base) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        fa[i][k] = AT ? frag_t(base, wm * 64 + i * 32, k) : frag_k(base, wm * 64 + i * 32, k);
+  };
+  auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = BT ? frag_t(base, wn * 32, k) : frag_k(base, wn * 32, k);
+  };
+  auto multiply = [&](int half, int col, const i32x4_t (&f)[4]) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[2 * half + i][col] = mfma32<H>(f[k], fa[i][k], acc[2 * half + i][col]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // The end of a section: nothing moves across.
+  auto meet = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+
+  if (stages > 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      load_a(s, 0);
+      load_b(s, 0);
+      load_b(s, 1);
+      load_a(s, 1);
+    }
+    asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of stage 0
+    meet();
+    if (wm) meet();
+    for (int s = 0; s < stages; ++s) {
+      const uint8_t* st = sm + (s & 1) * STAGE;
+      read_a(st + A0);
+      read_b(st + B0, fb0);
+      reads_done();
+      meet();
+      multiply(0, 0, fb0);
+      meet();
+      read_b(st + B1, fb1);
+      load_a(s + 2, 0);
+      load_b(s + 2, 0);
+      reads_done();
+      asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // A1 of this stage
+      meet();
+      multiply(0, 1, fb1);
+      meet();
+      read_a(st + A1);
+      load_b(s + 2, 1);
+      reads_done();
+      meet();
+      multiply(1, 1, fb1);
+      meet();
+      load_a(s + 2, 1);
+      asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the next stage
+      meet();
+      multiply(1, 0, fb0);
+      meet();
+    }
+    if (!wm) meet();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the masked loads' writes too
+  }
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + l31;
+    const int nb = n0 + wn * 32;
+    epilogue<MODE, H>(p, acc[i][0], acc[i][1], m, nb, nb + 128, hi);
   }
 }
 
@@ -555,27 +759,26 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
 
 // ---- launches -------------------------------------------------------------------------
 
-template <int MODE, bool H, int BM, int BN, int WM, int WN>
+template <int MODE, bool H>
 int gemm_go(GemmArgs& A, hipStream_t s) {
-  A.tiles_m = (A.M + BM - 1) / BM;
-  const int bn = MODE == kGateUp ? BN / 2 : BN;
-  A.tiles_n = (A.N + bn - 1) / bn;
+  // 256 x 256 tiles halve the LDS traffic of 128 x 128 ones, and need enough of them
+  const int64_t n = MODE == kGateUp ? 2 * (int64_t)A.N : A.N;
+  const int tile = (int64_t)((A.M + 255) / 256) * ((n + 255) / 256) >= 128 ? 256 : 128;
+  A.tiles_m = (A.M + tile - 1) / tile;
+  A.tiles_n = (int)((n + tile - 1) / tile);
   if (A.tiles_m == 0 || A.tiles_n == 0) return FT_OK;
   const int64_t nb = (int64_t)A.tiles_m * A.tiles_n;
   if (nb > 0x7fffffff) return fail(FT_EINVAL, "gated_ffn: too many tiles");
-  hipLaunchKernelGGL((gemm_kernel<MODE, H, BM, BN, WM, WN>), dim3((unsigned)nb), dim3(64 * WM * WN), 0, s, A);
+  if (tile == 256)
+    hipLaunchKernelGGL((gemm256_kernel<MODE, H>), dim3((unsigned)nb), dim3(512), 0, s, A);
+  else
+    hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)nb), dim3(256), 0, s, A);
   return launched("gemm_kernel");
 }
 
 template <int MODE>
 int gemm_launch(GemmArgs& A, bool half, hipStream_t s) {
-  // 256 x 256 tiles halve the LDS traffic of 128 x 128 ones, and need enough of them
-  const int64_t n = MODE == kGateUp ? 2 * (int64_t)A.N : A.N;
-  const int64_t big = (int64_t)((A.M + 255) / 256) * ((n + 255) / 256);
-  if (big >= 128) {
-    return half ? gemm_go<MODE, true, 256, 256, 2, 4>(A, s) : gemm_go<MODE, false, 256, 256, 2, 4>(A, s);
-  }
-  return half ? gemm_go<MODE, true, 128, 128, 2, 2>(A, s) : gemm_go<MODE, false, 128, 128, 2, 2>(A, s);
+  return half ? gemm_go<MODE, true>(A, s) : gemm_go<MODE, false>(A, s);
 }
 
 template <bool GU, bool H>

@@ -223,10 +223,18 @@ def _ptr(t):
     raise TypeError(f"cannot pass {type(t)} as a pointer")
 
 
+_torch = None
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch's current stream: building the Stream object takes 3 us a call
+        global _torch
+        if _torch is None:
+            import torch
+            torch.cuda.init()
+            _torch = torch
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
