@@ -67,6 +67,9 @@ __device__ __forceinline__ float to_f32(uint16_t v) {
   return lo16<H>(v);
 }
 
+// A buffer without an end of its own: offsets are checked against kOOB alone.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) { return buf_rsrc(p, 0x7fffffffu); }
+
 // ---- activations --------------------------------------------------------------------
 // act(z) and act'(z).  Every value that leaves these is rounded to 16 bits (or 8) after, so
 // exp and the reciprocal are the hardware's (a few ulp of fp32).

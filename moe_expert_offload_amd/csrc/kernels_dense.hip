@@ -91,8 +91,6 @@ struct GemmArgs {
   int tiles_m, tiles_n;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) { return buf_rsrc(p, 0x7fffffffu); }
-
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
 }

@@ -30,13 +30,17 @@ struct Bias16 {
   static constexpr uint32_t mask = 0x000f000fu << sh;
 };
 
-// Codes (0, 4), (1, 5), (2, 6), (3, 7) of a word of 8 as pairs of 16 + code.
+// Codes (0, 4), (1, 5), (2, 6), (3, 7) of a word of 8 as pairs of 16 + code: a shift and an and-or
+// each.  `one` comes in a vector register and `mask` in a scalar one (an instruction reads at
+// most one scalar operand and takes no second constant; written plainly it is an and and an or).
+// Multiplying a byte into place, which keeps the codes in order, is slower: the 24-bit multiply
+// runs at a quarter of the rate (the gate/up product of one token, d = 4096, d_ff = 11008: 24.0
+// against 19.4 us).
 template <bool H>
-__device__ __forceinline__ i32x4_t widen(uint32_t v) {
-  using B = Bias16<H>;
+__device__ __forceinline__ i32x4_t widen(uint32_t v, uint32_t mask, uint32_t one) {
   auto at = [&](int i) -> int {
-    const int s = B::sh - 4 * i;
-    return (int)(((s >= 0 ? v << s : v >> -s) & B::mask) | B::one);
+    const int s = Bias16<H>::sh - 4 * i;
+    return (int)(((s >= 0 ? v << s : v >> -s) & mask) | one);
   };
   return i32x4_t{at(0), at(1), at(2), at(3)};
 }
@@ -47,59 +51,127 @@ __device__ __forceinline__ i32x4_t reorder(i32x4_t x) {
                  (int)__builtin_amdgcn_perm(d, b, 0x05040100u), (int)__builtin_amdgcn_perm(d, b, 0x07060302u)};
 }
 
-template <bool GU, bool H, int G, int NT, int W>
-__global__ __launch_bounds__(64 * W) void w4_kernel(W4Args p) {
-  constexpr int RB = GU ? 8 : 16, NG = 128 / G, PER = 4 / NG, U = NT == 1 ? 2 : 1;
+// Copies `bytes` (more than 0) from memory of any alignment to LDS, 16 at a time: a last short piece is moved
+// back to end with the rest.  Less than one piece goes byte by byte.
+__device__ __forceinline__ void stage_bytes(uint8_t* dst, const uint8_t* src, int bytes) {
+  if (bytes >= 16) {
+    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) {
+      const int at = min(i, bytes - 16);
+      uint4 v;
+      __builtin_memcpy(&v, src + at, 16);
+      __builtin_memcpy(dst + at, &v, 16);
+    }
+  } else if ((int)threadIdx.x < bytes) {
+    dst[threadIdx.x] = src[threadIdx.x];
+  }
+}
+
+// TK: tokens the kernel is made for (1, 4: x in LDS, reordered once; 16, 32, 64 a pass: a chunk's x
+// comes with its codes).  The tile's scales and zeros lie in LDS: loaded chunk by chunk each of these loads
+// touches 16 rows and costs the load unit as much as the codes themselves; so do four loads of x that
+// all rows of tokens share.  SL = false reads them from memory one by one, for K / group too
+// large for LDS.  U chunks of a wave are in flight at once.
+template <bool GU, bool H, int G, int TK, int W, int U, bool SL>
+__global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
+  constexpr bool XL = TK <= 4;
+  constexpr int RB = GU ? 8 : 16, NM = GU ? 2 : 1, NG = 128 / G, PER = 4 / NG, NT = TK < 16 ? 1 : TK / 16;
+  constexpr int NR = TK == 1 ? 1 : 4;  // results of a lane that can belong to a token
   __shared__ float red[W][NT * 16][16];
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.x * RB, t0 = blockIdx.y * (16 * NT);
-  const int KG = p.K / G;
+  const int r0 = blockIdx.x * RB, t0 = blockIdx.y * (16 * NT), nt = min(p.T - t0, 16 * NT);
+  const int KG = p.K / G, KB = p.K >> 1;
+  const int chunks = (p.K + 127) >> 7;
+  const int nr = min(RB, p.N - r0), rl = min(GU ? (n & 7) : n, nr - 1);  // rows of the tile, the lane's
   const bool second = GU && n >= 8;
-  const int64_t row = min(r0 + (GU ? (n & 7) : n), p.N - 1);
-  const uint8_t* cp = (second ? p.codes2 : p.codes) + row * (p.K >> 1);
-  const uint16_t* sp = (second ? p.scales2 : p.scales) + row * KG;
-  const uint8_t* zp = second ? p.zeros2 : p.zeros;
-  const bool hasz = zp != nullptr;
-  zp += row * KG;
-  const uint16_t* xp[NT];
+  const uint8_t* const cp = (second ? p.codes2 : p.codes) + (int64_t)(r0 + rl) * KB + g * 16;
+  const bool hasz = (second ? p.zeros2 : p.zeros) != nullptr;
+  uint32_t mask, one;
+  asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(Bias16<H>::mask));
+  asm("v_mov_b32 %0, %1" : "=v"(one) : "i"(Bias16<H>::one));
+
+  // dynamic LDS: x [TK][K + 8] (XL), then the scales of the rows of each matrix, then their zeros
+  const int xs = (p.K >> 3) + 1;  // row stride of x, pieces of 16 bytes: an odd number of them (K % 32 == 0)
+  uint4* const sx = reinterpret_cast<uint4*>(dyn);
+  uint8_t* const ss = dyn + (XL ? (size_t)min(p.T, TK) * xs * 16 : 0);
+  uint8_t* const sz = ss + 16 * KG * 2;
+
+  auto load = [&](uint4& q, int ci) {
+    const int k0 = min(ci, chunks - 1) << 7;
+    // K % 32 == 0: a lane's 32 codes are there or not as a whole
+    q = *reinterpret_cast<const uint4*>(cp + (k0 + g * 32 < p.K ? k0 >> 1 : -g * 16));
+  };
+
+  uint4 q[U];
+  if constexpr (XL) {
+    const int per = p.K >> 3;
+    i32x4_t v[TK];
+    int c = threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xp[i] = p.x + (int64_t)min(t0 + i * 16 + n, p.T - 1) * p.ldx;
+    for (int t = 0; t < TK; ++t)
+      v[t] = *reinterpret_cast<const i32x4_t*>(p.x + (int64_t)min(t, nt - 1) * p.ldx + min(c, per - 1) * 8);
+    while (true) {
+      if (c < per) {
+#pragma unroll
+        for (int t = 0; t < TK; ++t)
+          if (t < nt) {
+            const i32x4_t r = reorder(v[t]);
+            sx[t * xs + c] = make_uint4(r.x, r.y, r.z, r.w);
+          }
+      }
+      c += 64 * W;
+      if (c - (int)threadIdx.x >= per) break;
+#pragma unroll
+      for (int t = 0; t < TK; ++t)
+        v[t] = *reinterpret_cast<const i32x4_t*>(p.x + (int64_t)min(t, nt - 1) * p.ldx + min(c, per - 1) * 8);
+    }
+  }
+  if constexpr (SL) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const uint8_t* s = reinterpret_cast<const uint8_t*>(m ? p.scales2 : p.scales);
+      const uint8_t* z = m ? p.zeros2 : p.zeros;
+      stage_bytes(ss + m * 8 * KG * 2, s + (int64_t)r0 * KG * 2, nr * KG * 2);
+      if (z) stage_bytes(sz + m * 8 * KG, z + (int64_t)r0 * KG, nr * KG);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(q[u], wave + u * W);
+  const uint8_t* xp[NT];  // rows of x past T repeat the last one; their sums are dropped
+  if constexpr (!XL) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      xp[i] = reinterpret_cast<const uint8_t*>(p.x + (int64_t)(t0 + min(i * 16 + n, nt - 1)) * p.ldx) + g * 16;
+  }
+  const uint4* const xl = sx + min(n, nt - 1) * xs + g;
+  const int lr = (second ? 8 : 0) + rl;
+  const uint16_t* const sp = SL ? reinterpret_cast<const uint16_t*>(ss) + lr * KG
+                                : (second ? p.scales2 : p.scales) + (int64_t)(r0 + rl) * KG;
+  const uint8_t* const zp = SL ? sz + lr * KG : (second ? p.zeros2 : p.zeros) + (int64_t)(r0 + rl) * KG;
   f32x4_t acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{};
-  const int chunks = (p.K + 127) >> 7;
+  if constexpr (XL || SL) __syncthreads();
+
   for (int c0 = wave; c0 < chunks; c0 += W * U) {
-    uint4 q[U];
-    i32x4_t fx[U][4][NT];
-    float sc[U][NG];
-    uint32_t zb[U][NG];
+    i32x4_t x[XL ? 1 : U][4][NT];
+    if constexpr (!XL) {
 #pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int k0 = (c0 + v * W) << 7;
-      const int kc = k0 + g * 32;  // K % 32 == 0
-      q[v] = *reinterpret_cast<const uint4*>(cp + (kc < p.K ? kc >> 1 : 0));
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const int gi = min(k0 / G + j, KG - 1);
-        sc[v][j] = to_f32<H>(sp[gi]);
-        zb[v][j] = hasz ? zp[gi] : 8;
-      }
+        for (int j = 0; j < 4; ++j) {
+          const int k0 = min(c0 + u * W, chunks - 1) << 7, k = k0 + j * 32 < p.K ? k0 + j * 32 : 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + j * 32 + g * 8;
-        const bool ok = k < p.K;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          fx[v][j][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + (ok ? k : 0));
-          if (!ok) fx[v][j][i] = i32x4_t{};
+          for (int i = 0; i < NT; ++i) x[u][j][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k * 2);
         }
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int k0 = (c0 + v * W) << 7;
-      uint32_t w[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
+    for (int u = 0; u < U; ++u) {
+      const int k0 = (c0 + u * W) << 7;
+      if (k0 >= p.K) break;
+      uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
       // word j of row group g to row group j, word g
       auto s32 = [](uint32_t& a, uint32_t& b) {
         const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -117,34 +189,44 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args p) {
       s16(w[2], w[3]);
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        if (k0 + j * G >= p.K) break;
-        const int bw = (int)((zb[v][j] << Bias16<H>::sh) * 0x10001u | Bias16<H>::one | 0x80008000u);
+        if (k0 + j * G >= p.K) break;  // a group is there whole or not at all
+        const float scale = to_f32<H>(sp[k0 / G + j]);
+        const uint32_t zb = hasz ? zp[k0 / G + j] : 8;
+        const int bw = (int)((zb << Bias16<H>::sh) * 0x10001u | Bias16<H>::one | 0x80008000u);
         const i32x4_t bias = {bw, bw, bw, bw};
+        f32x4_t s[NT];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          f32x4_t s = f32x4_t{};
+        for (int e = 0; e < PER; ++e) {
+          const i32x4_t wv = widen<H>(w[j * PER + e], mask, one);
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            const int jj = j * PER + e;
-            const i32x4_t xr = reorder(fx[v][jj][i]);
-            s = mfma16<H>(xr, widen<H>(w[jj]), s);
-            s = mfma16<H>(xr, bias, s);
+          for (int i = 0; i < NT; ++i) {
+            const i32x4_t xr = XL ? *reinterpret_cast<const i32x4_t*>(xl + (k0 >> 3) + (j * PER + e) * 4)
+                                  : reorder(x[XL ? 0 : u][j * PER + e][i]);
+            s[i] = mfma16<H>(xr, wv, e ? s[i] : f32x4_t{});
+            s[i] = mfma16<H>(xr, bias, s[i]);
           }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(sc[v][j], s[r], acc[i][r]);
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(scale, s[i][r], acc[i][r]);
       }
+    }
+    if (c0 + W * U < chunks) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(q[u], c0 + (U + u) * W);
     }
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][i * 16 + g * 4 + r][n] = acc[i][r];
+    for (int r = 0; r < NR; ++r) red[wave][i * 16 + g * 4 + r][n] = acc[i][r];
   __syncthreads();
-  for (int e = threadIdx.x; e < NT * 16 * RB; e += 64 * W) {
+  for (int e = threadIdx.x; e < nt * RB; e += 64 * W) {
     const int t = e / RB, c = e % RB;
-    const int tt = t0 + t, nn = r0 + c;
-    if (tt >= p.T || nn >= p.N) continue;
+    const int nn = r0 + c;
+    if (c >= nr) continue;
+    const int64_t tt = t0 + t;
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) s += red[w][t][c];
@@ -152,13 +234,13 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args p) {
       float u = 0.0f;
 #pragma unroll
       for (int w = 0; w < W; ++w) u += red[w][t][c + 8];
-      p.h[(int64_t)tt * p.N + nn] = (uint16_t)pack2<H>(act_f(s, p.act) * u, 0.0f);
+      p.h[tt * p.N + nn] = (uint16_t)pack2<H>(act_f(s, p.act) * u, 0.0f);
     } else if (p.y_f32) {
-      if (p.res) s += static_cast<const float*>(p.res)[(int64_t)tt * p.ldr + nn];
-      static_cast<float*>(p.y)[(int64_t)tt * p.ldy + nn] = s;
+      if (p.res) s += static_cast<const float*>(p.res)[tt * p.ldr + nn];
+      static_cast<float*>(p.y)[tt * p.ldy + nn] = s;
     } else {
-      if (p.res) s += to_f32<H>(static_cast<const uint16_t*>(p.res)[(int64_t)tt * p.ldr + nn]);
-      static_cast<uint16_t*>(p.y)[(int64_t)tt * p.ldy + nn] = (uint16_t)pack2<H>(s, 0.0f);
+      if (p.res) s += to_f32<H>(static_cast<const uint16_t*>(p.res)[tt * p.ldr + nn]);
+      static_cast<uint16_t*>(p.y)[tt * p.ldy + nn] = (uint16_t)pack2<H>(s, 0.0f);
     }
   }
 }
@@ -166,13 +248,21 @@ __global__ __launch_bounds__(64 * W) void w4_kernel(W4Args p) {
 template <bool GU, bool H, int G>
 int w4_go(const W4Args& A, hipStream_t s) {
   constexpr int RB = GU ? 8 : 16;
-  const unsigned nb = (unsigned)(((int64_t)A.N + RB - 1) / RB);
-  if (A.T <= 16)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 1, 8>), dim3(nb, 1), dim3(512), 0, s, A);
+  const unsigned tiles = (unsigned)(((int64_t)A.N + RB - 1) / RB), passes = (unsigned)((A.T + 63) / 64);
+  const size_t sl = 16 * (size_t)(A.K / G) * 3;                                            // scales and zeros
+  const size_t xl = (size_t)(A.T < 4 ? A.T : 4) * (2 * (size_t)A.K + 16), most = 128 << 10;  // 32 KB for the waves' parts
+  if (sl > most)
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 64, 8, 1, false>), dim3(tiles, passes), dim3(512), 0, s, A);
+  else if (A.T == 1 && sl + xl <= most)
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 1, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
+  else if (A.T <= 4 && sl + xl <= most)
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 4, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
+  else if (A.T <= 16)
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 16, 8, 4, true>), dim3(tiles), dim3(512), sl, s, A);
   else if (A.T <= 32)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 2, 8>), dim3(nb, 1), dim3(512), 0, s, A);
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 32, 8, 2, true>), dim3(tiles), dim3(512), sl, s, A);
   else
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 4, 8>), dim3(nb, (unsigned)((A.T + 63) / 64)), dim3(512), 0, s, A);
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 64, 8, 1, true>), dim3(tiles, passes), dim3(512), sl, s, A);
   return launched("w4_kernel");
 }
 template <bool GU, bool H>

@@ -375,6 +375,11 @@ W4 = [
     (33, 640, 19, 128, False, "fp16", "fp32", False),
     (64, 224, 48, 32, True, "fp16", "fp16", False),
     (131, 256, 35, 64, True, "bf16", "fp32", True),     # three passes over the tokens
+    (2, 96, 16500, 32, True, "bf16", "fp32", False),    # a block walks over several tiles of rows
+    (1, 1152, 20011, 128, False, "fp16", "fp32", True),
+    (40, 160, 9000, 32, True, "bf16", "fp32", False),
+    (16, 4096, 64, 32, True, "bf16", "fp32", False),    # the most of x that LDS holds
+    (11, 8224, 24, 32, False, "fp16", "fp32", False),   # more than that
 ]
 
 
@@ -421,6 +426,7 @@ def test_w4_every_code():
     (16, 192, 64, (64, 32), True, "bf16", "silu", True),
     (40, 128, 320, (32, 64), False, "bf16", "silu", False),
     (70, 64, 96, (64, 32), True, "fp16", "silu", True),
+    (1, 64, 8224, (32, 32), True, "bf16", "silu", False),
 ])
 def test_w4_gated_ffn(T, d, f, groups, zero, t, kind, res):
     torch = torch_mod()
