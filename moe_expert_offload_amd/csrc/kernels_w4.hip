@@ -66,14 +66,14 @@ __device__ __forceinline__ void stage_bytes(uint8_t* dst, const uint8_t* src, in
   }
 }
 
-// TK: tokens the kernel is made for (1, 4: x in LDS, reordered once; 16, 32, 64 a pass: a chunk's x
+// TK: tokens the kernel is made for (1, 4, 8: x in LDS, reordered once; 16, 32, 64 a pass: a chunk's x
 // comes with its codes).  The tile's scales and zeros lie in LDS: loaded chunk by chunk each of these loads
 // touches 16 rows and costs the load unit as much as the codes themselves; so do four loads of x that
 // all rows of tokens share.  SL = false reads them from memory one by one, for K / group too
 // large for LDS.  U chunks of a wave are in flight at once.
 template <bool GU, bool H, int G, int TK, int W, int U, bool SL>
 __global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
-  constexpr bool XL = TK <= 4;
+  constexpr bool XL = TK <= 8;
   constexpr int RB = GU ? 8 : 16, NM = GU ? 2 : 1, NG = 128 / G, PER = 4 / NG, NT = TK < 16 ? 1 : TK / 16;
   constexpr int NR = TK == 1 ? 1 : 4;  // results of a lane that can belong to a token
   __shared__ float red[W][NT * 16][16];
@@ -154,69 +154,75 @@ __global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
   for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{};
   if constexpr (XL || SL) __syncthreads();
 
-  for (int c0 = wave; c0 < chunks; c0 += W * U) {
-    i32x4_t x[XL ? 1 : U][4][NT];
+  auto use = [&](const uint4& qu, const i32x4_t (&xu)[XL ? 1 : 4][NT], int k0) {
+    uint32_t w[4] = {qu.x, qu.y, qu.z, qu.w};
+    // word j of row group g to row group j, word g
+    auto s32 = [](uint32_t& a, uint32_t& b) {
+      const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+      a = r.x;
+      b = r.y;
+    };
+    auto s16 = [](uint32_t& a, uint32_t& b) {
+      const u32x2_t r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+      a = r.x;
+      b = r.y;
+    };
+    s32(w[0], w[2]);
+    s32(w[1], w[3]);
+    s16(w[0], w[1]);
+    s16(w[2], w[3]);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      if (k0 + j * G >= p.K) break;  // a group is there whole or not at all
+      const float scale = to_f32<H>(sp[k0 / G + j]);
+      const uint32_t zb = hasz ? zp[k0 / G + j] : 8;
+      const int bw = (int)((zb << Bias16<H>::sh) * 0x10001u | Bias16<H>::one | 0x80008000u);
+      const i32x4_t bias = {bw, bw, bw, bw};
+      f32x4_t s[NT];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const i32x4_t wv = widen<H>(w[j * PER + e], mask, one);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const i32x4_t xr = XL ? *reinterpret_cast<const i32x4_t*>(xl + (k0 >> 3) + (j * PER + e) * 4)
+                                : reorder(xu[XL ? 0 : j * PER + e][i]);
+          s[i] = mfma16<H>(xr, wv, e ? s[i] : f32x4_t{});
+          s[i] = mfma16<H>(xr, bias, s[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(scale, s[i][r], acc[i][r]);
+    }
+  };
+  i32x4_t x[U][XL ? 1 : 4][NT];
+  auto load_x = [&](i32x4_t (&xu)[XL ? 1 : 4][NT], int ci) {
     if constexpr (!XL) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int j = 0; j < 4; ++j) {
+        const int k0 = min(ci, chunks - 1) << 7, k = k0 + j * 32 < p.K ? k0 + j * 32 : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k0 = min(c0 + u * W, chunks - 1) << 7, k = k0 + j * 32 < p.K ? k0 + j * 32 : 0;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) x[u][j][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k * 2);
-        }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k0 = (c0 + u * W) << 7;
-      if (k0 >= p.K) break;
-      uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-      // word j of row group g to row group j, word g
-      auto s32 = [](uint32_t& a, uint32_t& b) {
-        const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-        a = r.x;
-        b = r.y;
-      };
-      auto s16 = [](uint32_t& a, uint32_t& b) {
-        const u32x2_t r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-        a = r.x;
-        b = r.y;
-      };
-      s32(w[0], w[2]);
-      s32(w[1], w[3]);
-      s16(w[0], w[1]);
-      s16(w[2], w[3]);
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        if (k0 + j * G >= p.K) break;  // a group is there whole or not at all
-        const float scale = to_f32<H>(sp[k0 / G + j]);
-        const uint32_t zb = hasz ? zp[k0 / G + j] : 8;
-        const int bw = (int)((zb << Bias16<H>::sh) * 0x10001u | Bias16<H>::one | 0x80008000u);
-        const i32x4_t bias = {bw, bw, bw, bw};
-        f32x4_t s[NT];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const i32x4_t wv = widen<H>(w[j * PER + e], mask, one);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const i32x4_t xr = XL ? *reinterpret_cast<const i32x4_t*>(xl + (k0 >> 3) + (j * PER + e) * 4)
-                                  : reorder(x[XL ? 0 : u][j * PER + e][i]);
-            s[i] = mfma16<H>(xr, wv, e ? s[i] : f32x4_t{});
-            s[i] = mfma16<H>(xr, bias, s[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(scale, s[i][r], acc[i][r]);
+        for (int i = 0; i < NT; ++i) xu[j][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k * 2);
       }
     }
-    if (c0 + W * U < chunks) {
+  };
 #pragma unroll
-      for (int u = 0; u < U; ++u) load(q[u], c0 + (U + u) * W);
+  for (int u = 0; u < U; ++u) load_x(x[u], wave + u * W);
+  __builtin_amdgcn_sched_barrier(0);
+  int c0 = wave;
+  for (; c0 + W * U < chunks; c0 += W * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      use(q[u], x[u], (c0 + u * W) << 7);  // all before the last chunk
+      load(q[u], c0 + (U + u) * W);
+      load_x(x[u], c0 + (U + u) * W);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * W < chunks) use(q[u], x[u], (c0 + u * W) << 7);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -250,13 +256,15 @@ int w4_go(const W4Args& A, hipStream_t s) {
   constexpr int RB = GU ? 8 : 16;
   const unsigned tiles = (unsigned)(((int64_t)A.N + RB - 1) / RB), passes = (unsigned)((A.T + 63) / 64);
   const size_t sl = 16 * (size_t)(A.K / G) * 3;                                            // scales and zeros
-  const size_t xl = (size_t)(A.T < 4 ? A.T : 4) * (2 * (size_t)A.K + 16), most = 128 << 10;  // 32 KB for the waves' parts
+  const size_t xl = (size_t)(A.T < 8 ? A.T : 8) * (2 * (size_t)A.K + 16), most = 128 << 10;  // 32 KB for the waves' parts
   if (sl > most)
     hipLaunchKernelGGL((w4_kernel<GU, H, G, 64, 8, 1, false>), dim3(tiles, passes), dim3(512), 0, s, A);
   else if (A.T == 1 && sl + xl <= most)
     hipLaunchKernelGGL((w4_kernel<GU, H, G, 1, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
   else if (A.T <= 4 && sl + xl <= most)
     hipLaunchKernelGGL((w4_kernel<GU, H, G, 4, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
+  else if (A.T <= 8 && sl + xl <= most)
+    hipLaunchKernelGGL((w4_kernel<GU, H, G, 8, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
   else if (A.T <= 16)
     hipLaunchKernelGGL((w4_kernel<GU, H, G, 16, 8, 4, true>), dim3(tiles), dim3(512), sl, s, A);
   else if (A.T <= 32)
