@@ -80,7 +80,7 @@ extern "C" {
 
 size_t ft_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t d_ff) {
   if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8)) return 0;
-  return align256((size_t)T * d_ff * 2) + 256;
+  return align256((size_t)T * d_ff * 2) + ft::gated_ffn_part_bytes(T, d, d_ff, false) + 256;
 }
 
 size_t ft_gated_ffn_saved_bytes(int32_t T, int32_t d_ff, int32_t save_fmt) {
@@ -120,6 +120,7 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
   F.save_fmt = save_fmt;
   lay_saved(F, saved);
   F.h = static_cast<uint16_t*>(workspace);
+  F.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)T * d_ff * 2));
   return ft::launch_gated_ffn(F, stream);
 }
 
@@ -128,7 +129,7 @@ size_t ft_gated_ffn_bwd_workspace_bytes(int32_t T, int32_t d, int32_t d_ff, int3
   size_t n = align256((size_t)T * d_ff * 2) + align256((size_t)T * d_ff * 4);  // h; da and du
   if (save_fmt == FT_SAVE_NONE) n += align256((size_t)T * d_ff * 4);           // a and u
   if (x_mx8) n += align256((size_t)T * d * 2);                                 // x
-  return n + 256;
+  return n + ft::gated_ffn_part_bytes(T, d, d_ff, true) + 256;
 }
 
 int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_t T, int32_t d, int32_t d_ff,
@@ -188,6 +189,7 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
     F.x = x16;
     F.ldx = d;
   }
+  F.part = reinterpret_cast<float*>(ws);
   if (save_fmt == FT_SAVE_NONE && T > 0) {
     ft::DenseFfn P = F;  // a and u alone
     P.h = nullptr;

@@ -4,6 +4,8 @@
 //   a = x Wg^T, u = x Wu^T, h = act(a) * u, y = h Wd^T (+ residual)
 //   dh = dy Wd, du = dh act(a), da = dh u act'(a)
 //   dWd = dy^T h, dWg = da^T x, dWu = du^T x, dx = da Wg + du Wu
+#include <type_traits>
+
 #include "dense_common.h"
 
 namespace ft {
@@ -74,6 +76,8 @@ enum {
   kDw       // A and B transposed; rows of C from `split` on go to a second matrix
 };
 
+constexpr int kUnits = 256;  // compute units
+
 struct GemmArgs {
   const uint16_t *a, *b, *b2;  // b2: Wu (kGateUp: beside b; kDx: second piece of k)
   int64_t lda, ldb;
@@ -89,7 +93,21 @@ struct GemmArgs {
   uint8_t *sca, *scu;  // MX8 scales, null for 16-bit a and u
   uint16_t *h, *dag;   // kDh outputs: h [M, N], da and du [M, 2N]
   int tiles_m, tiles_n;
+  // gemm256_kernel: the first `whole` tiles have a block each; the other `rest` tiles' stages are one
+  // line that `parts` blocks share in pieces of `per` (rest = 0: none)
+  int whole, rest, parts, per;
+  float* part;  // sums of pieces
 };
+
+// Tile index to its place: consecutive tiles walk 8 tile rows per column of tiles.
+struct TilePos {
+  int m, n;
+};
+__device__ __forceinline__ TilePos tile_pos(const GemmArgs& p, int t) {
+  const int per = 8 * p.tiles_n, grp = t / per, first = grp * 8;
+  const int rows = min(8, p.tiles_m - first), in = t - grp * per;
+  return {first + in % rows, in / rows};
+}
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
@@ -296,11 +314,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  // consecutive blocks share an XCD; they walk 8 tile rows per column of tiles
-  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
-  const int per = 8 * p.tiles_n, grp = lb / per, first = grp * 8;
-  const int rows = min(8, p.tiles_m - first), in = lb - grp * per;
-  const int m0 = (first + in % rows) * BM, n0 = (in / rows) * (MODE == kGateUp ? BN / 2 : BN);
+  // consecutive blocks share an XCD
+  const TilePos tp = tile_pos(p, xcd_logical_block(blockIdx.x, gridDim.x));
+  const int m0 = tp.m * BM, n0 = tp.n * (MODE == kGateUp ? BN / 2 : BN);
 
   // ---- loads: per-lane byte offsets within the tile, from a base that moves with k ----
   uint32_t offA[LA], offB[LB];
@@ -446,6 +462,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 // second did (both end a read section with their reads done), and is waited for, by both groups, at least one
 // barrier before its first read; between the two lie 1.5 stages or more.  Loads past the last stage are
 // masked (they write zeros nobody reads), which keeps the counts of the waits.
+// Where the 32x32 result (i, j) of a wave lies in a piece's sums, in float4: 4 quads of 64 lanes each.
+constexpr int kPartFloats = 256 * 256;
+__device__ __forceinline__ size_t part_at(int slot, int wave, int i, int j) {
+  return (size_t)slot * (kPartFloats / 4) + (((wave * 4 + i) * 2 + j) * 4) * 64;
+}
+
 template <int MODE, bool H>
 __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
   constexpr bool AT = MODE == kDw;
@@ -457,167 +479,250 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
 
-  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
-  const int per = 8 * p.tiles_n, grp = lb / per, first = grp * 8;
-  const int rows = min(8, p.tiles_m - first), in = lb - grp * per;
-  const int m0 = (first + in % rows) * 256, n0 = (in / rows) * (MODE == kGateUp ? 128 : 256);
-
-  // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
-  uint32_t offA[2][2], offB[2][2];  // [half][chunk]
-  int kA[2], kB[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int c = wave * 2 + j;
-    const int r = c * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);       // along k
-    const int kt = c * 4 + (lane >> 4), pt = (lane & 15) ^ ((lane >> 4) << 2);  // transposed
-    kA[j] = AT ? kt : pk * 8;
-    kB[j] = BT ? kt : pk * 8;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (AT)
-        offA[h][j] = m0 + h * 128 + pt * 8 < p.M ? (uint32_t)(kt * p.lda * 2 + pt * 16) : kOOB;
-      else
-        offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda * 2 + pk * 16) : kOOB;
-      const int nh = n0 + (MODE == kGateUp ? 0 : h * 128);
-      if constexpr (BT)
-        offB[h][j] = nh + pt * 8 < p.N ? (uint32_t)(kt * p.ldb * 2 + pt * 16) : kOOB;
-      else
-        offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.ldb * 2 + pk * 16) : kOOB;
-    }
-  }
+  const int hi = lane >> 5, l31 = lane & 31, kk = (lane >> 2) & 3;
   const int per_seg = (p.K + 63) >> 6;
   const int stages = MODE == kDx ? 2 * per_seg : per_seg;
-  const uint32_t sm0 = lds_addr(sm) + wave * 2048;
 
-  auto load_a = [&](int s, int h) {
-    int k0 = s << 6;
-    const uint16_t* pa = p.a;
-    if (MODE == kDx && s >= per_seg) {
-      k0 = (s - per_seg) << 6;
-      pa = p.a + p.K;
-    }
-    const int left = p.K - k0;
-    const auto rs = rsrc_of(AT ? pa + k0 * p.lda + m0 + h * 128 : pa + (int64_t)(m0 + h * 128) * p.lda + k0);
-    const uint32_t dst = sm0 + (s & 1) * STAGE + (h ? A1 : A0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) lds_load16(rs, kA[j] < left ? offA[h][j] : kOOB, 0, dst + j * 1024);
-  };
-  auto load_b = [&](int s, int h) {
-    int k0 = s << 6;
-    const uint16_t* pb = p.b;
-    if (MODE == kDx && s >= per_seg) {
-      k0 = (s - per_seg) << 6;
-      pb = p.b2;
-    }
-    int nh = n0 + h * 128;
-    if (MODE == kGateUp) {
-      nh = n0;
-      pb = h ? p.b2 : p.b;
-    }
-    const int left = p.K - k0;
-    const auto rs = rsrc_of(BT ? pb + k0 * p.ldb + nh : pb + (int64_t)nh * p.ldb + k0);
-    const uint32_t dst = sm0 + (s & 1) * STAGE + (h ? B1 : B0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) lds_load16(rs, kB[j] < left ? offB[h][j] : kOOB, 0, dst + j * 1024);
-  };
-
-  // ---- fragments of a region: 32 rows (or columns) from `row`, slice of 16 k ----
-  const int hi = lane >> 5, l31 = lane & 31, kk = (lane >> 2) & 3;
-  auto frag_k = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
-    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
-  };
-  auto frag_t = [&](const uint8_t* base, int col, int slice) -> i32x4_t {
-    const int pc = ((col >> 3) ^ (kk << 2)) + ((lane >> 3) & 2) + ((lane >> 1) & 1);
-    const uint8_t* q = base + (16 * slice + 8 * hi + kk) * 256 + pc * 16 + (lane & 1) * 8;
-    typedef __attribute__((address_space(3))) s16x4_t* lp;
-    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)q));
-    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(q + 1024)));
-    return i32x4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
-  };
-
-  f32x16_t acc[4][2];  // [2 half + 32-row piece][half of the columns]
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
-  i32x4_t fa[2][4], fb0[4], fb1[4];
-
-  auto read_a = [&](const uint8_t* base) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        fa[i][k] = AT ? frag_t(base, wm * 64 + i * 32, k) : frag_k(base, wm * 64 + i * 32, k);
-  };
-  auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = BT ? frag_t(base, wn * 32, k) : frag_k(base, wn * 32, k);
-  };
-  auto multiply = [&](int half, int col, const i32x4_t (&f)[4]) {
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) acc[2 * half + i][col] = mfma32<H>(f[k], fa[i][k], acc[2 * half + i][col]);
-    __builtin_amdgcn_s_setprio(0);
-  };
-  // The end of a section: nothing moves across.
-  auto meet = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-
-  if (stages > 0) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      load_a(s, 0);
-      load_b(s, 0);
-      load_b(s, 1);
-      load_a(s, 1);
-    }
-    asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of stage 0
-    meet();
-    if (wm) meet();
-    for (int s = 0; s < stages; ++s) {
-      const uint8_t* st = sm + (s & 1) * STAGE;
-      read_a(st + A0);
-      read_b(st + B0, fb0);
-      reads_done();
-      meet();
-      multiply(0, 0, fb0);
-      meet();
-      read_b(st + B1, fb1);
-      load_a(s + 2, 0);
-      load_b(s + 2, 0);
-      reads_done();
-      asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // A1 of this stage
-      meet();
-      multiply(0, 1, fb1);
-      meet();
-      read_a(st + A1);
-      load_b(s + 2, 1);
-      reads_done();
-      meet();
-      multiply(1, 1, fb1);
-      meet();
-      load_a(s + 2, 1);
-      asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the next stage
-      meet();
-      multiply(1, 0, fb0);
-      meet();
-    }
-    if (!wm) meet();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the masked loads' writes too
+  // This block's piece of work: a whole tile, or stages [at, end) of the line of the rest, which
+  // touch at most two tiles (per < stages).
+  int tile, at = 0, end = stages;
+  const bool piece = (int)blockIdx.x >= p.whole;
+  if (!piece) {
+    tile = xcd_logical_block(blockIdx.x, p.whole);
+  } else {
+    const int b = xcd_logical_block(blockIdx.x - p.whole, p.parts);
+    at = b * p.per;
+    end = min(at + p.per, p.rest * stages);
+    tile = p.whole;
   }
+  do {
+    int s_begin = 0, s_end = stages, slot = -1;
+    if (piece) {
+      const int t = at / stages;
+      tile = p.whole + t;
+      s_begin = at - t * stages;
+      s_end = min(stages, end - t * stages);
+      if (s_end - s_begin < stages) slot = at / p.per + t;
+      at = t * stages + s_end;
+    }
+    const TilePos tp = tile_pos(p, tile);
+    const int m0 = tp.m * 256, n0 = tp.n * (MODE == kGateUp ? 128 : 256);
+    // rows of a wave in the two halves: those past the end are neither read nor multiplied
+    const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
+
+    // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
+    uint32_t offA[2][2], offB[2][2];  // [half][chunk]
+    int kA[2], kB[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = wave * 2 + j;
+      const int r = c * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);        // along k
+      const int kt = c * 4 + (lane >> 4), pt = (lane & 15) ^ ((lane >> 4) << 2);  // transposed
+      kA[j] = AT ? kt : pk * 8;
+      kB[j] = BT ? kt : pk * 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (AT)
+          offA[h][j] = m0 + h * 128 + pt * 8 < p.M ? (uint32_t)(kt * p.lda * 2 + pt * 16) : kOOB;
+        else
+          offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda * 2 + pk * 16) : kOOB;
+        const int nh = n0 + (MODE == kGateUp ? 0 : h * 128);
+        if constexpr (BT)
+          offB[h][j] = nh + pt * 8 < p.N ? (uint32_t)(kt * p.ldb * 2 + pt * 16) : kOOB;
+        else
+          offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.ldb * 2 + pk * 16) : kOOB;
+      }
+    }
+    // Each region's source moves on by a stage per load.
+    const uint32_t sm0 = lds_addr(sm) + wave * 2048;
+    const int64_t step_a = AT ? p.lda * 128 : 128, step_b = BT ? p.ldb * 128 : 128;  // bytes
+    auto first_a = [&](int h) -> const uint8_t* {
+      const bool two = MODE == kDx && s_begin >= per_seg;
+      const int k0 = (s_begin - (two ? per_seg : 0)) << 6, m = m0 + h * 128;
+      const uint16_t* a = p.a + (two ? p.K : 0);
+      return reinterpret_cast<const uint8_t*>(AT ? a + k0 * p.lda + m : a + m * p.lda + k0);
+    };
+    auto first_b = [&](int h) -> const uint8_t* {
+      const bool two = MODE == kDx && s_begin >= per_seg;
+      const int k0 = (s_begin - (two ? per_seg : 0)) << 6, n = n0 + (MODE == kGateUp ? 0 : h * 128);
+      const uint16_t* b = two || (MODE == kGateUp && h) ? p.b2 : p.b;
+      return reinterpret_cast<const uint8_t*>(BT ? b + k0 * p.ldb + n : b + n * p.ldb + k0);
+    };
+    const uint8_t *pa[2] = {first_a(0), first_a(1)}, *pb[2] = {first_b(0), first_b(1)};
+    auto k_left = [&](int s) {
+      if (s >= s_end) return 0;
+      return p.K - ((MODE == kDx && s >= per_seg ? s - per_seg : s) << 6);
+    };
+    auto load_a = [&](int s, int h) {
+      if (MODE == kDx && s == per_seg && s != s_begin)
+        pa[h] = reinterpret_cast<const uint8_t*>(p.a + p.K + (m0 + h * 128) * p.lda);
+      const int left = k_left(s);
+      const auto rs = rsrc_of(pa[h]);
+      const uint32_t dst = sm0 + ((s - s_begin) & 1) * STAGE + (h ? A1 : A0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lds_load16(rs, kA[j] < left ? offA[h][j] : kOOB, 0, dst + j * 1024);
+      pa[h] += step_a;
+    };
+    auto load_b = [&](int s, int h) {
+      if (MODE == kDx && s == per_seg && s != s_begin) pb[h] = reinterpret_cast<const uint8_t*>(p.b2 + n0 + h * 128);
+      const int left = k_left(s);
+      const auto rs = rsrc_of(pb[h]);
+      const uint32_t dst = sm0 + ((s - s_begin) & 1) * STAGE + (h ? B1 : B0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lds_load16(rs, kB[j] < left ? offB[h][j] : kOOB, 0, dst + j * 1024);
+      pb[h] += step_b;
+    };
+
+    // ---- fragments of a region: 32 rows (or columns) from `row`, slice of 16 k ----
+    auto frag_k = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
+      return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
+    };
+    auto frag_t = [&](const uint8_t* base, int col, int slice) -> i32x4_t {
+      const int pc = ((col >> 3) ^ (kk << 2)) + ((lane >> 3) & 2) + ((lane >> 1) & 1);
+      const uint8_t* q = base + (16 * slice + 8 * hi + kk) * 256 + pc * 16 + (lane & 1) * 8;
+      typedef __attribute__((address_space(3))) s16x4_t* lp;
+      const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)q));
+      const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(q + 1024)));
+      return i32x4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
+    };
+
+    f32x16_t acc[4][2];  // [2 half + 32-row piece][half of the columns]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
+    i32x4_t fa[2][4], fb0[4], fb1[4];
+
+    auto read_a = [&](const uint8_t* base) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          fa[i][k] = AT ? frag_t(base, wm * 64 + i * 32, k) : frag_k(base, wm * 64 + i * 32, k);
+    };
+    auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = BT ? frag_t(base, wn * 32, k) : frag_k(base, wn * 32, k);
+    };
+    auto multiply = [&](int half, int col, const i32x4_t (&f)[4]) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[2 * half + i][col] = mfma32<H>(f[k], fa[i][k], acc[2 * half + i][col]);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    // The end of a section: nothing moves across.
+    auto meet = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+
+    if (s_begin < s_end) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        load_a(s_begin + s, 0);
+        load_b(s_begin + s, 0);
+        load_b(s_begin + s, 1);
+        load_a(s_begin + s, 1);
+      }
+      asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the first stage
+      meet();
+      if (wm) meet();
+      // RAGGED: the tile has rows past the end.  Asking at every step would cost a whole tile 4 %.
+      auto walk = [&](auto ragged) {
+        constexpr bool RAGGED = decltype(ragged)::value;
+        for (int s = s_begin; s < s_end; ++s) {
+          const uint8_t* st = sm + ((s - s_begin) & 1) * STAGE;
+          if (!RAGGED || any[0]) read_a(st + A0);
+          read_b(st + B0, fb0);
+          reads_done();
+          meet();
+          if (!RAGGED || any[0]) multiply(0, 0, fb0);
+          meet();
+          read_b(st + B1, fb1);
+          load_a(s + 2, 0);
+          load_b(s + 2, 0);
+          reads_done();
+          asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // A1 of this stage
+          meet();
+          if (!RAGGED || any[0]) multiply(0, 1, fb1);
+          meet();
+          if (!RAGGED || any[1]) read_a(st + A1);
+          load_b(s + 2, 1);
+          reads_done();
+          meet();
+          if (!RAGGED || any[1]) multiply(1, 1, fb1);
+          meet();
+          load_a(s + 2, 1);
+          asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the next stage
+          meet();
+          if (!RAGGED || any[1]) multiply(1, 0, fb0);
+          meet();
+        }
+      };
+      if (m0 + 192 < p.M)
+        walk(std::false_type{});
+      else
+        walk(std::true_type{});
+      if (!wm) meet();
+      // the masked loads' writes too: a wave's next loads go where its own last ones went
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + l31;
-    const int nb = n0 + wn * 32;
-    epilogue<MODE, H>(p, acc[i][0], acc[i][1], m, nb, nb + 128, hi);
+    for (int i = 0; i < 4; ++i) {
+      if (slot >= 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float4* d = reinterpret_cast<float4*>(p.part) + part_at(slot, wave, i, j) + lane;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            d[q * 64] = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        }
+      } else {
+        const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + l31;
+        const int nb = n0 + wn * 32;
+        epilogue<MODE, H>(p, acc[i][0], acc[i][1], m, nb, nb + 128, hi);
+      }
+    }
+  } while (piece && at < end);
+}
+
+// The tiles whose stages several blocks shared: their sums, always added in the order of k, then the
+// epilogue.  A block per tile and 32-row piece of the waves; bound by memory (256 KB a part and tile).
+template <int MODE, bool H>
+__global__ __launch_bounds__(512) void gemm256_join_kernel(GemmArgs p) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x & 3, t = blockIdx.x >> 2;
+  const int stages = (MODE == kDx ? 2 : 1) * ((p.K + 63) >> 6);
+  const int first = t * stages / p.per, last = ((t + 1) * stages - 1) / p.per;
+  if (first == last) return;  // one block had it all
+  const TilePos tp = tile_pos(p, p.whole + t);
+  const int m = tp.m * 256 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+  if (m >= p.M) return;
+  f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
+  for (int b = first; b <= last; ++b) {
+    float4 v[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[j][q] = (reinterpret_cast<const float4*>(p.part) + part_at(b + t, wave, i, j) + lane)[q * 64];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[j][4 * q] += v[j][q].x;
+        acc[j][4 * q + 1] += v[j][q].y;
+        acc[j][4 * q + 2] += v[j][q].z;
+        acc[j][4 * q + 3] += v[j][q].w;
+      }
   }
+  const int nb = tp.n * (MODE == kGateUp ? 128 : 256) + wn * 32;
+  epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 128, lane >> 5);
 }
 
 // ---- few rows: the weights stream once ------------------------------------------------
@@ -757,20 +862,57 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
 
 // ---- launches -------------------------------------------------------------------------
 
+// How a product is cut.  `n` columns count gate and up apart.
+struct Cut {
+  int tile;  // 256 or 128
+  int tiles_m, tiles_n, whole, rest, parts, per;
+  size_t part_bytes;
+};
+Cut cut_of(int64_t M, int64_t n, int stages) {
+  Cut c{};
+  const int64_t t256 = ((M + 255) / 256) * ((n + 255) / 256);
+  c.tile = t256 >= 128 || (t256 >= 16 && t256 * stages >= 2048) ? 256 : 128;
+  c.tiles_m = (int)((M + c.tile - 1) / c.tile);
+  c.tiles_n = (int)((n + c.tile - 1) / c.tile);
+  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
+  c.whole = (int)tiles;
+  if (c.tile == 256) {
+    const int rest = (int)(tiles % kUnits);
+    // shared only where it saves more stages than writing and reading the sums again takes
+    if (rest && (kUnits - rest) * (int64_t)stages >= 24 * (int64_t)kUnits) {
+      int parts = kUnits;
+      if ((int64_t)rest * stages < 8 * (int64_t)parts) parts = (int)((int64_t)rest * stages / 8);
+      const int per = (int)(((int64_t)rest * stages + parts - 1) / parts);
+      if (per < stages) {
+        c.rest = rest;
+        c.whole = (int)tiles - rest;
+        c.per = per;
+        c.parts = (int)(((int64_t)rest * stages + per - 1) / per);
+        c.part_bytes = (size_t)(c.parts + rest) * kPartFloats * 4;
+      }
+    }
+  }
+  return c;
+}
+
 template <int MODE, bool H>
 int gemm_go(GemmArgs& A, hipStream_t s) {
-  // 256 x 256 tiles halve the LDS traffic of 128 x 128 ones, and need enough of them
   const int64_t n = MODE == kGateUp ? 2 * (int64_t)A.N : A.N;
-  const int tile = (int64_t)((A.M + 255) / 256) * ((n + 255) / 256) >= 128 ? 256 : 128;
-  A.tiles_m = (A.M + tile - 1) / tile;
-  A.tiles_n = (int)((n + tile - 1) / tile);
+  const Cut c = cut_of(A.M, n, (MODE == kDx ? 2 : 1) * ((A.K + 63) / 64));
+  A.tiles_m = c.tiles_m;
+  A.tiles_n = c.tiles_n;
+  A.whole = c.whole;
+  A.rest = c.rest;
+  A.parts = c.parts;
+  A.per = c.per;
   if (A.tiles_m == 0 || A.tiles_n == 0) return FT_OK;
-  const int64_t nb = (int64_t)A.tiles_m * A.tiles_n;
-  if (nb > 0x7fffffff) return fail(FT_EINVAL, "gated_ffn: too many tiles");
-  if (tile == 256)
-    hipLaunchKernelGGL((gemm256_kernel<MODE, H>), dim3((unsigned)nb), dim3(512), 0, s, A);
-  else
-    hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)nb), dim3(256), 0, s, A);
+  if ((int64_t)A.tiles_m * A.tiles_n > 0x7ffffff) return fail(FT_EINVAL, "gated_ffn: too many tiles");
+  if (c.tile == 256) {
+    hipLaunchKernelGGL((gemm256_kernel<MODE, H>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((gemm256_join_kernel<MODE, H>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
+  } else {
+    hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)(c.tiles_m * c.tiles_n)), dim3(256), 0, s, A);
+  }
   return launched("gemm_kernel");
 }
 
@@ -796,6 +938,23 @@ int skinny_go(SkinnyArgs& A, hipStream_t s) {
 
 // Rows up to which the weights stream once (skinny_kernel); beyond, tiles.
 constexpr int kSkinnyRows = 64;
+
+// The most that the pieces of the calls below take.
+size_t gated_ffn_part_bytes(int T, int d, int d_ff, bool backward) {
+  auto one = [](int64_t M, int64_t n, int64_t K, int segs) { return cut_of(M, n, (int)(segs * ((K + 63) / 64))).part_bytes; };
+  size_t m = 0;
+  auto up = [&](size_t v) { m = v > m ? v : m; };
+  up(one(T, 2 * (int64_t)d_ff, d, 1));
+  if (!backward) {
+    up(one(T, d, d_ff, 1));
+  } else {
+    up(one(T, d_ff, d, 1));
+    up(one(d, d_ff, T, 1));
+    up(one(2 * (int64_t)d_ff, d, T, 1));
+    up(one(T, d, d_ff, 2));
+  }
+  return m;
+}
 
 int launch_gated_ffn(const DenseFfn& F, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -829,6 +988,7 @@ int launch_gated_ffn(const DenseFfn& F, void* stream) {
     return half ? skinny_go<false, true>(D, s) : skinny_go<false, false>(D, s);
   }
   GemmArgs A{};
+  A.part = F.part;
   A.a = F.x;
   A.lda = F.ldx;
   A.b = F.wg;
@@ -846,6 +1006,7 @@ int launch_gated_ffn(const DenseFfn& F, void* stream) {
   int st = gemm_launch<kGateUp>(A, half, s);
   if (st || !F.y) return st;
   GemmArgs D{};
+  D.part = F.part;
   D.a = F.h;
   D.lda = F.d_ff;
   D.b = F.wd;
@@ -867,6 +1028,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   int st;
   if (F.T > 0) {
     GemmArgs A{};
+  A.part = F.part;
     A.a = G.dy;
     A.lda = G.lddy;
     A.b = F.wd;
@@ -885,6 +1047,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   }
   if (G.dwd) {
     GemmArgs A{};
+  A.part = F.part;
     A.a = G.dy;
     A.lda = G.lddy;
     A.b = F.h;
@@ -897,6 +1060,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
     A.split = F.d;
     if ((st = gemm_launch<kDw>(A, half, s))) return st;
     GemmArgs B{};
+    B.part = F.part;
     B.a = G.dag;
     B.lda = 2 * (int64_t)F.d_ff;
     B.b = F.x;
@@ -912,6 +1076,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   }
   if (G.dx && F.T > 0) {
     GemmArgs A{};
+  A.part = F.part;
     A.a = G.dag;
     A.lda = 2 * (int64_t)F.d_ff;
     A.b = F.wg;
