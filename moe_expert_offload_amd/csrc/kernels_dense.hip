@@ -444,24 +444,20 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 // The same product on 256 x 256 tiles, for results large enough to fill the chip with them.
 // 8 waves, two per SIMD; each computes 64 rows and 32 columns of every 128 x 128 quarter.  A
 // stage of 64 k is four regions of 16 KB (the two halves of A's rows and of B's), two stages
-// in LDS.  A stage is four steps, one per quarter: a read section (fragments from LDS, loads
-// into regions that everyone has read) and a multiply section (8 MFMAs), each closed by a
+// in LDS.  A stage is two steps, one per half of A's rows: a read section (fragments from LDS, loads
+// into regions that everyone has read) and a multiply section (16 MFMAs), each closed by a
 // barrier.  The waves 4..7 run one section behind the waves 0..3, so on every SIMD one
-// wave multiplies while the other reads.  With sections t = 0..7 of a stage for the first
-// group:
-//   t  first group                              second group (one section later)
-//   0  read A0, B0                              -
-//   1  A0 x B0                                  read A0, B0
-//   2  read B1; load A0, B0 of stage s + 2      A0 x B0
-//   3  A0 x B1                                  read B1; load A0, B0 of s + 2
-//   4  read A1; load B1 of s + 2                A0 x B1
-//   5  A1 x B1                                  read A1; load B1 of s + 2
-//   6  load A1 of s + 2; wait for A0, B0, B1 of s + 1
-//   7  A1 x B0                                  load A1 of s + 2; wait
-// A region is loaded again two sections after the first group read it, one after the
-// second did (both end a read section with their reads done), and is waited for, by both groups, at least one
-// barrier before its first read; between the two lie 1.5 stages or more.  Loads past the last stage are
-// masked (they write zeros nobody reads), which keeps the counts of the waits.
+// wave multiplies while the other reads.  Sections t = 0..3 of stage s for the first group (the
+// second does the same one later):
+//   t = 0  read A0, B0, B1 of s; load A1 of s + 1; wait for A1 of s
+//   t = 1  A0 x B0, A0 x B1
+//   t = 2  read A1 of s; load A0, B0, B1 of s + 2; wait for A0, B0, B1 of s + 1
+//   t = 3  A1 x B1, A1 x B0
+// A region is loaded again two sections after the first group read it, one after the second did
+// (both end a read section with their reads done): A1 of s + 1 goes where A1 of s - 1 was read at t = -2
+// and -1.  It is waited for by both groups at least one barrier before its first read, and has six
+// sections to arrive.  Loads past the last stage are masked (they write zeros nobody reads), which keeps
+// the counts of the waits.  (Four steps of a quarter each, with 8 MFMAs a section, took 4 % longer.)
 // Where the 32x32 result (i, j) of a wave lies in a piece's sums, in float4: 4 quads of 64 lanes each.
 constexpr int kPartFloats = 256 * 256;
 __device__ __forceinline__ size_t part_at(int slot, int wave, int i, int j) {
@@ -602,12 +598,15 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) f[k] = BT ? frag_t(base, wn * 32, k) : frag_k(base, wn * 32, k);
     };
-    auto multiply = [&](int half, int col, const i32x4_t (&f)[4]) {
+    auto multiply = [&](int half) {
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) acc[2 * half + i][col] = mfma32<H>(f[k], fa[i][k], acc[2 * half + i][col]);
+        for (int i = 0; i < 2; ++i) acc[2 * half + i][0] = mfma32<H>(fb0[k], fa[i][k], acc[2 * half + i][0]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[2 * half + i][1] = mfma32<H>(fb1[k], fa[i][k], acc[2 * half + i][1]);
+      }
       __builtin_amdgcn_s_setprio(0);
     };
     // The end of a section: nothing moves across.
@@ -621,14 +620,14 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
     auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
 
     if (s_begin < s_end) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        load_a(s_begin + s, 0);
-        load_b(s_begin + s, 0);
-        load_b(s_begin + s, 1);
-        load_a(s_begin + s, 1);
-      }
-      asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the first stage
+      load_a(s_begin, 0);
+      load_b(s_begin, 0);
+      load_b(s_begin, 1);
+      load_a(s_begin, 1);
+      load_a(s_begin + 1, 0);
+      load_b(s_begin + 1, 0);
+      load_b(s_begin + 1, 1);
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the first stage
       meet();
       if (wm) meet();
       // RAGGED: the tile has rows past the end.  Asking at every step would cost a whole tile 4 %.
@@ -638,28 +637,21 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
           const uint8_t* st = sm + ((s - s_begin) & 1) * STAGE;
           if (!RAGGED || any[0]) read_a(st + A0);
           read_b(st + B0, fb0);
-          reads_done();
-          meet();
-          if (!RAGGED || any[0]) multiply(0, 0, fb0);
-          meet();
           read_b(st + B1, fb1);
-          load_a(s + 2, 0);
-          load_b(s + 2, 0);
+          load_a(s + 1, 1);
           reads_done();
-          asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // A1 of this stage
+          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
           meet();
-          if (!RAGGED || any[0]) multiply(0, 1, fb1);
+          if (!RAGGED || any[0]) multiply(0);
           meet();
           if (!RAGGED || any[1]) read_a(st + A1);
+          load_a(s + 2, 0);
+          load_b(s + 2, 0);
           load_b(s + 2, 1);
           reads_done();
+          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
           meet();
-          if (!RAGGED || any[1]) multiply(1, 1, fb1);
-          meet();
-          load_a(s + 2, 1);
-          asm volatile("s_waitcnt vmcnt(10)" ::: "memory");  // A0, B0 and B1 of the next stage
-          meet();
-          if (!RAGGED || any[1]) multiply(1, 0, fb0);
+          if (!RAGGED || any[1]) multiply(1);
           meet();
         }
       };
