@@ -93,9 +93,9 @@ struct GemmArgs {
   uint8_t *sca, *scu;  // MX8 scales, null for 16-bit a and u
   uint16_t *h, *dag;   // kDh outputs: h [M, N], da and du [M, 2N]
   int tiles_m, tiles_n;
-  // gemm256_kernel: the first `whole` tiles have a block each; the other `rest` tiles' stages are one
-  // line that `parts` blocks share in pieces of `per` (rest = 0: none)
-  int whole, rest, parts, per;
+  // gemm256_kernel: the first `whole` tiles have a block each; of the other `rest` tiles (0: none), every
+  // `group` tiles' stages are one line that `blocks` blocks share in pieces of `per`; `parts` in all
+  int whole, rest, group, blocks, per, parts;
   float* part;  // sums of pieces
 };
 
@@ -479,27 +479,30 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
   const int per_seg = (p.K + 63) >> 6;
   const int stages = MODE == kDx ? 2 * per_seg : per_seg;
 
-  // This block's piece of work: a whole tile, or stages [at, end) of the line of the rest, which
-  // touch at most two tiles (per < stages).
-  int tile, at = 0, end = stages;
+  // This block's piece of work: a whole tile, or stages [at, end) of the rest's, which touch at
+  // most two tiles (per < stages).
+  int tile, at = 0, end = 1, b = 0;
   const bool piece = (int)blockIdx.x >= p.whole;
   if (!piece) {
     tile = xcd_logical_block(blockIdx.x, p.whole);
   } else {
-    const int b = xcd_logical_block(blockIdx.x - p.whole, p.parts);
-    at = b * p.per;
-    end = min(at + p.per, p.rest * stages);
+    b = xcd_logical_block(blockIdx.x - p.whole, p.parts);
+    const int g = b / p.blocks, line = p.group * stages;
+    at = g * line + (b - g * p.blocks) * p.per;
+    end = min(min(at + p.per, (g + 1) * line), p.rest * stages);
     tile = p.whole;
   }
-  do {
+  while (at < end) {
     int s_begin = 0, s_end = stages, slot = -1;
     if (piece) {
       const int t = at / stages;
       tile = p.whole + t;
       s_begin = at - t * stages;
       s_end = min(stages, end - t * stages);
-      if (s_end - s_begin < stages) slot = at / p.per + t;
+      if (s_end - s_begin < stages) slot = b + t;
       at = t * stages + s_end;
+    } else {
+      at = end;
     }
     const TilePos tp = tile_pos(p, tile);
     const int m0 = tp.m * 256, n0 = tp.n * (MODE == kGateUp ? 128 : 256);
@@ -680,7 +683,7 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
         epilogue<MODE, H>(p, acc[i][0], acc[i][1], m, nb, nb + 128, hi);
       }
     }
-  } while (piece && at < end);
+  }
 }
 
 // The tiles whose stages several blocks shared: their sums, always added in the order of k, then the
@@ -690,7 +693,8 @@ __global__ __launch_bounds__(512) void gemm256_join_kernel(GemmArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x & 3, t = blockIdx.x >> 2;
   const int stages = (MODE == kDx ? 2 : 1) * ((p.K + 63) >> 6);
-  const int first = t * stages / p.per, last = ((t + 1) * stages - 1) / p.per;
+  const int g = t / p.group, from = (t - g * p.group) * stages;
+  const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
   if (first == last) return;  // one block had it all
   const TilePos tp = tile_pos(p, p.whole + t);
   const int m = tp.m * 256 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
@@ -857,32 +861,59 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
 // How a product is cut.  `n` columns count gate and up apart.
 struct Cut {
   int tile;  // 256 or 128
-  int tiles_m, tiles_n, whole, rest, parts, per;
+  int tiles_m, tiles_n, whole, rest, group, blocks, per, parts;
   size_t part_bytes;
 };
+
+// Tiles of 256 run one to a compute unit, tiles of 128 two; both in rounds that cost their fullest
+// unit's time, and the last round of 256 may share its tiles.  Measured in stages of the 256
+// tiles (1.3 us, of which 0.2 are what a whole chip's loads wait for each other; the 2 m0, n0 walks of
+// neighbours in step keep the operands in L2):
+//   a round of 256 tiles: the stages + 12 (first loads, epilogue);
+//   a round of up to 512 tiles of 128: the stages + 6 (M = 1021, N = 5632, K = 2048: 48 us), of up to 256: half
+//   the stages + 5 (M = 1021, N = 2048, K = 11264: 124 us);
+//   joining: 256 KB written and read for each piece, 0.09 a piece + 5.
+// Sharing cuts groups of tiles alike (all into 2 .. 16 parts, or 2 tiles into 3, or 3 into 4), so that blocks
+// at the same place of their groups still walk k in step: cutting one line of all tiles into equal
+// pieces left M = 2053, N = 4096, K = 11008 at 235 us, as slow as not sharing.
 Cut cut_of(int64_t M, int64_t n, int stages) {
   Cut c{};
-  const int64_t t256 = ((M + 255) / 256) * ((n + 255) / 256);
-  c.tile = t256 >= 128 || (t256 >= 16 && t256 * stages >= 2048) ? 256 : 128;
-  c.tiles_m = (int)((M + c.tile - 1) / c.tile);
-  c.tiles_n = (int)((n + c.tile - 1) / c.tile);
+  c.tile = 256;
+  c.tiles_m = (int)((M + 255) / 256);
+  c.tiles_n = (int)((n + 255) / 256);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
   c.whole = (int)tiles;
-  if (c.tile == 256) {
-    const int rest = (int)(tiles % kUnits);
-    // shared only where it saves more stages than writing and reading the sums again takes
-    if (rest && (kUnits - rest) * (int64_t)stages >= 24 * (int64_t)kUnits) {
-      int parts = kUnits;
-      if ((int64_t)rest * stages < 8 * (int64_t)parts) parts = (int)((int64_t)rest * stages / 8);
-      const int per = (int)(((int64_t)rest * stages + parts - 1) / parts);
-      if (per < stages) {
-        c.rest = rest;
-        c.whole = (int)tiles - rest;
-        c.per = per;
-        c.parts = (int)(((int64_t)rest * stages + per - 1) / per);
-        c.part_bytes = (size_t)(c.parts + rest) * kPartFloats * 4;
-      }
-    }
+  double cost = (double)(tiles / kUnits) * (stages + 12);
+  const int rest = (int)(tiles % kUnits);
+  if (rest) {
+    double best = stages + 12;
+    auto offer = [&](int group, int blocks) {
+      const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
+      if (groups * blocks > kUnits || per < 4 || per >= stages) return;
+      const double t = per + 12 + 0.09 * (groups * blocks + rest) + 5;
+      if (t >= best) return;
+      best = t;
+      c.rest = rest;
+      c.whole = (int)tiles - rest;
+      c.group = group;
+      c.blocks = blocks;
+      c.per = per;
+      c.parts = groups * blocks;
+      c.part_bytes = (size_t)(c.parts + rest) * kPartFloats * 4;
+    };
+    for (int k = 2; k <= 16; ++k) offer(1, k);
+    offer(2, 3);
+    offer(3, 4);
+    cost += best;
+  }
+  const int64_t t128 = ((M + 127) / 128) * ((n + 127) / 128), last = t128 % (2 * kUnits);
+  const double cost128 = (double)(t128 / (2 * kUnits)) * (stages + 6) +
+                         (last == 0 ? 0.0 : last > kUnits ? stages + 6 : 0.52 * stages + 5);
+  if (cost128 < cost) {
+    c = Cut{};
+    c.tile = 128;
+    c.tiles_m = (int)((M + 127) / 128);
+    c.tiles_n = (int)((n + 127) / 128);
   }
   return c;
 }
@@ -895,8 +926,10 @@ int gemm_go(GemmArgs& A, hipStream_t s) {
   A.tiles_n = c.tiles_n;
   A.whole = c.whole;
   A.rest = c.rest;
-  A.parts = c.parts;
+  A.group = c.group;
+  A.blocks = c.blocks;
   A.per = c.per;
+  A.parts = c.parts;
   if (A.tiles_m == 0 || A.tiles_n == 0) return FT_OK;
   if ((int64_t)A.tiles_m * A.tiles_n > 0x7ffffff) return fail(FT_EINVAL, "gated_ffn: too many tiles");
   if (c.tile == 256) {
