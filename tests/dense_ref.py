@@ -18,8 +18,9 @@ F32 = 2.0 ** -23
 TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -149}
 
 
-def exactly(t):
-    v = t.detach().cpu().double()
+def exactly(t, on="cpu"):
+    """on: where the 64-bit work is done (large cases: the GPU's own 64-bit products)."""
+    v = t.detach().to(on).double()
     return v, torch.zeros_like(v)
 
 
@@ -93,7 +94,7 @@ def ffn_bwd(x, wg, wu, wd, a, u, dy, kind, dt):
 def check(got, want, what=""):
     """Every element within its bound; prints the worst use of it."""
     v, e = want
-    g = got.detach().cpu().double()
+    g = got.detach().to(v.device).double()
     assert g.shape == v.shape, (what, g.shape, v.shape)
     assert torch.isfinite(g).all(), what
     use = ((g - v).abs() / e).max().item() if g.numel() else 0.0

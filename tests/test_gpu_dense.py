@@ -80,8 +80,8 @@ class Block:
         s = [saved[2 * n + i * m:2 * n + (i + 1) * m].reshape(self.T, self.f // 32) for i in range(2)]
         return c, s
 
-    def exact(self):
-        return [R.exactly(v) for v in (self.x, self.wg, self.wu, self.wd)]
+    def exact(self, on="cpu"):
+        return [R.exactly(v, on) for v in (self.x, self.wg, self.wu, self.wd)]
 
 
 FWD = [
@@ -172,6 +172,43 @@ def test_backward(T, d, f, t, kind, save, x8):
         A, U = (R.rounded(R.mm(X, R.t_(w)), b.dt) for w in (Wg, Wu))
     want = R.ffn_bwd(X, Wg, Wu, Wd, A, U, R.exactly(b.dy), kind, b.dt)
     for g, k in zip(got, ("dx", "dwg", "dwu", "dwd")):
+        R.check(g, want[k], k)
+
+
+@pytest.mark.parametrize("T,d,f,t,res", [
+    (1100, 2056, 11008, "bf16", True),   # every tile of the second product into several parts, ragged ends
+    (2053, 4096, 11008, "fp16", False),  # two tiles into three parts, and an odd tile left over
+    (2816, 4096, 11008, "bf16", False),  # three into four
+])
+def test_forward_with_shared_tiles(T, d, f, t, res):
+    torch = torch_mod()
+    _say("ffn shared", T, d, f, t, res)
+    b = Block(T, d, f, t, "silu", seed=11)
+    r = torch.randn(T, d, generator=b.g).cuda() if res else None
+    y, _ = b.forward("none", r, "fp32" if res else t)
+    again, _ = b.forward("none", r, "fp32" if res else t)
+    torch.cuda.synchronize()
+    assert torch.equal(y, again)
+    R.check(y, R.ffn(*b.exact("cuda"), "silu", b.dt, R.exactly(r, "cuda") if res else None,
+                     torch.float32 if res else b.dt)["y"], "y")
+
+
+@pytest.mark.parametrize("T,d,f,t", [
+    (1021, 2048, 5632, "fp16"),  # dx's few tiles into eight parts, across the two weights
+    (8200, 2048, 4096, "bf16"),  # dw_down's tiles into two
+])
+def test_backward_with_shared_tiles(T, d, f, t):
+    torch = torch_mod()
+    _say("bwd shared", T, d, f, t)
+    b = Block(T, d, f, t, "silu", seed=12)
+    _, saved = b.forward("16")
+    got = b.backward(saved, "16")
+    again = b.backward(saved, "16")
+    torch.cuda.synchronize()
+    A, U = (R.exactly(v, "cuda") for v in b.split16(saved))
+    want = R.ffn_bwd(*b.exact("cuda"), A, U, R.exactly(b.dy, "cuda"), "silu", b.dt)
+    for g, h, k in zip(got, again, ("dx", "dwg", "dwu", "dwd")):
+        assert torch.equal(g, h)
         R.check(g, want[k], k)
 
 
