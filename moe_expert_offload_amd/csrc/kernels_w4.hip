@@ -51,111 +51,133 @@ __device__ __forceinline__ i32x4_t reorder(i32x4_t x) {
                  (int)__builtin_amdgcn_perm(d, b, 0x05040100u), (int)__builtin_amdgcn_perm(d, b, 0x07060302u)};
 }
 
-// Copies `bytes` (more than 0) from memory of any alignment to LDS, 16 at a time: a last short piece is moved
-// back to end with the rest.  Less than one piece goes byte by byte.
-__device__ __forceinline__ void stage_bytes(uint8_t* dst, const uint8_t* src, int bytes) {
-  if (bytes >= 16) {
-    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) {
-      const int at = min(i, bytes - 16);
-      uint4 v;
-      __builtin_memcpy(&v, src + at, 16);
-      __builtin_memcpy(dst + at, &v, 16);
-    }
-  } else if ((int)threadIdx.x < bytes) {
-    dst[threadIdx.x] = src[threadIdx.x];
+// The scales and zeros of a tile's rows on their way from memory of any alignment to LDS, 16 bytes a
+// thread at a time; a region's last short piece is moved back to end with the rest (regions have 16
+// bytes or more).  All regions' loads leave before the first is written, without a branch between
+// (one behind the other they took 1.7 us each).
+template <int R>
+struct Regions {
+  const uint8_t* src[R];
+  uint8_t* dst[R];
+  int bytes[R];
+  uint4 v[R];
+  __device__ __forceinline__ void load(int i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) __builtin_memcpy(&v[r], src[r] + min(i, bytes[r] - 16), 16);
   }
-}
+  __device__ __forceinline__ void store(int i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i < bytes[r]) __builtin_memcpy(dst[r] + min(i, bytes[r] - 16), &v[r], 16);
+  }
+};
 
-// TK: tokens the kernel is made for (1, 4, 8: x in LDS, reordered once; 16, 32, 64 a pass: a chunk's x
-// comes with its codes).  The tile's scales and zeros lie in LDS: loaded chunk by chunk each of these loads
-// touches 16 rows and costs the load unit as much as the codes themselves; so do four loads of x that
-// all rows of tokens share.  SL = false reads them from memory one by one, for K / group too
-// large for LDS.  U chunks of a wave are in flight at once.
+// TK: tokens the kernel is made for.  Up to 16 (NX > 0): a chunk's x comes as whole rows of 256
+// bytes, 4 tokens a load, and goes to its fragments through a piece of LDS of the wave's own, reordered on the way
+// (a wave's LDS operations run in order, so that takes no barrier).  Loading fragments from
+// memory takes 4 loads of 16 rows whatever the number of tokens, each as dear to the load unit as the
+// chunk's codes.  32 and 64 a pass: fragments from memory.
+// The tile's scales and zeros lie in LDS for the same reason: chunk by chunk each of these loads touches 16
+// rows.  SL = false reads them from memory one by one, for K / group too large for LDS or matrices too small
+// for Regions.
+// U chunks of a wave are in flight at once; a chunk's registers are loaded again as it is used up.
 template <bool GU, bool H, int G, int TK, int W, int U, bool SL>
 __global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
-  constexpr bool XL = TK <= 8;
-  constexpr int RB = GU ? 8 : 16, NM = GU ? 2 : 1, NG = 128 / G, PER = 4 / NG, NT = TK < 16 ? 1 : TK / 16;
+  constexpr int NX = TK > 16 ? 0 : (TK + 3) / 4;
+  constexpr int RB = GU ? 8 : 16, NM = GU ? 2 : 1, NG = 128 / G, PER = 4 / NG, NT = TK <= 16 ? 1 : TK / 16;
   constexpr int NR = TK == 1 ? 1 : 4;  // results of a lane that can belong to a token
+  constexpr int XS = 17;               // row stride of x in LDS, in 16 bytes: rows start on different banks
   __shared__ float red[W][NT * 16][16];
-  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ uint4 sx[W][NX ? NX * 4 * XS : 1];
+  extern __shared__ __attribute__((aligned(16))) uint8_t ss[];  // scales of the tile's rows, then zeros
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.x * RB, t0 = blockIdx.y * (16 * NT), nt = min(p.T - t0, 16 * NT);
   const int KG = p.K / G, KB = p.K >> 1;
   const int chunks = (p.K + 127) >> 7;
   const int nr = min(RB, p.N - r0), rl = min(GU ? (n & 7) : n, nr - 1);  // rows of the tile, the lane's
+  const int rb = SL ? min(r0, p.N - RB) : r0;  // LDS holds RB rows from here
   const bool second = GU && n >= 8;
   const uint8_t* const cp = (second ? p.codes2 : p.codes) + (int64_t)(r0 + rl) * KB + g * 16;
   const bool hasz = (second ? p.zeros2 : p.zeros) != nullptr;
   uint32_t mask, one;
   asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(Bias16<H>::mask));
   asm("v_mov_b32 %0, %1" : "=v"(one) : "i"(Bias16<H>::one));
-
-  // dynamic LDS: x [TK][K + 8] (XL), then the scales of the rows of each matrix, then their zeros
-  const int xs = (p.K >> 3) + 1;  // row stride of x, pieces of 16 bytes: an odd number of them (K % 32 == 0)
-  uint4* const sx = reinterpret_cast<uint4*>(dyn);
-  uint8_t* const ss = dyn + (XL ? (size_t)min(p.T, TK) * xs * 16 : 0);
   uint8_t* const sz = ss + 16 * KG * 2;
 
-  auto load = [&](uint4& q, int ci) {
-    const int k0 = min(ci, chunks - 1) << 7;
-    // K % 32 == 0: a lane's 32 codes are there or not as a whole
-    q = *reinterpret_cast<const uint4*>(cp + (k0 + g * 32 < p.K ? k0 >> 1 : -g * 16));
-  };
-
-  uint4 q[U];
-  if constexpr (XL) {
-    const int per = p.K >> 3;
-    i32x4_t v[TK];
-    int c = threadIdx.x;
+  // rows of x past T repeat the last one; their sums are dropped
+  const uint8_t* xp[NX ? NX : NT];
 #pragma unroll
-    for (int t = 0; t < TK; ++t)
-      v[t] = *reinterpret_cast<const i32x4_t*>(p.x + (int64_t)min(t, nt - 1) * p.ldx + min(c, per - 1) * 8);
-    while (true) {
-      if (c < per) {
-#pragma unroll
-        for (int t = 0; t < TK; ++t)
-          if (t < nt) {
-            const i32x4_t r = reorder(v[t]);
-            sx[t * xs + c] = make_uint4(r.x, r.y, r.z, r.w);
-          }
-      }
-      c += 64 * W;
-      if (c - (int)threadIdx.x >= per) break;
-#pragma unroll
-      for (int t = 0; t < TK; ++t)
-        v[t] = *reinterpret_cast<const i32x4_t*>(p.x + (int64_t)min(t, nt - 1) * p.ldx + min(c, per - 1) * 8);
-    }
+  for (int i = 0; i < (NX ? NX : NT); ++i) {
+    const int t = NX ? i * 4 + g : i * 16 + n;
+    xp[i] = reinterpret_cast<const uint8_t*>(p.x + (int64_t)(t0 + min(t, nt - 1)) * p.ldx) + (NX ? n : g) * 16;
   }
+  struct Chunk {
+    uint4 q;
+    i32x4_t x[NX ? NX : 4 * NT];
+  };
+  Chunk ch[U];
+  auto load = [&](Chunk& c, int ci) {
+    const int k0 = min(ci, chunks - 1) << 7;  // past the last: that one again, not used
+    // K % 32 == 0: a lane's 32 codes are there or not as a whole; what is not there is not used
+    c.q = *reinterpret_cast<const uint4*>(cp + (k0 + g * 32 < p.K ? k0 >> 1 : -g * 16));
+    if constexpr (NX > 0) {
+      const int k = k0 + n * 8 < p.K ? k0 * 2 : -n * 16;
+#pragma unroll
+      for (int i = 0; i < NX; ++i) c.x[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * 32 < p.K ? k0 + j * 32 : 0;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) c.x[j * NT + i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k * 2);
+      }
+    }
+  };
+  Regions<2 * NM> rg;
+  const int at = threadIdx.x * 16;
   if constexpr (SL) {
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(m ? p.scales2 : p.scales);
-      const uint8_t* z = m ? p.zeros2 : p.zeros;
-      stage_bytes(ss + m * 8 * KG * 2, s + (int64_t)r0 * KG * 2, nr * KG * 2);
-      if (z) stage_bytes(sz + m * 8 * KG, z + (int64_t)r0 * KG, nr * KG);
+      const uint8_t *sc = reinterpret_cast<const uint8_t*>(m ? p.scales2 : p.scales), *z = m ? p.zeros2 : p.zeros;
+      rg.src[m] = sc + (int64_t)rb * KG * 2;
+      rg.dst[m] = ss + m * 8 * KG * 2;
+      rg.bytes[m] = RB * KG * 2;
+      rg.src[NM + m] = (z ? z : sc) + (int64_t)rb * KG;  // without zeros these bytes are not used
+      rg.dst[NM + m] = sz + m * 8 * KG;
+      rg.bytes[NM + m] = RB * KG;
     }
+    rg.load(at);
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) load(q[u], wave + u * W);
-  const uint8_t* xp[NT];  // rows of x past T repeat the last one; their sums are dropped
-  if constexpr (!XL) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-      xp[i] = reinterpret_cast<const uint8_t*>(p.x + (int64_t)(t0 + min(i * 16 + n, nt - 1)) * p.ldx) + g * 16;
+  for (int u = 0; u < U; ++u) load(ch[u], wave + u * W);
+  if constexpr (SL) {
+    rg.store(at);
+    for (int i = at + 64 * W * 16; i - at < RB * KG * 2; i += 64 * W * 16) {
+      rg.load(i);
+      rg.store(i);
+    }
+    __syncthreads();
   }
-  const uint4* const xl = sx + min(n, nt - 1) * xs + g;
-  const int lr = (second ? 8 : 0) + rl;
+  const int lr = (second ? 8 : 0) + rl + r0 - rb;
   const uint16_t* const sp = SL ? reinterpret_cast<const uint16_t*>(ss) + lr * KG
                                 : (second ? p.scales2 : p.scales) + (int64_t)(r0 + rl) * KG;
-  const uint8_t* const zp = SL ? sz + lr * KG : (second ? p.zeros2 : p.zeros) + (int64_t)(r0 + rl) * KG;
+  const uint8_t* const zp = SL      ? sz + lr * KG
+                            : hasz ? (second ? p.zeros2 : p.zeros) + (int64_t)(r0 + rl) * KG
+                                   : reinterpret_cast<const uint8_t*>(sp);  // read, not used
   f32x4_t acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{};
-  if constexpr (XL || SL) __syncthreads();
 
-  auto use = [&](const uint4& qu, const i32x4_t (&xu)[XL ? 1 : 4][NT], int k0) {
-    uint32_t w[4] = {qu.x, qu.y, qu.z, qu.w};
+  uint4* const xw = sx[wave] + g * XS + n;
+  const uint4* const xr = sx[wave] + min(n, NX * 4 - 1) * XS + g;
+  auto use = [&](const Chunk& c, int k0) {
+    if constexpr (NX > 0) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) xw[i * 4 * XS] = __builtin_bit_cast(uint4, reorder(c.x[i]));
+      __builtin_amdgcn_wave_barrier();
+    }
+    uint32_t w[4] = {c.q.x, c.q.y, c.q.z, c.q.w};
     // word j of row group g to row group j, word g
     auto s32 = [](uint32_t& a, uint32_t& b) {
       const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -171,23 +193,35 @@ __global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
     s32(w[1], w[3]);
     s16(w[0], w[1]);
     s16(w[2], w[3]);
+    float scales[NG];
+    uint32_t zeros[NG];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      const int gi = NG == 1 ? k0 / G : min(k0 / G + j, KG - 1);
+      scales[j] = to_f32<H>(sp[gi]);
+      zeros[j] = zp[gi];
+    }
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       if (k0 + j * G >= p.K) break;  // a group is there whole or not at all
-      const float scale = to_f32<H>(sp[k0 / G + j]);
-      const uint32_t zb = hasz ? zp[k0 / G + j] : 8;
+      const float scale = scales[j];
+      const uint32_t zb = hasz ? zeros[j] : 8;
       const int bw = (int)((zb << Bias16<H>::sh) * 0x10001u | Bias16<H>::one | 0x80008000u);
       const i32x4_t bias = {bw, bw, bw, bw};
       f32x4_t s[NT];
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const i32x4_t wv = widen<H>(w[j * PER + e], mask, one);
+        const int jj = j * PER + e;
+        const i32x4_t wv = widen<H>(w[jj], mask, one);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const i32x4_t xr = XL ? *reinterpret_cast<const i32x4_t*>(xl + (k0 >> 3) + (j * PER + e) * 4)
-                                : reorder(xu[XL ? 0 : j * PER + e][i]);
-          s[i] = mfma16<H>(xr, wv, e ? s[i] : f32x4_t{});
-          s[i] = mfma16<H>(xr, bias, s[i]);
+          i32x4_t xv;
+          if constexpr (NX > 0)
+            xv = __builtin_bit_cast(i32x4_t, xr[jj * 4]);
+          else
+            xv = reorder(c.x[jj * NT + i]);
+          s[i] = mfma16<H>(xv, wv, e ? s[i] : f32x4_t{});
+          s[i] = mfma16<H>(xv, bias, s[i]);
         }
       }
 #pragma unroll
@@ -195,34 +229,21 @@ __global__ __launch_bounds__(64 * W, W / 4) void w4_kernel(W4Args p) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(scale, s[i][r], acc[i][r]);
     }
+    if constexpr (NX > 0) __builtin_amdgcn_wave_barrier();
   };
-  i32x4_t x[U][XL ? 1 : 4][NT];
-  auto load_x = [&](i32x4_t (&xu)[XL ? 1 : 4][NT], int ci) {
-    if constexpr (!XL) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k0 = min(ci, chunks - 1) << 7, k = k0 + j * 32 < p.K ? k0 + j * 32 : 0;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) xu[j][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + k * 2);
-      }
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) load_x(x[u], wave + u * W);
   __builtin_amdgcn_sched_barrier(0);
   int c0 = wave;
   for (; c0 + W * U < chunks; c0 += W * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      use(q[u], x[u], (c0 + u * W) << 7);  // all before the last chunk
-      load(q[u], c0 + (U + u) * W);
-      load_x(x[u], c0 + (U + u) * W);
+      use(ch[u], (c0 + u * W) << 7);  // all before the last chunk
+      load(ch[u], c0 + (U + u) * W);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (c0 + u * W < chunks) use(q[u], x[u], (c0 + u * W) << 7);
+    if (c0 + u * W < chunks) use(ch[u], (c0 + u * W) << 7);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -255,22 +276,22 @@ template <bool GU, bool H, int G>
 int w4_go(const W4Args& A, hipStream_t s) {
   constexpr int RB = GU ? 8 : 16;
   const unsigned tiles = (unsigned)(((int64_t)A.N + RB - 1) / RB), passes = (unsigned)((A.T + 63) / 64);
-  const size_t sl = 16 * (size_t)(A.K / G) * 3;                                            // scales and zeros
-  const size_t xl = (size_t)(A.T < 8 ? A.T : 8) * (2 * (size_t)A.K + 16), most = 128 << 10;  // 32 KB for the waves' parts
-  if (sl > most)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 64, 8, 1, false>), dim3(tiles, passes), dim3(512), 0, s, A);
-  else if (A.T == 1 && sl + xl <= most)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 1, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
-  else if (A.T <= 4 && sl + xl <= most)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 4, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
-  else if (A.T <= 8 && sl + xl <= most)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 8, 8, 4, true>), dim3(tiles), dim3(512), sl + xl, s, A);
+  const size_t sl = 16 * (size_t)(A.K / G) * 3;  // scales and zeros
+  auto go = [&](auto kernel, unsigned y, size_t lds) { hipLaunchKernelGGL(kernel, dim3(tiles, y), dim3(512), lds, s, A); };
+  if (sl > (64 << 10) || A.N < RB || RB * (A.K / G) < 16)
+    go(w4_kernel<GU, H, G, 64, 8, 1, false>, passes, 0);
+  else if (A.T == 1)
+    go(w4_kernel<GU, H, G, 1, 8, 4, true>, 1, sl);
+  else if (A.T <= 4)
+    go(w4_kernel<GU, H, G, 4, 8, 4, true>, 1, sl);
+  else if (A.T <= 8)
+    go(w4_kernel<GU, H, G, 8, 8, 4, true>, 1, sl);
   else if (A.T <= 16)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 16, 8, 4, true>), dim3(tiles), dim3(512), sl, s, A);
+    go(w4_kernel<GU, H, G, 16, 8, 3, true>, 1, sl);
   else if (A.T <= 32)
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 32, 8, 2, true>), dim3(tiles), dim3(512), sl, s, A);
+    go(w4_kernel<GU, H, G, 32, 8, 2, true>, 1, sl);
   else
-    hipLaunchKernelGGL((w4_kernel<GU, H, G, 64, 8, 1, true>), dim3(tiles, passes), dim3(512), sl, s, A);
+    go(w4_kernel<GU, H, G, 64, 8, 1, true>, passes, sl);
   return launched("w4_kernel");
 }
 template <bool GU, bool H>
