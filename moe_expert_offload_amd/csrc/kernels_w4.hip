@@ -58,17 +58,24 @@ __device__ __forceinline__ i32x4_t reorder(i32x4_t x) {
 template <int R>
 struct Regions {
   const uint8_t* src[R];
-  uint8_t* dst[R];
+  uint8_t* dst[R];  // 8-byte aligned, and so are the pieces: regions are multiples of 8 bytes
   int bytes[R];
-  uint4 v[R];
+  i32x4_t v[R];
   __device__ __forceinline__ void load(int i) {
+    struct __attribute__((packed)) Any {
+      i32x4_t v;
+    };
 #pragma unroll
-    for (int r = 0; r < R; ++r) __builtin_memcpy(&v[r], src[r] + min(i, bytes[r] - 16), 16);
+    for (int r = 0; r < R; ++r) v[r] = reinterpret_cast<const Any*>(src[r] + min(i, bytes[r] - 16))->v;
   }
   __device__ __forceinline__ void store(int i) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (i < bytes[r]) __builtin_memcpy(dst[r] + min(i, bytes[r] - 16), &v[r], 16);
+      if (i < bytes[r]) {
+        uint2* d = reinterpret_cast<uint2*>(dst[r] + min(i, bytes[r] - 16));
+        d[0] = make_uint2((uint32_t)v[r].x, (uint32_t)v[r].y);
+        d[1] = make_uint2((uint32_t)v[r].z, (uint32_t)v[r].w);
+      }
   }
 };
 
