@@ -94,7 +94,8 @@ struct GemmArgs {
   uint16_t *h, *dag;   // kDh outputs: h [M, N], da and du [M, 2N]
   int tiles_m, tiles_n;
   // gemm256_kernel: the first `whole` tiles have a block each; of the other `rest` tiles (0: none), every
-  // `group` tiles' stages are one line that `blocks` blocks share in pieces of `per`; `parts` in all
+  // `group` tiles' stages are one line that `blocks` blocks share in pieces of `per`; `parts` in all.
+  // gemm_kernel: all tiles (rest > 0) or none are shared, one a group.
   int whole, rest, group, blocks, per, parts;
   float* part;  // sums of pieces
 };
@@ -301,6 +302,33 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16_t& c0, 
   }
 }
 
+// Two 32x32 results of a wave among a piece's sums: 2048 floats, quads of 4 n by lane.
+__device__ __forceinline__ void store_part(float* at, const f32x16_t (&c)[2], int lane) {
+  float4* d = reinterpret_cast<float4*>(at) + lane;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      d[(j * 4 + q) * 64] = make_float4(c[j][4 * q], c[j][4 * q + 1], c[j][4 * q + 2], c[j][4 * q + 3]);
+}
+__device__ __forceinline__ void add_part(f32x16_t (&c)[2], const float* at, int lane) {
+  const float4* d = reinterpret_cast<const float4*>(at) + lane;
+  float4 v[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[j][q] = d[(j * 4 + q) * 64];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      c[j][4 * q] += v[j][q].x;
+      c[j][4 * q + 1] += v[j][q].y;
+      c[j][4 * q + 2] += v[j][q].z;
+      c[j][4 * q + 3] += v[j][q].w;
+    }
+}
+
 template <int MODE, bool H, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs p) {
   constexpr bool AT = MODE == kDw;
@@ -314,8 +342,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  // consecutive blocks share an XCD
-  const TilePos tp = tile_pos(p, xcd_logical_block(blockIdx.x, gridDim.x));
+  const int per_seg = (p.K + 63) >> 6;
+  const int stages = MODE == kDx ? 2 * per_seg : per_seg;
+  // consecutive blocks share an XCD; `blocks` of them share each tile's stages (rest > 0)
+  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int tile = p.rest ? lb / p.blocks : lb;
+  const int s_begin = p.rest ? (lb - tile * p.blocks) * p.per : 0;
+  const int s_end = p.rest ? min(stages, s_begin + p.per) : stages;
+  const TilePos tp = tile_pos(p, tile);
   const int m0 = tp.m * BM, n0 = tp.n * (MODE == kGateUp ? BN / 2 : BN);
 
   // ---- loads: per-lane byte offsets within the tile, from a base that moves with k ----
@@ -351,8 +385,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
     }
   }
 
-  const int per_seg = (p.K + 63) >> 6;
-  const int stages = MODE == kDx ? 2 * per_seg : per_seg;
   const uint32_t sm0 = lds_addr(sm);
 
   auto load_stage = [&](int s) {
@@ -407,14 +439,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
 
-  if (stages > 0) load_stage(0);
-  for (int s = 0; s < stages; ++s) {
+  if (s_begin < s_end) load_stage(s_begin);
+  for (int s = s_begin; s < s_end; ++s) {
     // this wave's loads of stage s have landed; past the barrier everyone's have, and nobody
     // reads the other buffer any more
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + 1 < stages) load_stage(s + 1);
+    if (s + 1 < s_end) load_stage(s + 1);
     const uint8_t* sa = sm + (s & 1) * SBYTES;
     const uint8_t* sb = sa + ABYTES;
 #pragma unroll
@@ -436,9 +468,30 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int nb = n0 + wn * (MODE == kGateUp ? 32 : 64);
-    epilogue<MODE, H>(p, acc[i][0], acc[i][1], m0 + wm * TM + i * 32 + l31, nb, nb + 32, hi);
+    if (p.rest) {
+      store_part(p.part + (size_t)lb * (BM * BN) + (wave * MT + i) * 2 * 1024, acc[i], lane);
+    } else {
+      const int nb = n0 + wn * (MODE == kGateUp ? 32 : 64);
+      epilogue<MODE, H>(p, acc[i][0], acc[i][1], m0 + wm * TM + i * 32 + l31, nb, nb + 32, hi);
+    }
   }
+}
+
+// The shared tiles of the kernel above: sums in the order of k, then the epilogue.  A block per tile and
+// 32-row piece of the waves.
+template <int MODE, bool H, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_join_kernel(GemmArgs p) {
+  constexpr int TM = BM / WM, MT = TM / 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN, t = blockIdx.x / MT, i = blockIdx.x % MT;
+  const TilePos tp = tile_pos(p, t);
+  const int m = tp.m * BM + wm * TM + i * 32;
+  if (m >= p.M) return;
+  f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
+  for (int b = 0; b < p.blocks; ++b)
+    add_part(acc, p.part + (size_t)(t * p.blocks + b) * (BM * BN) + (wave * MT + i) * 2 * 1024, lane);
+  const int nb = tp.n * (MODE == kGateUp ? BN / 2 : BN) + wn * (MODE == kGateUp ? 32 : 64);
+  epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 32, lane >> 5);
 }
 
 // The same product on 256 x 256 tiles, for results large enough to fill the chip with them.
@@ -458,11 +511,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 // and -1.  It is waited for by both groups at least one barrier before its first read, and has six
 // sections to arrive.  Loads past the last stage are masked (they write zeros nobody reads), which keeps
 // the counts of the waits.  (Four steps of a quarter each, with 8 MFMAs a section, took 4 % longer.)
-// Where the 32x32 result (i, j) of a wave lies in a piece's sums, in float4: 4 quads of 64 lanes each.
-constexpr int kPartFloats = 256 * 256;
-__device__ __forceinline__ size_t part_at(int slot, int wave, int i, int j) {
-  return (size_t)slot * (kPartFloats / 4) + (((wave * 4 + i) * 2 + j) * 4) * 64;
-}
+constexpr int kPartFloats = 256 * 256;  // of a 256 x 256 tile
 
 template <int MODE, bool H>
 __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
@@ -670,13 +719,8 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (slot >= 0) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float4* d = reinterpret_cast<float4*>(p.part) + part_at(slot, wave, i, j) + lane;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            d[q * 64] = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-        }
+        if (m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 < p.M)
+          store_part(p.part + (size_t)slot * kPartFloats + (wave * 4 + i) * 2048, acc[i], lane);
       } else {
         const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + l31;
         const int nb = n0 + wn * 32;
@@ -700,23 +744,7 @@ __global__ __launch_bounds__(512) void gemm256_join_kernel(GemmArgs p) {
   const int m = tp.m * 256 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
   if (m >= p.M) return;
   f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
-  for (int b = first; b <= last; ++b) {
-    float4 v[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        v[j][q] = (reinterpret_cast<const float4*>(p.part) + part_at(b + t, wave, i, j) + lane)[q * 64];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[j][4 * q] += v[j][q].x;
-        acc[j][4 * q + 1] += v[j][q].y;
-        acc[j][4 * q + 2] += v[j][q].z;
-        acc[j][4 * q + 3] += v[j][q].w;
-      }
-  }
+  for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * kPartFloats + (wave * 4 + i) * 2048, lane);
   const int nb = tp.n * (MODE == kGateUp ? 128 : 256) + wn * 32;
   epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 128, lane >> 5);
 }
@@ -742,7 +770,7 @@ struct SkinnyArgs {
 
 template <bool GU, bool H, int NT, int W>
 __global__ __launch_bounds__(64 * W) void skinny_kernel(SkinnyArgs p) {
-  constexpr int RB = GU ? 8 : 16, U = NT == 1 ? 8 : (NT == 2 ? 4 : 2);
+  constexpr int RB = GU ? 8 : 16, U = NT <= 2 ? 4 : 2;
   __shared__ float red[W][NT * 16][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
@@ -872,7 +900,7 @@ struct Cut {
 //   a round of 256 tiles: the stages + 12 (first loads, epilogue);
 //   a round of up to 512 tiles of 128: the stages + 6 (M = 1021, N = 5632, K = 2048: 48 us), of up to 256: half
 //   the stages + 5 (M = 1021, N = 2048, K = 11264: 124 us);
-//   joining: 256 KB written and read for each piece, 0.09 a piece + 5.
+//   joining: 256 KB written and read for each piece, 0.07 a piece + 4 (a quarter of it for 128, + 6).
 // Sharing cuts groups of tiles alike (all into 2 .. 16 parts, or 2 tiles into 3, or 3 into 4), so that blocks
 // at the same place of their groups still walk k in step: cutting one line of all tiles into equal
 // pieces left M = 2053, N = 4096, K = 11008 at 235 us, as slow as not sharing.
@@ -890,7 +918,7 @@ Cut cut_of(int64_t M, int64_t n, int stages) {
     auto offer = [&](int group, int blocks) {
       const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
       if (groups * blocks > kUnits || per < 4 || per >= stages) return;
-      const double t = per + 12 + 0.09 * (groups * blocks + rest) + 5;
+      const double t = per + 12 + 0.07 * (groups * blocks + rest) + 4;
       if (t >= best) return;
       best = t;
       c.rest = rest;
@@ -906,14 +934,28 @@ Cut cut_of(int64_t M, int64_t n, int stages) {
     offer(3, 4);
     cost += best;
   }
-  const int64_t t128 = ((M + 127) / 128) * ((n + 127) / 128), last = t128 % (2 * kUnits);
-  const double cost128 = (double)(t128 / (2 * kUnits)) * (stages + 6) +
-                         (last == 0 ? 0.0 : last > kUnits ? stages + 6 : 0.52 * stages + 5);
-  if (cost128 < cost) {
+  // 128: whole tiles, or all of them cut alike
+  const int tm = (int)((M + 127) / 128), tn = (int)((n + 127) / 128);
+  const int64_t t128 = (int64_t)tm * tn;
+  for (int k = 1; k <= 16; ++k) {
+    const int64_t nb = t128 * k, last = nb % (2 * kUnits);
+    const int per = (stages + k - 1) / k;
+    if (k > 1 && (nb > 2 * kUnits || per < 2)) break;
+    double t = (double)(nb / (2 * kUnits)) * (per + 6) + (last == 0 ? 0.0 : last > kUnits ? per + 6 : 0.52 * per + 5);
+    if (k > 1) t += 0.0175 * (double)(nb + t128) + 6;
+    if (t >= cost) continue;
+    cost = t;
     c = Cut{};
     c.tile = 128;
-    c.tiles_m = (int)((M + 127) / 128);
-    c.tiles_n = (int)((n + 127) / 128);
+    c.tiles_m = tm;
+    c.tiles_n = tn;
+    c.whole = c.parts = (int)nb;
+    c.blocks = k;
+    c.per = per;
+    if (k > 1) {
+      c.rest = (int)t128;
+      c.part_bytes = (size_t)nb * 128 * 128 * 4;
+    }
   }
   return c;
 }
@@ -936,7 +978,9 @@ int gemm_go(GemmArgs& A, hipStream_t s) {
     hipLaunchKernelGGL((gemm256_kernel<MODE, H>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
     if (c.rest) hipLaunchKernelGGL((gemm256_join_kernel<MODE, H>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
   } else {
-    hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)(c.tiles_m * c.tiles_n)), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)c.parts), dim3(256), 0, s, A);
+    if (c.rest)
+      hipLaunchKernelGGL((gemm_join_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)c.rest * 2), dim3(256), 0, s, A);
   }
   return launched("gemm_kernel");
 }
@@ -950,8 +994,9 @@ template <bool GU, bool H>
 int skinny_go(SkinnyArgs& A, hipStream_t s) {
   constexpr int RB = GU ? 8 : 16;
   const unsigned nb = (unsigned)((A.N + RB - 1) / RB);
+  // (one token, d = 4096, d_ff = 2048, both products: 13.1 us with 16 waves, 14.5 us with 8)
   if (A.T <= 16)
-    hipLaunchKernelGGL((skinny_kernel<GU, H, 1, 8>), dim3(nb, 1), dim3(512), 0, s, A);
+    hipLaunchKernelGGL((skinny_kernel<GU, H, 1, 16>), dim3(nb, 1), dim3(1024), 0, s, A);
   else if (A.T <= 32)
     hipLaunchKernelGGL((skinny_kernel<GU, H, 2, 8>), dim3(nb, 1), dim3(512), 0, s, A);
   else

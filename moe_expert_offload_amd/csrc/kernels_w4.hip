@@ -285,16 +285,19 @@ int w4_go(const W4Args& A, hipStream_t s) {
   const unsigned tiles = (unsigned)(((int64_t)A.N + RB - 1) / RB), passes = (unsigned)((A.T + 63) / 64);
   const size_t sl = 16 * (size_t)(A.K / G) * 3;  // scales and zeros
   auto go = [&](auto kernel, unsigned y, size_t lds) { hipLaunchKernelGGL(kernel, dim3(tiles, y), dim3(512), lds, s, A); };
+  // Chunks in flight a wave: more of them is longer code, which these short kernels wait for as it is
+  // fetched (one token d = 4096, d_ff = 11008, group 128, chunks in flight 1, 2, 3, 4, 8: 21.4, 20.6, 23.9, 22.2,
+  // 31.3 us; 16 tokens d = 4096, d_ff = 2048, group 32, 1, 2, 3: 14.9, 15.2, 16.1 us).
   if (sl > (64 << 10) || A.N < RB || RB * (A.K / G) < 16)
     go(w4_kernel<GU, H, G, 64, 8, 1, false>, passes, 0);
   else if (A.T == 1)
-    go(w4_kernel<GU, H, G, 1, 8, 4, true>, 1, sl);
+    go(w4_kernel<GU, H, G, 1, 8, 2, true>, 1, sl);
   else if (A.T <= 4)
-    go(w4_kernel<GU, H, G, 4, 8, 4, true>, 1, sl);
+    go(w4_kernel<GU, H, G, 4, 8, 2, true>, 1, sl);
   else if (A.T <= 8)
-    go(w4_kernel<GU, H, G, 8, 8, 4, true>, 1, sl);
+    go(w4_kernel<GU, H, G, 8, 8, 2, true>, 1, sl);
   else if (A.T <= 16)
-    go(w4_kernel<GU, H, G, 16, 8, 3, true>, 1, sl);
+    go(w4_kernel<GU, H, G, 16, 8, 1, true>, 1, sl);
   else if (A.T <= 32)
     go(w4_kernel<GU, H, G, 32, 8, 2, true>, 1, sl);
   else
