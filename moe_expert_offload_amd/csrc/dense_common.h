@@ -70,6 +70,12 @@ __device__ __forceinline__ float to_f32(uint16_t v) {
 // A buffer without an end of its own: offsets are checked against kOOB alone.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) { return buf_rsrc(p, 0x7fffffffu); }
 
+__device__ __forceinline__ uint2 buf_ld8b(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  typedef int i32x2_t __attribute__((ext_vector_type(2)));
+  const i32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+  return make_uint2((uint32_t)v.x, (uint32_t)v.y);
+}
+
 // ---- activations --------------------------------------------------------------------
 // act(z) and act'(z).  Every value that leaves these is rounded to 16 bits (or 8) after, so
 // exp and the reciprocal are the hardware's (a few ulp of fp32).
