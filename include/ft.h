@@ -419,7 +419,7 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
  * and so may the three weight gradients together.  With T = 0 the weights' gradients
  * are zeros.
  * saved, save_fmt: a and u as the forward call kept them; FT_SAVE_NONE computes them
- * again from x (4 T d d_ff more operations), rounded to `dtype`.
+ * again from x (4 T d d_ff more operations), in fp32.
  * x: `dtype` [T, d], or with x_scales not NULL MX8 codes [T, d] (contiguous, ldx = d,
  * d % 32 == 0) with their scales [T, d / 32].  Scales and MX8 saves need no alignment
  * beyond 16 bytes.

@@ -127,7 +127,7 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
 size_t ft_gated_ffn_bwd_workspace_bytes(int32_t T, int32_t d, int32_t d_ff, int32_t save_fmt, int32_t x_mx8) {
   if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8) || save_fmt < FT_SAVE_NONE || save_fmt > FT_SAVE_MX8) return 0;
   size_t n = align256((size_t)T * d_ff * 2) + align256((size_t)T * d_ff * 4);  // h; da and du
-  if (save_fmt == FT_SAVE_NONE) n += align256((size_t)T * d_ff * 4);           // a and u
+  if (save_fmt == FT_SAVE_NONE) n += align256((size_t)T * d_ff * 4);           // dh
   if (x_mx8) n += align256((size_t)T * d * 2);                                 // x
   return n + ft::gated_ffn_part_bytes(T, d, d_ff, true) + 256;
 }
@@ -180,8 +180,9 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
   G.dwu = static_cast<uint16_t*>(dw_up);
   G.dwd = static_cast<uint16_t*>(dw_down);
   G.dag = reinterpret_cast<uint16_t*>(take(n * 4));
-  F.save_fmt = save_fmt == FT_SAVE_NONE ? (int)FT_SAVE_16 : save_fmt;
-  lay_saved(F, save_fmt == FT_SAVE_NONE ? take(n * 4) : saved);
+  F.save_fmt = save_fmt;
+  lay_saved(F, saved);
+  if (save_fmt == FT_SAVE_NONE) G.dh = reinterpret_cast<float*>(take(n * 4));
   if (x_scales) {
     uint16_t* x16 = reinterpret_cast<uint16_t*>(take((size_t)T * d * 2));
     if (int st = ft::launch_act8_unpack(static_cast<const uint8_t*>(x), x_scales, T, d, dtype == FT_T_FP16, x16, d, stream))
@@ -190,11 +191,6 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
     F.ldx = d;
   }
   F.part = reinterpret_cast<float*>(ws);
-  if (save_fmt == FT_SAVE_NONE && T > 0) {
-    ft::DenseFfn P = F;  // a and u alone
-    P.h = nullptr;
-    if (int st = ft::launch_gated_ffn(P, stream)) return st;
-  }
   return ft::launch_gated_ffn_bwd(F, G, stream);
 }
 

@@ -144,13 +144,12 @@ struct DenseFfn {
   const uint16_t *x, *wg, *wu, *wd;
   int64_t ldx;
   int T, d, d_ff, dtype, act;
-  // forward: null y computes a and u alone
   const void* res;
   int64_t ldr;
   void* y;
   int64_t ldy;
   int y_f32;
-  // a and u: 16 bits, or MX8 codes with their scales (sca, scu not null)
+  // a and u: 16 bits, or MX8 codes with their scales (sca, scu not null); null: not kept
   int save_fmt;
   void *sa, *su;
   uint8_t *sca, *scu;
@@ -166,6 +165,7 @@ struct DenseGrad {
   int64_t lddx;
   uint16_t *dwg, *dwu, *dwd;  // all or none
   uint16_t* dag;              // [T, 2 d_ff]: da, du
+  float* dh;                  // [T, d_ff], where a and u were not kept
 };
 int launch_gated_ffn(const DenseFfn& F, void* stream);
 int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream);

@@ -71,12 +71,17 @@ __device__ __forceinline__ float fit16(float v) {
 enum {
   kGateUp,  // A = x, B = 32 rows of Wg then 32 rows of Wu per wave; h, and a and u when kept
   kOut,     // C (+ residual) to 16 bits or fp32
-  kDh,      // dh = dy Wd, then h, da and du from a and u
+  kDh,      // dh = dy Wd, then h, da and du from a and u; or dh itself in fp32, where a and u were not kept
+  kAgain,   // as kGateUp, then h, da and du from a, u and that dh
   kDx,      // two pieces of k: da Wg + du Wu
   kDw       // A and B transposed; rows of C from `split` on go to a second matrix
 };
 
 constexpr int kUnits = 256;  // compute units
+
+// Modes that compute Wg and Wu side by side.
+template <int MODE>
+constexpr bool kBeside = MODE == kGateUp || MODE == kAgain;
 
 struct GemmArgs {
   const uint16_t *a, *b, *b2;  // b2: Wu (kGateUp: beside b; kDx: second piece of k)
@@ -88,7 +93,7 @@ struct GemmArgs {
   int split, c_f32;
   const void* res;
   int64_t ldr;
-  // kGateUp: where a and u go (null: not kept); kDh: where they come from
+  // kGateUp: where a and u go (null: not kept); kDh: where they come from (null: dh to c); kAgain: dh in c
   void *sa, *su;
   uint8_t *sca, *scu;  // MX8 scales, null for 16-bit a and u
   uint16_t *h, *dag;   // kDh outputs: h [M, N], da and du [M, 2N]
@@ -166,22 +171,69 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16_t& c0, 
         }
       }
     }
-    if (p.h) {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        uint32_t w[4];
+    for (int q = 0; q < 4; q += 2) {
+      uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int k = 4 * q + 2 * e;
-          w[e] = pack2<H>(act_f(c0[k], p.act) * c1[k], act_f(c0[k + 1], p.act) * c1[k + 1]);
-        }
-        swap_halves(w[0], w[2]);
-        swap_halves(w[1], w[3]);
-        const int n = nb + 8 * q + 8 * hi;
-        if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 4; ++e) {
+        const int k = 4 * q + 2 * e;
+        w[e] = pack2<H>(act_f(c0[k], p.act) * c1[k], act_f(c0[k + 1], p.act) * c1[k + 1]);
+      }
+      swap_halves(w[0], w[2]);
+      swap_halves(w[1], w[3]);
+      const int n = nb + 8 * q + 8 * hi;
+      if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else if constexpr (MODE == kAgain) {
+    const auto rd = rsrc_of(static_cast<const float*>(p.c) + (int64_t)mu * p.N);
+    float4 g[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = nb0 + 8 * q + 4 * hi;
+      const uint4 v = buf_ld16(rd, mok && n < p.N ? (uint32_t)(((m - mu) * p.N + n) * 4) : kOOB);
+      g[q] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      uint32_t oh[4], oa[4], ou[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 4 * q + 2 * e;
+        const float4 d = g[q + (e >> 1)];
+        const float d0 = e & 1 ? d.z : d.x, d1 = e & 1 ? d.w : d.y;
+        const ActD f0 = act_df(c0[k], p.act), f1 = act_df(c0[k + 1], p.act);
+        oh[e] = pack2<H>(f0.f * c1[k], f1.f * c1[k + 1]);
+        oa[e] = pack2<H>(d0 * c1[k] * f0.df, d1 * c1[k + 1] * f1.df);
+        ou[e] = pack2<H>(d0 * f0.f, d1 * f1.f);
+      }
+      swap_halves(oh[0], oh[2]);
+      swap_halves(oh[1], oh[3]);
+      swap_halves(oa[0], oa[2]);
+      swap_halves(oa[1], oa[3]);
+      swap_halves(ou[0], ou[2]);
+      swap_halves(ou[1], ou[3]);
+      const int n = nb0 + 8 * q + 8 * hi;
+      if (mok && n < p.N) {
+        *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        uint16_t* dg = p.dag + 2 * (int64_t)m * p.N + n;
+        *reinterpret_cast<uint4*>(dg) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+        *reinterpret_cast<uint4*>(dg + p.N) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
       }
     }
   } else if constexpr (MODE == kDh) {
+    if (!p.sa) {
+      float* c = static_cast<float*>(p.c) + (int64_t)m * p.N;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = (j ? nb1 : nb0) + 8 * q + 4 * hi;
+          const f32x16_t& r = j ? c1 : c0;
+          if (mok && n < p.N)
+            *reinterpret_cast<float4*>(c + n) = make_float4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+        }
+      return;
+    }
     // A result's a and u leave together, without a branch between (each waited for in its turn: the
     // backward pass of 8192 rows, d = 4096, d_ff = 2048, 716 against 709 us; those of both results at once
     // do not fit the registers).
@@ -367,7 +419,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
   const int s_begin = p.rest ? (lb - tile * p.blocks) * p.per : 0;
   const int s_end = p.rest ? min(stages, s_begin + p.per) : stages;
   const TilePos tp = tile_pos(p, tile);
-  const int m0 = tp.m * BM, n0 = tp.n * (MODE == kGateUp ? BN / 2 : BN);
+  const int m0 = tp.m * BM, n0 = tp.n * (kBeside<MODE> ? BN / 2 : BN);
 
   // ---- loads: per-lane byte offsets within the tile, from a base that moves with k ----
   uint32_t offA[LA], offB[LB];
@@ -391,7 +443,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
     const int q = (wave * LB + j) * 64 + lane;
     if constexpr (!BT) {
       const int r = q >> 3, pc = (q & 7) ^ ((r >> 1) & 7);
-      const int n = MODE == kGateUp ? (r >> 6) * 32 + (r & 31) : r;
+      const int n = kBeside<MODE> ? (r >> 6) * 32 + (r & 31) : r;
       kB[j] = pc * 8;
       offB[j] = n0 + n < p.N ? (uint32_t)(n * p.ldb * 2 + pc * 16) : kOOB;
     } else {
@@ -418,7 +470,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
 #pragma unroll
     for (int j = 0; j < LA; ++j)
       lds_load16(ra, kA[j] < left ? offA[j] : kOOB, 0, dst + (wave * LA + j) * 1024);
-    if constexpr (MODE == kGateUp) {
+    if constexpr (kBeside<MODE>) {
 #pragma unroll
       for (int j = 0; j < LB; ++j) {
         // 8 rows of one matrix: blocks of 32 rows alternate between Wg and Wu
@@ -488,7 +540,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM* WN / 4) void gemm_kernel(GemmArgs
     if (p.rest) {
       store_part(p.part + (size_t)lb * (BM * BN) + (wave * MT + i) * 2 * 1024, acc[i], lane);
     } else {
-      const int nb = n0 + wn * (MODE == kGateUp ? 32 : 64);
+      const int nb = n0 + wn * (kBeside<MODE> ? 32 : 64);
       const int m = m0 + wm * TM + i * 32;
       epilogue<MODE, H>(p, acc[i][0], acc[i][1], m, m + l31, nb, nb + 32, hi);
     }
@@ -508,7 +560,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_join_kernel(GemmArgs p) {
   f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
   for (int b = 0; b < p.blocks; ++b)
     add_part(acc, p.part + (size_t)(t * p.blocks + b) * (BM * BN) + (wave * MT + i) * 2 * 1024, lane);
-  const int nb = tp.n * (MODE == kGateUp ? BN / 2 : BN) + wn * (MODE == kGateUp ? 32 : 64);
+  const int nb = tp.n * (kBeside<MODE> ? BN / 2 : BN) + wn * (kBeside<MODE> ? 32 : 64);
   epilogue<MODE, H>(p, acc[0], acc[1], m, m + (lane & 31), nb, nb + 32, lane >> 5);
 }
 
@@ -572,7 +624,7 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
       at = end;
     }
     const TilePos tp = tile_pos(p, tile);
-    const int m0 = tp.m * 256, n0 = tp.n * (MODE == kGateUp ? 128 : 256);
+    const int m0 = tp.m * 256, n0 = tp.n * (kBeside<MODE> ? 128 : 256);
     // rows of a wave in the two halves: those past the end are neither read nor multiplied
     const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
 
@@ -592,7 +644,7 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
           offA[h][j] = m0 + h * 128 + pt * 8 < p.M ? (uint32_t)(kt * p.lda * 2 + pt * 16) : kOOB;
         else
           offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda * 2 + pk * 16) : kOOB;
-        const int nh = n0 + (MODE == kGateUp ? 0 : h * 128);
+        const int nh = n0 + (kBeside<MODE> ? 0 : h * 128);
         if constexpr (BT)
           offB[h][j] = nh + pt * 8 < p.N ? (uint32_t)(kt * p.ldb * 2 + pt * 16) : kOOB;
         else
@@ -610,8 +662,8 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
     };
     auto first_b = [&](int h) -> const uint8_t* {
       const bool two = MODE == kDx && s_begin >= per_seg;
-      const int k0 = (s_begin - (two ? per_seg : 0)) << 6, n = n0 + (MODE == kGateUp ? 0 : h * 128);
-      const uint16_t* b = two || (MODE == kGateUp && h) ? p.b2 : p.b;
+      const int k0 = (s_begin - (two ? per_seg : 0)) << 6, n = n0 + (kBeside<MODE> ? 0 : h * 128);
+      const uint16_t* b = two || (kBeside<MODE> && h) ? p.b2 : p.b;
       return reinterpret_cast<const uint8_t*>(BT ? b + k0 * p.ldb + n : b + n * p.ldb + k0);
     };
     const uint8_t *pa[2] = {first_a(0), first_a(1)}, *pb[2] = {first_b(0), first_b(1)};
@@ -763,7 +815,7 @@ __global__ __launch_bounds__(512) void gemm256_join_kernel(GemmArgs p) {
   if (m >= p.M) return;
   f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
   for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * kPartFloats + (wave * 4 + i) * 2048, lane);
-  const int nb = tp.n * (MODE == kGateUp ? 128 : 256) + wn * 32;
+  const int nb = tp.n * (kBeside<MODE> ? 128 : 256) + wn * 32;
   epilogue<MODE, H>(p, acc[0], acc[1], m, m + (lane & 31), nb, nb + 128, lane >> 5);
 }
 
@@ -980,7 +1032,7 @@ Cut cut_of(int64_t M, int64_t n, int stages) {
 
 template <int MODE, bool H>
 int gemm_go(GemmArgs& A, hipStream_t s) {
-  const int64_t n = MODE == kGateUp ? 2 * (int64_t)A.N : A.N;
+  const int64_t n = kBeside<MODE> ? 2 * (int64_t)A.N : A.N;
   const Cut c = cut_of(A.M, n, (MODE == kDx ? 2 : 1) * ((A.K + 63) / 64));
   A.tiles_m = c.tiles_m;
   A.tiles_n = c.tiles_n;
@@ -1092,7 +1144,7 @@ int launch_gated_ffn(const DenseFfn& F, void* stream) {
   A.sca = F.sca;
   A.scu = F.scu;
   int st = gemm_launch<kGateUp>(A, half, s);
-  if (st || !F.y) return st;
+  if (st) return st;
   GemmArgs D{};
   D.part = F.part;
   D.a = F.h;
@@ -1131,7 +1183,27 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
     A.scu = F.scu;
     A.h = F.h;
     A.dag = G.dag;
+    A.c = G.dh;
     if ((st = gemm_launch<kDh>(A, half, s))) return st;
+    if (!F.sa) {
+      // a and u again, in fp32 where they are used: rounded to 16 bits on the way they would double
+      // the gradients' error
+      GemmArgs B{};
+      B.part = F.part;
+      B.a = F.x;
+      B.lda = F.ldx;
+      B.b = F.wg;
+      B.b2 = F.wu;
+      B.ldb = F.d;
+      B.M = F.T;
+      B.N = F.d_ff;
+      B.K = F.d;
+      B.act = F.act;
+      B.c = G.dh;
+      B.h = F.h;
+      B.dag = G.dag;
+      if ((st = gemm_launch<kAgain>(B, half, s))) return st;
+    }
   }
   if (G.dwd) {
     GemmArgs A{};
