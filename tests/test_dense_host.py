@@ -1,11 +1,14 @@
 """Refusals of the dense operators (no GPU: every check comes before a launch), and pins of the
 plain forms their GPU tests compare against."""
 import math
+import os
+import re
+import subprocess
 
 import pytest
 import torch
 
-from moe_expert_offload_amd import ft
+from moe_expert_offload_amd import build, ft
 from tests import dense_ref as R
 
 A = 1 << 20  # an aligned address; nothing below reaches a launch
@@ -186,3 +189,29 @@ def test_mx8_rule():
     assert R.e4m3_points()[126] == 448 and R.e4m3_points()[8] == 2.0 ** -6
     pts = torch.arange(126, dtype=torch.uint8)
     assert torch.equal(pts.view(torch.float8_e4m3fn).double(), R.e4m3_points()[:126])
+
+
+# ---- generated code --------------------------------------------------------------------
+
+def test_hand_issued_loads_write_lds(tmp_path):
+    """The tiled products load straight into LDS with inline-asm loads and count their waits by hand:
+    whatever else the compiler issues only makes such a wait stricter, but an inline-asm load into a
+    register could be copied before its data lands.  There is none."""
+    if not os.path.exists(build.HIPCC):
+        pytest.skip("hipcc not available")
+    out = tmp_path / "dense.s"
+    cmd = [build.HIPCC, f"--offload-arch={build.ARCH}", "--cuda-device-only", "-S", "-O3", "-std=c++17",
+           f"-I{os.path.join(build.PKG, '..', 'include')}", "-o", str(out),
+           os.path.join(build.CSRC, "kernels_dense.hip")] + build.DEVICE_FLAGS
+    subprocess.run(cmd, check=True, capture_output=True, timeout=600)
+    src = out.read_text()
+    seen = 0
+    for name, body in re.findall(r"^(_Z\w*gemm(?:256)?_kernel\w*):[^\n]*\n(.*?); -- End function", src, re.S | re.M):
+        blocks = re.findall(r";;#ASMSTART\n(.*?);;#ASMEND", body, re.S)
+        loads = [v.strip() for b in blocks for v in b.split("\n") if re.match(r"\s*(buffer|global|flat|scratch)_load", v)]
+        assert loads and all(v.endswith(" lds") for v in loads), name
+        if "gemm256" in name:
+            # entry, and two a stage, in the whole and the ragged walk
+            assert sum("s_waitcnt vmcnt(8)" in b for b in blocks) == 5, name
+        seen += 1
+    assert seen == 24  # 6 modes, 2 types, 2 tile sizes

@@ -214,6 +214,35 @@ def test_backward_with_shared_tiles(T, d, f, t):
         R.check(g, want[k], k)
 
 
+def test_offsets_past_32_bits():
+    """x, y, dy and dx of more than 2^31 elements: rows beyond that place, of the outputs and as the only
+    ones that the weights' gradients see."""
+    torch = torch_mod()
+    T, d, f, n = 270000, 8192, 8, 100
+    assert T * d > 2 ** 31 and (T - n) * d > 2 ** 31
+    b = Block(n, d, f, "bf16", "silu", seed=13)
+    x = torch.zeros((T, d), dtype=b.dt, device="cuda")
+    dy = torch.zeros((T, d), dtype=b.dt, device="cuda")
+    x[-n:], dy[-n:] = b.x, b.dy
+    want = R.ffn(*b.exact(), "silu", b.dt)["y"]
+    A, U = (R.mm(R.exactly(b.x), R.t_(R.exactly(w))) for w in (b.wg, b.wu))
+    grads = R.ffn_bwd(*b.exact(), A, U, R.exactly(b.dy), "silu", b.dt)
+    small = b.dy
+    b.T, b.x, b.dy = T, x, dy
+    y, _ = b.forward()
+    torch.cuda.synchronize()
+    R.check(y[-n:], want, "y")
+    assert not y[:-n].any()
+    del y
+    got = b.backward(None, "none")
+    torch.cuda.synchronize()
+    R.check(got[0][-n:], grads["dx"], "dx")
+    assert not got[0][:-n].any()
+    for g, k in zip(got[1:], ("dwg", "dwu", "dwd")):
+        R.check(g, grads[k], k)
+    del small
+
+
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 def test_gradients_against_differences(kind):
     """The gradients against central differences of the plain forward in 64 bits, along random
@@ -419,6 +448,10 @@ W4 = [
     (40, 160, 9000, 32, True, "bf16", "fp32", False),
     (16, 4096, 64, 32, True, "bf16", "fp32", False),    # the most of x that LDS holds
     (11, 8224, 24, 32, False, "fp16", "fp32", False),   # more than that
+    (16, 40960, 20, 32, True, "bf16", "fp32", False),   # the most of scales that LDS holds
+    (64, 40960, 18, 32, True, "fp16", "fp32", False),
+    (3, 65536, 20, 32, True, "bf16", "fp32", False),    # more than that
+    (5, 64, 40, 64, True, "bf16", "fp32", False),       # one group a row
 ]
 
 
