@@ -581,15 +581,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_join_kernel(GemmArgs p) {
 // and -1.  It is waited for by both groups at least one barrier before its first read, and has six
 // sections to arrive.  Loads past the last stage are masked (they write zeros nobody reads), which keeps
 // the counts of the waits.  (Four steps of a quarter each, with 8 MFMAs a section, took 4 % longer.)
-constexpr int kPartFloats = 256 * 256;  // of a 256 x 256 tile
-
-template <int MODE, bool H>
+// MH: halves of A's rows, 2 as above or 1 (tiles of 128 x 256 for fewer rows: a stage is one step of A0, B0
+// and B1, three stages lie in LDS, and the loads of stage s + 2 go where stage s - 1 was read).
+template <int MODE, bool H, int MH>
 __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
   constexpr bool AT = MODE == kDw;
   constexpr bool BT = MODE == kDh || MODE == kDx || MODE == kDw;
   constexpr int REG = 16384;
-  enum { A0 = 0, B0 = REG, B1 = 2 * REG, A1 = 3 * REG, STAGE = 4 * REG };
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[2 * STAGE];
+  enum { A0 = 0, B0 = REG, B1 = 2 * REG, A1 = 3 * REG, STAGE = (2 + MH) * REG, PLACES = MH == 2 ? 2 : 3 };
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[PLACES * STAGE];
+  constexpr int BM = 128 * MH, PART = BM * 256;  // rows of a tile, floats of its sums
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -624,12 +625,12 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
       at = end;
     }
     const TilePos tp = tile_pos(p, tile);
-    const int m0 = tp.m * 256, n0 = tp.n * (kBeside<MODE> ? 128 : 256);
+    const int m0 = tp.m * BM, n0 = tp.n * (kBeside<MODE> ? 128 : 256);
     // rows of a wave in the two halves: those past the end are neither read nor multiplied
     const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
 
     // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
-    uint32_t offA[2][2], offB[2][2];  // [half][chunk]
+    uint32_t offA[MH][2], offB[2][2];  // [half][chunk]
     int kA[2], kB[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -639,11 +640,14 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
       kA[j] = AT ? kt : pk * 8;
       kB[j] = BT ? kt : pk * 8;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < MH; ++h) {
         if constexpr (AT)
           offA[h][j] = m0 + h * 128 + pt * 8 < p.M ? (uint32_t)(kt * p.lda * 2 + pt * 16) : kOOB;
         else
           offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda * 2 + pk * 16) : kOOB;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         const int nh = n0 + (kBeside<MODE> ? 0 : h * 128);
         if constexpr (BT)
           offB[h][j] = nh + pt * 8 < p.N ? (uint32_t)(kt * p.ldb * 2 + pt * 16) : kOOB;
@@ -671,21 +675,21 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
       if (s >= s_end) return 0;
       return p.K - ((MODE == kDx && s >= per_seg ? s - per_seg : s) << 6);
     };
-    auto load_a = [&](int s, int h) {
+    auto load_a = [&](int s, int h, int place) {
       if (MODE == kDx && s == per_seg && s != s_begin)
         pa[h] = reinterpret_cast<const uint8_t*>(p.a + p.K + (m0 + h * 128) * p.lda);
       const int left = k_left(s);
       const auto rs = rsrc_of(pa[h]);
-      const uint32_t dst = sm0 + ((s - s_begin) & 1) * STAGE + (h ? A1 : A0);
+      const uint32_t dst = sm0 + place * STAGE + (h ? A1 : A0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) lds_load16(rs, kA[j] < left ? offA[h][j] : kOOB, 0, dst + j * 1024);
       pa[h] += step_a;
     };
-    auto load_b = [&](int s, int h) {
+    auto load_b = [&](int s, int h, int place) {
       if (MODE == kDx && s == per_seg && s != s_begin) pb[h] = reinterpret_cast<const uint8_t*>(p.b2 + n0 + h * 128);
       const int left = k_left(s);
       const auto rs = rsrc_of(pb[h]);
-      const uint32_t dst = sm0 + ((s - s_begin) & 1) * STAGE + (h ? B1 : B0);
+      const uint32_t dst = sm0 + place * STAGE + (h ? B1 : B0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) lds_load16(rs, kB[j] < left ? offB[h][j] : kOOB, 0, dst + j * 1024);
       pb[h] += step_b;
@@ -704,9 +708,9 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
       return i32x4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
     };
 
-    f32x16_t acc[4][2];  // [2 half + 32-row piece][half of the columns]
+    f32x16_t acc[2 * MH][2];  // [2 half + 32-row piece][half of the columns]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
+    for (int i = 0; i < 2 * MH; ++i) acc[i][0] = acc[i][1] = f32x16_t{};
     i32x4_t fa[2][4], fb0[4], fb1[4];
 
     auto read_a = [&](const uint8_t* base) {
@@ -742,42 +746,56 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
     auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
 
     if (s_begin < s_end) {
-      load_a(s_begin, 0);
-      load_b(s_begin, 0);
-      load_b(s_begin, 1);
-      load_a(s_begin, 1);
-      load_a(s_begin + 1, 0);
-      load_b(s_begin + 1, 0);
-      load_b(s_begin + 1, 1);
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the first stage
+      load_a(s_begin, 0, 0);
+      load_b(s_begin, 0, 0);
+      load_b(s_begin, 1, 0);
+      if constexpr (MH == 2) load_a(s_begin, 1, 0);
+      load_a(s_begin + 1, 0, 1);
+      load_b(s_begin + 1, 0, 1);
+      load_b(s_begin + 1, 1, 1);
+      constexpr int WAIT = MH == 2 ? 8 : 6;
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(WAIT) : "memory");  // A0, B0 and B1 of the first stage
       meet();
       if (wm) meet();
       // RAGGED: the tile has rows past the end.  Asking at every step would cost a whole tile 4 %.
       auto walk = [&](auto ragged) {
         constexpr bool RAGGED = decltype(ragged)::value;
+        int here = 0;
         for (int s = s_begin; s < s_end; ++s) {
-          const uint8_t* st = sm + ((s - s_begin) & 1) * STAGE;
+          const uint8_t* st = sm + here * STAGE;
+          const int other = here == 0 ? PLACES - 1 : here - 1;
           if (!RAGGED || any[0]) read_a(st + A0);
           read_b(st + B0, fb0);
           read_b(st + B1, fb1);
-          load_a(s + 1, 1);
-          reads_done();
-          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
+          if constexpr (MH == 2) {
+            load_a(s + 1, 1, other);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
+          } else {
+            load_a(s + 2, 0, other);
+            load_b(s + 2, 0, other);
+            load_b(s + 2, 1, other);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(6)" ::: "memory");  // the next stage
+          }
           meet();
           if (!RAGGED || any[0]) multiply(0);
           meet();
-          if (!RAGGED || any[1]) read_a(st + A1);
-          load_a(s + 2, 0);
-          load_b(s + 2, 0);
-          load_b(s + 2, 1);
-          reads_done();
-          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
-          meet();
-          if (!RAGGED || any[1]) multiply(1);
-          meet();
+          if constexpr (MH == 2) {
+            if (!RAGGED || any[1]) read_a(st + A1);
+            load_a(s + 2, 0, here);
+            load_b(s + 2, 0, here);
+            load_b(s + 2, 1, here);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
+            meet();
+            if (!RAGGED || any[1]) multiply(1);
+            meet();
+          }
+          here = here == PLACES - 1 ? 0 : here + 1;
         }
       };
-      if (m0 + 192 < p.M)
+      if (m0 + BM - 64 < p.M)
         walk(std::false_type{});
       else
         walk(std::true_type{});
@@ -787,10 +805,10 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
     }
 
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * MH; ++i) {
       if (slot >= 0) {
         if (m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32 < p.M)
-          store_part(p.part + (size_t)slot * kPartFloats + (wave * 4 + i) * 2048, acc[i], lane);
+          store_part(p.part + (size_t)slot * PART + (wave * 2 * MH + i) * 2048, acc[i], lane);
       } else {
         const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
         const int nb = n0 + wn * 32;
@@ -802,19 +820,19 @@ __global__ __launch_bounds__(512, 2) void gemm256_kernel(GemmArgs p) {
 
 // The tiles whose stages several blocks shared: their sums, always added in the order of k, then the
 // epilogue.  A block per tile and 32-row piece of the waves; bound by memory (256 KB a part and tile).
-template <int MODE, bool H>
+template <int MODE, bool H, int MH>
 __global__ __launch_bounds__(512) void gemm256_join_kernel(GemmArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x & 3, t = blockIdx.x >> 2;
+  const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x % (2 * MH), t = blockIdx.x / (2 * MH);
   const int stages = (MODE == kDx ? 2 : 1) * ((p.K + 63) >> 6);
   const int g = t / p.group, from = (t - g * p.group) * stages;
   const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
   if (first == last) return;  // one block had it all
   const TilePos tp = tile_pos(p, p.whole + t);
-  const int m = tp.m * 256 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+  const int m = tp.m * 128 * MH + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
   if (m >= p.M) return;
   f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
-  for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * kPartFloats + (wave * 4 + i) * 2048, lane);
+  for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * (MH * 128 * 256) + (wave * 2 * MH + i) * 2048, lane);
   const int nb = tp.n * (kBeside<MODE> ? 128 : 256) + wn * 32;
   epilogue<MODE, H>(p, acc[0], acc[1], m, m + (lane & 31), nb, nb + 128, lane >> 5);
 }
@@ -959,50 +977,60 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
 
 // How a product is cut.  `n` columns count gate and up apart.
 struct Cut {
-  int tile;  // 256 or 128
+  int tile;  // 256: 256 x 256; 384: 128 x 256; 128: 128 x 128
   int tiles_m, tiles_n, whole, rest, group, blocks, per, parts;
   size_t part_bytes;
 };
 
-// Tiles of 256 run one to a compute unit, tiles of 128 two; both in rounds that cost their fullest
-// unit's time, and the last round of 256 may share its tiles.  Counted in stages of the 256 tiles, 1.3 us
-// each when the whole chip runs them:
-//   a round of 256 tiles: the stages + 12 (first loads, epilogue);
-//   a round of up to 512 tiles of 128: the stages + 6 (M = 1021, N = 5632, K = 2048: 48 us), of up to 256: half
-//   the stages + 5 (M = 1021, N = 2048, K = 11264: 124 us);
-//   joining: 256 KB written and read for each piece, 0.07 a piece + 4 (a quarter of it for 128, + 6).
+// Tiles of 256 columns run one to a compute unit, tiles of 128 x 128 two; both in rounds that cost their
+// fullest unit's time, and the last round may share its tiles.  Counted in stages of the 256 x 256 tiles,
+// 1.3 us each when the whole chip runs them:
+//   a round of 256 x 256 tiles: the stages + 12 (first loads, epilogue); of 128 x 256 tiles: 0.62 of the
+//   stages + 9 (M = 1021, N = 5632, K = 2048: 48 us, by 128 x 128 tiles 57);
+//   a round of up to 512 tiles of 128 x 128: the stages + 6, of up to 256: half the stages + 5 (M = 1021, N = 2048,
+//   K = 11264: 124 us);
+//   joining: what a piece writes and the join reads, 0.07 for 256 KB, + 4 (+ 16 behind whole rounds, + 6 for 128 x 128).
 // Sharing cuts groups of tiles alike (all into 2 .. 16 parts, or 2 tiles into 3, or 3 into 4), so that blocks
 // at the same place of their groups still walk k in step: cutting one line of all tiles into equal
 // pieces left M = 2053, N = 4096, K = 11008 at 235 us, as slow as not sharing.
 Cut cut_of(int64_t M, int64_t n, int stages) {
   Cut c{};
-  c.tile = 256;
-  c.tiles_m = (int)((M + 255) / 256);
-  c.tiles_n = (int)((n + 255) / 256);
-  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  c.whole = (int)tiles;
-  double cost = (double)(tiles / kUnits) * (stages + 12);
-  const int rest = (int)(tiles % kUnits);
-  if (rest) {
-    double best = stages + 12;
-    auto offer = [&](int group, int blocks) {
-      const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
-      if (groups * blocks > kUnits || per < 4 || per >= stages) return;
-      const double t = per + 12 + 0.07 * (groups * blocks + rest) + 4;
-      if (t >= best) return;
-      best = t;
-      c.rest = rest;
-      c.whole = (int)tiles - rest;
-      c.group = group;
-      c.blocks = blocks;
-      c.per = per;
-      c.parts = groups * blocks;
-      c.part_bytes = (size_t)(c.parts + rest) * kPartFloats * 4;
-    };
-    for (int k = 2; k <= 16; ++k) offer(1, k);
-    offer(2, 3);
-    offer(3, 4);
-    cost += best;
+  double cost = 1e30;
+  for (int mh = 2; mh >= 1; --mh) {
+    Cut d{};
+    d.tile = mh == 2 ? 256 : 384;
+    d.tiles_m = (int)((M + 128 * mh - 1) / (128 * mh));
+    d.tiles_n = (int)((n + 255) / 256);
+    const int64_t tiles = (int64_t)d.tiles_m * d.tiles_n;
+    d.whole = (int)tiles;
+    const double stage = mh == 2 ? 1.0 : 0.62, fixed = mh == 2 ? 12 : 9, piece = mh == 2 ? 0.07 : 0.035;
+    double t = (double)(tiles / kUnits) * (stage * stages + fixed);
+    const int rest = (int)(tiles % kUnits);
+    if (rest) {
+      double best = stage * stages + fixed;
+      auto offer = [&](int group, int blocks) {
+        const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
+        if (groups * blocks > kUnits || per < 4 || per >= stages) return;
+        const double u = stage * per + fixed + piece * (groups * blocks + rest) + (tiles > kUnits ? 16 : 4);
+        if (u >= best) return;
+        best = u;
+        d.rest = rest;
+        d.whole = (int)tiles - rest;
+        d.group = group;
+        d.blocks = blocks;
+        d.per = per;
+        d.parts = groups * blocks;
+        d.part_bytes = (size_t)(d.parts + rest) * mh * 128 * 256 * 4;
+      };
+      for (int k = 2; k <= 16; ++k) offer(1, k);
+      offer(2, 3);
+      offer(3, 4);
+      t += best;
+    }
+    if (t < cost) {
+      cost = t;
+      c = d;
+    }
   }
   // 128: whole tiles, or all of them cut alike
   const int tm = (int)((M + 127) / 128), tn = (int)((n + 127) / 128);
@@ -1045,8 +1073,11 @@ int gemm_go(GemmArgs& A, hipStream_t s) {
   if (A.tiles_m == 0 || A.tiles_n == 0) return FT_OK;
   if ((int64_t)A.tiles_m * A.tiles_n > 0x7ffffff) return fail(FT_EINVAL, "gated_ffn: too many tiles");
   if (c.tile == 256) {
-    hipLaunchKernelGGL((gemm256_kernel<MODE, H>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
-    if (c.rest) hipLaunchKernelGGL((gemm256_join_kernel<MODE, H>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
+    hipLaunchKernelGGL((gemm256_kernel<MODE, H, 2>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((gemm256_join_kernel<MODE, H, 2>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
+  } else if (c.tile == 384) {
+    hipLaunchKernelGGL((gemm256_kernel<MODE, H, 1>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((gemm256_join_kernel<MODE, H, 1>), dim3((unsigned)c.rest * 2), dim3(512), 0, s, A);
   } else {
     hipLaunchKernelGGL((gemm_kernel<MODE, H, 128, 128, 2, 2>), dim3((unsigned)c.parts), dim3(256), 0, s, A);
     if (c.rest)

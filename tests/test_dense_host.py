@@ -210,8 +210,10 @@ def test_hand_issued_loads_write_lds(tmp_path):
         blocks = re.findall(r";;#ASMSTART\n(.*?);;#ASMEND", body, re.S)
         loads = [v.strip() for b in blocks for v in b.split("\n") if re.match(r"\s*(buffer|global|flat|scratch)_load", v)]
         assert loads and all(v.endswith(" lds") for v in loads), name
-        if "gemm256" in name:
-            # entry, and two a stage, in the whole and the ragged walk
+        # on entry, and in the whole and the ragged walk twice a stage (256 rows) or once (128 rows)
+        if "gemm256" in name and "ELi2EE" in name:
             assert sum("s_waitcnt vmcnt(8)" in b for b in blocks) == 5, name
+        elif "gemm256" in name:
+            assert sum("s_waitcnt vmcnt(6)" in b for b in blocks) == 3, name
         seen += 1
-    assert seen == 24  # 6 modes, 2 types, 2 tile sizes
+    assert seen == 36  # 6 modes, 2 types, 3 tile sizes

@@ -196,8 +196,8 @@ def test_forward_with_shared_tiles(T, d, f, t, res):
 
 
 @pytest.mark.parametrize("T,d,f,t", [
-    (1021, 2048, 5632, "fp16"),  # dx's few tiles into eight parts, across the two weights
-    (8200, 2048, 4096, "bf16"),  # dw_down's tiles into two
+    (1021, 2048, 5632, "fp16"),  # dx's few tiles into four parts, across the two weights
+    (8200, 2048, 4096, "bf16"),  # ragged rows' tiles into four and sixteen, behind whole ones
 ])
 def test_backward_with_shared_tiles(T, d, f, t):
     torch = torch_mod()
