@@ -97,7 +97,8 @@ __device__ __forceinline__ ActD act_df(float z, int act) {
     r.df = s * (1.0f + z * (1.0f - s));
   } else {
     // with s = 1/(1 + e^-2w): f = z s, f' = s + z s (1 - s) (2w)'
-    const float zz = z * z;
+    // (past |z| = 10^5 s is 0 or 1 and s (1 - s) is 0: a square past fp32 would make that NaN)
+    const float zz = fminf(z * z, 1e10f);
     const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-1.5957691216057308f * (z + 0.044715f * z * zz)));
     r.f = z * s;
     r.df = s + z * (s * (1.0f - s)) * (1.5957691216057308f * (1.0f + 0.134145f * zz));

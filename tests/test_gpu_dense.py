@@ -363,6 +363,37 @@ def test_extreme_gates():
             R.check(g, want[k], k)
 
 
+def test_largest_gates():
+    """Gates up to the type's end, whose squares and cubes pass fp32: the activation is z or 0 and its
+    slope 1 or 0 there, the same for both kinds, kept or computed again."""
+    torch = torch_mod()
+    T, d, f = 70, 32, 96
+    out = {}
+    for kind in ("silu", "gelu"):
+        b = Block(T, d, f, "bf16", kind, seed=8)
+        b.wg.copy_(torch.eye(d).repeat(f // d, 1))
+        b.wu.copy_(b.wu * 2.0 ** -60)
+        top = torch.exp2(torch.randint(8, 128, (T, d), generator=b.g).float())
+        b.x.copy_(torch.where(torch.rand(T, d, generator=b.g) < 0.5, top, -top))
+        A, u = b.x.repeat(1, f // d), b.rnd(T, f, std=2.0 ** -60)
+        saved = torch.cat([v.contiguous().view(torch.uint8).flatten() for v in (A, u)])
+        got = b.backward(saved, "16"), b.backward(None, "none", want_dw=False)
+        torch.cuda.synchronize()
+        on = R.exactly((A > 0).to(b.dt))
+        x, wg, wu, wd = b.exact()
+        dh = R.mm(R.exactly(b.dy), wd)
+        for g, U in zip(got, (R.exactly(u), R.mm(x, R.t_(wu)))):
+            da = R.rounded(R.mul(R.mul(dh, U), on), b.dt)
+            du = R.rounded(R.mul(R.mul(dh, R.exactly(A)), on), b.dt)
+            v, e = R.add(R.mm(da, wg), R.mm(du, wu))
+            e = e + (f + 1) * R.F32 * (da[0].abs() @ wg[0].abs() + du[0].abs() @ wu[0].abs())
+            R.check(g[0], R.rounded((v, e), b.dt), f"dx {kind}")
+        # not dw_up = du^T x: du reaches 2^126 and x 2^127, so that its sums pass fp32 and are NaN by rights
+        out[kind] = [got[0][0], got[0][1], got[0][3], got[1][0]]
+    for p, q in zip(out["silu"], out["gelu"]):
+        assert torch.isfinite(p).all() and torch.equal(p, q)
+
+
 # ---- 8-bit activations --------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,n,t", [(1, 32, "bf16"), (3, 32, "fp16"), (257, 96, "bf16"), (5, 4096, "fp16"),
