@@ -463,8 +463,10 @@ typedef struct {
 
 /* y = x w^T (+ residual): x `dtype` [T, K] (bf16 or fp16), y [T, N] and residual (may
  * be NULL) of y_dtype, `dtype` or FT_T_FP32.  Weights are applied as the exact
- * integers code - zero, scaled per group in fp32; fp32 sums.  The decode form: the
- * weights stream once per 64 tokens; T >= 0.  ldy and ldr are any strides >= N, and y and
+ * integers code - zero, scaled per group in fp32; fp32 sums.  They go through the products as
+ * 16 + code and -(16 + zero): an infinity in a row of x makes that row of y NaN, and so
+ * may finite x whose sum of 31 |x| over a group passes fp32.  The decode form: the
+ * weights stream once per 64 tokens; 0 <= T <= 4194240.  ldy and ldr are any strides >= N, and y and
  * residual need their element's alignment only. */
 int ft_w4_gemv(const void* x, int64_t ldx, int32_t T, int32_t dtype, const ft_w4_matrix* w,
                const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
