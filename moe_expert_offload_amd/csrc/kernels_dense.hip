@@ -1199,7 +1199,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   int st;
   if (F.T > 0) {
     GemmArgs A{};
-  A.part = F.part;
+    A.part = F.part;
     A.a = G.dy;
     A.lda = G.lddy;
     A.b = F.wd;
@@ -1238,7 +1238,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   }
   if (G.dwd) {
     GemmArgs A{};
-  A.part = F.part;
+    A.part = F.part;
     A.a = G.dy;
     A.lda = G.lddy;
     A.b = F.h;
@@ -1267,7 +1267,7 @@ int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream) {
   }
   if (G.dx && F.T > 0) {
     GemmArgs A{};
-  A.part = F.part;
+    A.part = F.part;
     A.a = G.dag;
     A.lda = 2 * (int64_t)F.d_ff;
     A.b = F.wg;
