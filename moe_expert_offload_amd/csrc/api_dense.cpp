@@ -2,6 +2,7 @@
 // for the contract of each call; the kernels are in kernels_dense.hip and kernels_w4.hip.
 #include <string>
 
+#include "dense_cut.h"
 #include "internal.h"
 
 using ft::fail;

@@ -154,10 +154,8 @@ struct DenseFfn {
   void *sa, *su;
   uint8_t *sca, *scu;
   uint16_t* h;  // [T, d_ff]
-  float* part;  // gated_ffn_part_bytes
+  float* part;  // gated_ffn_part_bytes (dense_cut.h)
 };
-// Workspace for the sums of tiles that several blocks share (0 where none are).
-size_t gated_ffn_part_bytes(int T, int d, int d_ff, bool backward);
 struct DenseGrad {
   const uint16_t* dy;
   int64_t lddy;

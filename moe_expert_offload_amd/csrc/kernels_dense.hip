@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "dense_common.h"
+#include "dense_cut.h"
 
 namespace ft {
 
@@ -76,8 +77,6 @@ enum {
   kDx,      // two pieces of k: da Wg + du Wu
   kDw       // A and B transposed; rows of C from `split` on go to a second matrix
 };
-
-constexpr int kUnits = 256;  // compute units
 
 // Modes that compute Wg and Wu side by side.
 template <int MODE>
@@ -975,89 +974,6 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
 
 // ---- launches -------------------------------------------------------------------------
 
-// How a product is cut.  `n` columns count gate and up apart.
-struct Cut {
-  int tile;  // 256: 256 x 256; 384: 128 x 256; 128: 128 x 128
-  int tiles_m, tiles_n, whole, rest, group, blocks, per, parts;
-  size_t part_bytes;
-};
-
-// Tiles of 256 columns run one to a compute unit, tiles of 128 x 128 two; both in rounds that cost their
-// fullest unit's time, and the last round may share its tiles.  Counted in stages of the 256 x 256 tiles,
-// 1.3 us each when the whole chip runs them:
-//   a round of 256 x 256 tiles: the stages + 12 (first loads, epilogue); of 128 x 256 tiles: 0.62 of the
-//   stages + 9 (M = 1021, N = 5632, K = 2048: 48 us, by 128 x 128 tiles 57);
-//   a round of up to 512 tiles of 128 x 128: the stages + 6, of up to 256: half the stages + 5 (M = 1021, N = 2048,
-//   K = 11264: 124 us);
-//   joining: what a piece writes and the join reads, 0.07 for 256 KB, + 4 (+ 16 behind whole rounds, + 6 for 128 x 128).
-// Sharing cuts groups of tiles alike (all into 2 .. 16 parts, or 2 tiles into 3, or 3 into 4), so that blocks
-// at the same place of their groups still walk k in step: cutting one line of all tiles into equal
-// pieces left M = 2053, N = 4096, K = 11008 at 235 us, as slow as not sharing.
-Cut cut_of(int64_t M, int64_t n, int stages) {
-  Cut c{};
-  double cost = 1e30;
-  for (int mh = 2; mh >= 1; --mh) {
-    Cut d{};
-    d.tile = mh == 2 ? 256 : 384;
-    d.tiles_m = (int)((M + 128 * mh - 1) / (128 * mh));
-    d.tiles_n = (int)((n + 255) / 256);
-    const int64_t tiles = (int64_t)d.tiles_m * d.tiles_n;
-    d.whole = (int)tiles;
-    const double stage = mh == 2 ? 1.0 : 0.62, fixed = mh == 2 ? 12 : 9, piece = mh == 2 ? 0.07 : 0.035;
-    double t = (double)(tiles / kUnits) * (stage * stages + fixed);
-    const int rest = (int)(tiles % kUnits);
-    if (rest) {
-      double best = stage * stages + fixed;
-      auto offer = [&](int group, int blocks) {
-        const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
-        if (groups * blocks > kUnits || per < 4 || per >= stages) return;
-        const double u = stage * per + fixed + piece * (groups * blocks + rest) + (tiles > kUnits ? 16 : 4);
-        if (u >= best) return;
-        best = u;
-        d.rest = rest;
-        d.whole = (int)tiles - rest;
-        d.group = group;
-        d.blocks = blocks;
-        d.per = per;
-        d.parts = groups * blocks;
-        d.part_bytes = (size_t)(d.parts + rest) * mh * 128 * 256 * 4;
-      };
-      for (int k = 2; k <= 16; ++k) offer(1, k);
-      offer(2, 3);
-      offer(3, 4);
-      t += best;
-    }
-    if (t < cost) {
-      cost = t;
-      c = d;
-    }
-  }
-  // 128: whole tiles, or all of them cut alike
-  const int tm = (int)((M + 127) / 128), tn = (int)((n + 127) / 128);
-  const int64_t t128 = (int64_t)tm * tn;
-  for (int k = 1; k <= 16; ++k) {
-    const int64_t nb = t128 * k, last = nb % (2 * kUnits);
-    const int per = (stages + k - 1) / k;
-    if (k > 1 && (nb > 2 * kUnits || per < 2)) break;
-    double t = (double)(nb / (2 * kUnits)) * (per + 6) + (last == 0 ? 0.0 : last > kUnits ? per + 6 : 0.52 * per + 5);
-    if (k > 1) t += 0.0175 * (double)(nb + t128) + 6;
-    if (t >= cost) continue;
-    cost = t;
-    c = Cut{};
-    c.tile = 128;
-    c.tiles_m = tm;
-    c.tiles_n = tn;
-    c.whole = c.parts = (int)nb;
-    c.blocks = k;
-    c.per = per;
-    if (k > 1) {
-      c.rest = (int)t128;
-      c.part_bytes = (size_t)nb * 128 * 128 * 4;
-    }
-  }
-  return c;
-}
-
 template <int MODE, bool H>
 int gemm_go(GemmArgs& A, hipStream_t s) {
   const int64_t n = kBeside<MODE> ? 2 * (int64_t)A.N : A.N;
@@ -1106,26 +1022,6 @@ int skinny_go(SkinnyArgs& A, hipStream_t s) {
 }
 
 }  // namespace
-
-// Rows up to which the weights stream once (skinny_kernel); beyond, tiles.
-constexpr int kSkinnyRows = 64;
-
-// The most that the pieces of the calls below take.
-size_t gated_ffn_part_bytes(int T, int d, int d_ff, bool backward) {
-  auto one = [](int64_t M, int64_t n, int64_t K, int segs) { return cut_of(M, n, (int)(segs * ((K + 63) / 64))).part_bytes; };
-  size_t m = 0;
-  auto up = [&](size_t v) { m = v > m ? v : m; };
-  up(one(T, 2 * (int64_t)d_ff, d, 1));
-  if (!backward) {
-    up(one(T, d, d_ff, 1));
-  } else {
-    up(one(T, d_ff, d, 1));
-    up(one(d, d_ff, T, 1));
-    up(one(2 * (int64_t)d_ff, d, T, 1));
-    up(one(T, d, d_ff, 2));
-  }
-  return m;
-}
 
 int launch_gated_ffn(const DenseFfn& F, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
