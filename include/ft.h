@@ -381,8 +381,10 @@ int ft_host_experts(const void* x, int32_t T, int32_t d, int32_t d_ff, int32_t f
  * may be captured into a HIP graph (a workspace then belongs to that graph's replays
  * alone).  No output may overlap an input, another output or the workspace, except a
  * residual given as the output itself (same pointer and stride).  A workspace is
- * 256-byte aligned; FT_ENOMEM when smaller than its size query says (0 from a query:
- * bad sizes).  Results do not depend on timing: equal calls give equal bits.
+ * 256-byte aligned.  Its size query (0: bad sizes) never falls with T: a workspace for T
+ * rows serves every call of up to T rows with the other arguments the same.  FT_ENOMEM
+ * when smaller than the call needs, which may be less than the query says.
+ * Results do not depend on timing: equal calls give equal bits.
  * Values that are not finite pass through the sums as IEEE arithmetic has it. */
 typedef enum { FT_T_BF16 = 0, FT_T_FP16 = 1, FT_T_FP32 = 2 } ft_dtype;
 typedef enum { FT_ACT_SILU = 0, FT_ACT_GELU_TANH = 1 } ft_act;

@@ -36,6 +36,15 @@ int check_block(const char* fn, int32_t T, int32_t d, int32_t d_ff, int32_t dtyp
   return FT_OK;
 }
 
+// Bytes of a block's workspace, with `parts` bytes for the sums of shared tiles.
+size_t ffn_bytes(int32_t T, int32_t d_ff, size_t parts) { return align256((size_t)T * d_ff * 2) + parts + 256; }
+size_t ffn_bwd_bytes(int32_t T, int32_t d, int32_t d_ff, int32_t save_fmt, bool x_mx8, size_t parts) {
+  size_t n = align256((size_t)T * d_ff * 2) + align256((size_t)T * d_ff * 4);  // h; da and du
+  if (save_fmt == FT_SAVE_NONE) n += align256((size_t)T * d_ff * 4);           // dh
+  if (x_mx8) n += align256((size_t)T * d * 2);                                 // x
+  return n + parts + 256;
+}
+
 // Points a block at the parts of its saved buffer.
 void lay_saved(ft::DenseFfn& F, const void* saved) {
   uint8_t* p = static_cast<uint8_t*>(const_cast<void*>(saved));
@@ -81,7 +90,7 @@ extern "C" {
 
 size_t ft_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t d_ff) {
   if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8)) return 0;
-  return align256((size_t)T * d_ff * 2) + ft::gated_ffn_part_bytes(T, d, d_ff, false) + 256;
+  return ffn_bytes(T, d_ff, ft::gated_ffn_part_bound(T, d, d_ff, false));
 }
 
 size_t ft_gated_ffn_saved_bytes(int32_t T, int32_t d_ff, int32_t save_fmt) {
@@ -101,7 +110,9 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
   if (int st = check_io("gated_ffn", x, ldx, d, residual, ldr, y, ldy, d, dtype, y_dtype, 16)) return st;
   if (save_fmt != FT_SAVE_NONE && (!saved || misaligned(saved, 16))) return fail(FT_EINVAL, "gated_ffn: bad saved buffer");
   if (!workspace || misaligned(workspace, 256)) return fail(FT_EINVAL, "gated_ffn: need a 256-byte aligned workspace");
-  if (workspace_bytes < ft_gated_ffn_workspace_bytes(T, d, d_ff)) return fail(FT_ENOMEM, "gated_ffn: workspace too small");
+  const bool tiles = !ft::gated_ffn_streams(T, save_fmt);
+  if (workspace_bytes < ffn_bytes(T, d_ff, tiles ? ft::gated_ffn_part_bytes(T, d, d_ff, false) : 0))
+    return fail(FT_ENOMEM, "gated_ffn: workspace too small");
   ft::DenseFfn F{};
   F.x = static_cast<const uint16_t*>(x);
   F.ldx = ldx;
@@ -127,10 +138,7 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
 
 size_t ft_gated_ffn_bwd_workspace_bytes(int32_t T, int32_t d, int32_t d_ff, int32_t save_fmt, int32_t x_mx8) {
   if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8) || save_fmt < FT_SAVE_NONE || save_fmt > FT_SAVE_MX8) return 0;
-  size_t n = align256((size_t)T * d_ff * 2) + align256((size_t)T * d_ff * 4);  // h; da and du
-  if (save_fmt == FT_SAVE_NONE) n += align256((size_t)T * d_ff * 4);           // dh
-  if (x_mx8) n += align256((size_t)T * d * 2);                                 // x
-  return n + ft::gated_ffn_part_bytes(T, d, d_ff, true) + 256;
+  return ffn_bwd_bytes(T, d, d_ff, save_fmt, x_mx8 != 0, ft::gated_ffn_part_bound(T, d, d_ff, true));
 }
 
 int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_t T, int32_t d, int32_t d_ff,
@@ -150,7 +158,8 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
     if (save_fmt != FT_SAVE_NONE && (!saved || misaligned(saved, 16))) return fail(FT_EINVAL, "gated_ffn_bwd: bad saved buffer");
   }
   if (!workspace || misaligned(workspace, 256)) return fail(FT_EINVAL, "gated_ffn_bwd: need a 256-byte aligned workspace");
-  if (workspace_bytes < ft_gated_ffn_bwd_workspace_bytes(T, d, d_ff, save_fmt, x_scales != nullptr))
+  if (workspace_bytes <
+      ffn_bwd_bytes(T, d, d_ff, save_fmt, x_scales != nullptr, ft::gated_ffn_part_bytes(T, d, d_ff, true)))
     return fail(FT_ENOMEM, "gated_ffn_bwd: workspace too small");
   if (!dx && !dw_gate) return FT_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

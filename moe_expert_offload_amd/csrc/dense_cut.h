@@ -5,12 +5,15 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/ft.h"
+
 namespace ft {
 
 constexpr int kUnits = 256;  // compute units
 
 // Rows up to which the weights stream once (skinny_kernel); beyond, tiles.
 constexpr int kSkinnyRows = 64;
+inline bool gated_ffn_streams(int64_t T, int save_fmt) { return T <= kSkinnyRows && save_fmt == FT_SAVE_NONE; }
 
 // How a product is cut.  `n` columns count gate and up apart.
 struct Cut {
@@ -95,8 +98,8 @@ inline Cut cut_of(int64_t M, int64_t n, int stages) {
   return c;
 }
 
-// The most that the pieces of the calls below take.
-inline size_t gated_ffn_part_bytes(int T, int d, int d_ff, bool backward) {
+// What the pieces' sums of a call of T rows take in its tiled form.
+inline size_t gated_ffn_part_bytes(int64_t T, int d, int d_ff, bool backward) {
   auto one = [](int64_t M, int64_t n, int64_t K, int segs) { return cut_of(M, n, (int)(segs * ((K + 63) / 64))).part_bytes; };
   size_t m = 0;
   auto up = [&](size_t v) { m = v > m ? v : m; };
@@ -108,6 +111,20 @@ inline size_t gated_ffn_part_bytes(int T, int d, int d_ff, bool backward) {
     up(one(d, d_ff, T, 1));
     up(one(2 * (int64_t)d_ff, d, T, 1));
     up(one(T, d, d_ff, 2));
+  }
+  return m;
+}
+
+// The most of that over 1 .. T rows, so that a workspace for the largest batch serves every smaller one.  Rows
+// count by tiles of 128 and, where k runs over them, by stages of 64: every 64th number stands for all (60 us for
+// 8192 rows).  Past 16384 rows: what no cut passes, a slot of 256 KB for each unit's piece and each shared tile
+// (128 x 128 tiles: 2 kUnits pieces of 64 KB).
+inline size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward) {
+  if (T > 16384) return (size_t)2 * kUnits * (256 << 10);
+  size_t m = 0;
+  for (int64_t t = 64; t < T + 64; t += 64) {
+    const size_t v = gated_ffn_part_bytes(t, d, d_ff, backward);
+    m = v > m ? v : m;
   }
   return m;
 }

@@ -1027,7 +1027,7 @@ int launch_gated_ffn(const DenseFfn& F, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool half = F.dtype == FT_T_FP16;
   if (F.T <= 0) return FT_OK;
-  if (F.T <= kSkinnyRows && F.save_fmt == FT_SAVE_NONE) {
+  if (gated_ffn_streams(F.T, F.save_fmt)) {
     SkinnyArgs A{};
     A.x = F.x;
     A.ldx = F.ldx;

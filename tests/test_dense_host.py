@@ -137,6 +137,24 @@ def test_w4_gated_ffn_refuses():
     _fails(ft.FT_ENOMEM, ft.ft_w4_gated_ffn, **{**a, "workspace_bytes": need - 1})
 
 
+# rows at the ends of tiles, of stages and of rounds of tiles, and in between
+ROWS = (1, 2, 16, 17, 63, 64, 65, 127, 128, 129, 192, 193, 256, 300, 512, 640, 700, 1000, 1021, 1024, 1300, 2048, 2053, 2816,
+        4096, 4100, 4416, 4928, 5000, 7616, 8192, 8200, 11072, 16383, 16384, 16385, 20000, 65536, 270000)
+
+
+@pytest.mark.parametrize("d,f", [(4096, 2048), (2048, 768), (4096, 11008), (2048, 5632), (8192, 8), (256, 512), (64, 96)])
+def test_a_workspace_serves_fewer_rows(d, f):
+    """No size falls as the rows grow: a buffer for the largest batch is large enough for each smaller one."""
+    sizes = [lambda T: ft.ft_gated_ffn_workspace_bytes(T, d, f)]
+    if f % 32 == 0:
+        sizes.append(lambda T: ft.ft_w4_gated_ffn_workspace_bytes(T, f))
+    sizes += [lambda T, s=s, x=x: ft.ft_gated_ffn_bwd_workspace_bytes(T, d, f, s, x)
+              for s in (ft.FT_SAVE_NONE, ft.FT_SAVE_16, ft.FT_SAVE_MX8) for x in (False, True)]
+    for size in sizes:
+        got = [size(T) for T in ROWS]
+        assert all(0 < a <= b for a, b in zip(got, got[1:])), [(T, n) for T, n in zip(ROWS, got)]
+
+
 # ---- the plain forms themselves --------------------------------------------------------
 
 def test_plain_backward_is_autograd():
