@@ -441,10 +441,13 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
  * 2^e, stored as e + 127, with the least e >= -127 such that its largest finite
  * magnitude is at most 448 * 2^e: nothing saturates, and an element is off by at most
  * 2^-4 of itself (or 2^(e - 10)).  Rounding to nearest even; infinities and NaN become
- * NaN and leave the block's scale to the others; a block of zeros has scale byte 0.  (The MXFP8
- * conversion of the experts' prefill form takes its exponent from the largest
- * element alone and clamps.)  Unpacking is exact in bf16 and rounds in fp16, where
- * magnitudes past 65504 become 65504. */
+ * NaN and leave the block's scale to the others; a block of zeros has scale byte 0, and no
+ * scale byte is past 247.  (The MXFP8 conversion of the experts' prefill form takes its
+ * exponent from the largest element alone and clamps.)  Unpacking rounds to nearest even:
+ * in bf16 it is exact for magnitudes from 2^-126 on and below 2^128 (that value, which
+ * magnitudes from 1.9375 * 2^127 on are packed to, becomes infinite); in fp16 magnitudes
+ * past 65504 become 65504.  ft_gated_ffn_bwd takes MX8 a and u past fp32's largest value,
+ * and MX8 x past its type's, as that value. */
 int ft_act8_pack(const void* src, int64_t ld, int32_t rows, int32_t n, int32_t dtype,
                  uint8_t* codes, uint8_t* scales, void* stream);
 int ft_act8_unpack(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t n,

@@ -195,7 +195,7 @@ int ft_gated_ffn_bwd(const void* x, int64_t ldx, const uint8_t* x_scales, int32_
   if (save_fmt == FT_SAVE_NONE) G.dh = reinterpret_cast<float*>(take(n * 4));
   if (x_scales) {
     uint16_t* x16 = reinterpret_cast<uint16_t*>(take((size_t)T * d * 2));
-    if (int st = ft::launch_act8_unpack(static_cast<const uint8_t*>(x), x_scales, T, d, dtype == FT_T_FP16, x16, d, stream))
+    if (int st = ft::launch_act8_unpack(static_cast<const uint8_t*>(x), x_scales, T, d, dtype == FT_T_FP16, true, x16, d, stream))
       return st;
     F.x = x16;
     F.ldx = d;
@@ -223,7 +223,7 @@ int ft_act8_unpack(const uint8_t* codes, const uint8_t* scales, int32_t rows, in
   if (bad_ld(ld, n)) return fail(FT_EINVAL, "act8_unpack: bad row stride");
   if (!codes || !scales || !dst || misaligned(codes, 16) || misaligned(dst, 16))
     return fail(FT_EINVAL, "act8_unpack: null or unaligned pointer");
-  return ft::launch_act8_unpack(codes, scales, rows, n, dtype == FT_T_FP16, static_cast<uint16_t*>(dst), ld, stream);
+  return ft::launch_act8_unpack(codes, scales, rows, n, dtype == FT_T_FP16, false, static_cast<uint16_t*>(dst), ld, stream);
 }
 
 int ft_w4_gemv(const void* x, int64_t ldx, int32_t T, int32_t dtype, const ft_w4_matrix* w, const void* residual,

@@ -169,8 +169,9 @@ int launch_gated_ffn(const DenseFfn& F, void* stream);
 int launch_gated_ffn_bwd(const DenseFfn& F, const DenseGrad& G, void* stream);
 int launch_act8_pack(const uint16_t* src, int64_t ld, int rows, int n, bool half, uint8_t* codes, uint8_t* scales,
                      void* stream);
-int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, uint16_t* dst,
-                       int64_t ld, void* stream);
+// fit: bf16 values past its end become its largest, as fp16's always do.
+int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, bool fit,
+                       uint16_t* dst, int64_t ld, void* stream);
 
 // ---- products with 4-bit weights (kernels_w4.hip) ----------------------------------
 struct W4Args {

@@ -45,12 +45,18 @@ __device__ __forceinline__ void mx8_values4(uint32_t c, int sc, float* v) {
   v[1] = ldexpf(a.y, k);
   v[2] = ldexpf(b.x, k);
   v[3] = ldexpf(b.y, k);
+  if (sc > 246) {
+    // past fp32 (from 1.9375 * 2^127 on a finite value is packed to 2^128): its largest value, not an infinity,
+    // whose slope would be NaN
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v[e] > 0x1.fffffep127f ? 0x1.fffffep127f : (v[e] < -0x1.fffffep127f ? -0x1.fffffep127f : v[e]);
+  }
 }
-// fp16 holds less than a code times its scale may be: the largest finite value stands for more.
+// A 16-bit type holds less than a code times its scale may be: its largest finite value stands for more.
 template <bool H>
 __device__ __forceinline__ float fit16(float v) {
-  if constexpr (H) return v > 65504.0f ? 65504.0f : (v < -65504.0f ? -65504.0f : v);
-  return v;
+  constexpr float top = H ? 65504.0f : 0x1.fep127f;
+  return v > top ? top : (v < -top ? -top : v);
 }
 
 // ---- the tiled product ----------------------------------------------------------------
@@ -950,7 +956,8 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const uint16_t* src, int
     if ((c & 1) == 0) scales[row * (n / 32) + c / 2] = (uint8_t)sc;
   }
 }
-template <bool H>
+// FIT: values past the type's end become its largest (fp16 always, bf16 for a backward pass); else infinities.
+template <bool H, bool FIT>
 __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int n,
                                                           uint16_t* dst, int64_t ld) {
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -965,7 +972,8 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, 
     mx8_values4(v.w, sc, f + 12);
     uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = pack2<H>(fit16<H>(f[2 * e]), fit16<H>(f[2 * e + 1]));
+    for (int e = 0; e < 8; ++e)
+      w[e] = FIT ? pack2<H>(fit16<H>(f[2 * e]), fit16<H>(f[2 * e + 1])) : pack2<H>(f[2 * e], f[2 * e + 1]);
     uint4* q = reinterpret_cast<uint4*>(dst + row * ld + c * 16);
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     q[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -1196,15 +1204,17 @@ int launch_act8_pack(const uint16_t* src, int64_t ld, int rows, int n, bool half
     hipLaunchKernelGGL(act8_pack_kernel<false>, g, b, 0, s, src, ld, rows, n, codes, scales);
   return launched("act8_pack_kernel");
 }
-int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, uint16_t* dst,
-                       int64_t ld, void* stream) {
+int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, bool fit,
+                       uint16_t* dst, int64_t ld, void* stream) {
   if (rows <= 0) return FT_OK;
   const dim3 b = act8_block(n), g((unsigned)((rows + b.y - 1) / b.y));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (half)
-    hipLaunchKernelGGL(act8_unpack_kernel<true>, g, b, 0, s, codes, scales, rows, n, dst, ld);
+    hipLaunchKernelGGL((act8_unpack_kernel<true, true>), g, b, 0, s, codes, scales, rows, n, dst, ld);
+  else if (fit)
+    hipLaunchKernelGGL((act8_unpack_kernel<false, true>), g, b, 0, s, codes, scales, rows, n, dst, ld);
   else
-    hipLaunchKernelGGL(act8_unpack_kernel<false>, g, b, 0, s, codes, scales, rows, n, dst, ld);
+    hipLaunchKernelGGL((act8_unpack_kernel<false, false>), g, b, 0, s, codes, scales, rows, n, dst, ld);
   return launched("act8_unpack_kernel");
 }
 

@@ -2,6 +2,7 @@
 import pytest
 
 from moe_expert_offload_amd import ft
+from tests import dense_ref as R
 from tests.gpu_helpers import torch_mod
 from tests.test_gpu_dense import ACT, FT, SAVE, Block, _say
 
@@ -54,3 +55,65 @@ def test_few_rows_need_no_more_than_h():
         ft.ft_gated_ffn(b.x, d, T, d, f, FT[t], ACT["silu"], b.wg, b.wu, b.wd, None, d, y2, d, FT[t], saved, ft.FT_SAVE_16,
                         ws, n)
     assert e.value.status == ft.FT_ENOMEM
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward_from_the_largest_mx8_values(kind):
+    """A finite a, u or x next to the type's end is packed to 2^128, which fp32 does not hold: the backward pass takes
+    the largest value there (slope 1 or 0 of both activations), not an infinity whose slope is NaN."""
+    torch = torch_mod()
+    T, d, f = 70, 32, 96
+    b = Block(T, d, f, "bf16", kind, seed=23)
+    b.dy.copy_(b.rnd(T, d, std=2.0 ** -40))
+    # the whole way: the largest a's as the forward call packs them
+    top = torch.finfo(torch.bfloat16).max
+    x0 = torch.zeros(T, d)
+    x0[:, 0] = torch.where(torch.rand(T, generator=b.g) < 0.5, top, -top)
+    x0[:, 1] = 1.0
+    b.x.copy_(x0)
+    b.wg.zero_()
+    b.wg[:, 0] = 1.0
+    b.wu.zero_()
+    b.wu[:, 1] = b.rnd(f, std=2.0 ** -60)
+    _, saved = b.forward("mx8")
+    c, s = b.split8(saved)
+    torch.cuda.synchronize()
+    A, U = (R.mx8_values(ci, si) for ci, si in zip(c, s))
+    assert (A.abs() == 2.0 ** 128).all()
+    A = A.clamp(-torch.finfo(torch.float32).max, torch.finfo(torch.float32).max)
+    b.wu.copy_(b.rnd(f, d, std=d ** -0.5))
+    b.x.copy_(b.rnd(T, d))
+    got = b.backward(saved, "mx8")
+    torch.cuda.synchronize()
+    zero = lambda v: (v, torch.zeros_like(v))  # noqa: E731
+    on = zero((A > 0).double())
+    x, wg, wu, wd = b.exact()
+    dy = R.exactly(b.dy)
+    dh = R.mm(dy, wd)
+    h = R.rounded(R.mul(R.mul(zero(A), on), zero(U)), b.dt)
+    da = R.rounded(R.mul(R.mul(dh, zero(U)), on), b.dt)
+    du = R.rounded(R.mul(R.mul(dh, zero(A)), on), b.dt)
+    v, e = R.add(R.mm(da, wg), R.mm(du, wu))
+    e = e + (f + 1) * R.F32 * (da[0].abs() @ wg[0].abs() + du[0].abs() @ wu[0].abs())
+    R.check(got[0], R.rounded((v, e), b.dt), "dx")
+    for g, w, k in zip(got[1:], (R.mm(R.t_(da), x), R.mm(R.t_(du), x), R.mm(R.t_(dy), h)), ("dwg", "dwu", "dwd")):
+        R.check(g, R.rounded(w, b.dt), k)
+
+
+def test_backward_from_the_largest_mx8_x():
+    torch = torch_mod()
+    T, d, f = 70, 64, 96
+    b = Block(T, d, f, "bf16", "silu", seed=24)
+    b.dy.copy_(b.rnd(T, d, std=2.0 ** -40))
+    _, saved = b.forward("16")
+    pick = torch.tensor([120, 248, 126, 254, 56, 3, 0], dtype=torch.uint8)  # +-256, +-448, 1, 3 * 2^-9, 0
+    xc = pick[torch.randint(0, 7, (T, d), generator=b.g)].cuda()
+    xs = torch.full((T, d // 32), 247, dtype=torch.uint8, device="cuda")
+    got = b.backward(saved, "16", xc, xs)
+    torch.cuda.synchronize()
+    top = torch.finfo(torch.bfloat16).max
+    X = R.mx8_values(xc, xs).clamp(-top, top)
+    A, U = (R.exactly(v) for v in b.split16(saved))
+    want = R.ffn_bwd((X, torch.zeros_like(X)), *b.exact()[1:], A, U, R.exactly(b.dy), "silu", b.dt)
+    for g, k in zip(got, ("dx", "dwg", "dwu", "dwd")):
+        R.check(g, want[k], k)
