@@ -931,10 +931,13 @@ __global__ __launch_bounds__(64 * W) void skinny_kernel(SkinnyArgs p) {
 // ---- 8-bit activations --------------------------------------------------------------
 // One thread per 16 elements (half a block of 32): 32 bytes in, 16 out, the block's largest by one
 // exchange with its neighbour; bound by memory (8192 x 4096: 18 us, 5.6 TB/s; unpacking 20 us, 5.1 TB/s).
+__device__ __forceinline__ int64_t act8_row() {
+  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+}
 template <bool H>
 __global__ __launch_bounds__(256) void act8_pack_kernel(const uint16_t* src, int64_t ld, int rows, int n,
                                                         uint8_t* codes, uint8_t* scales) {
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t row = act8_row();
   if (row >= rows) return;  // a row's two halves of a block always stay together
   for (int c = threadIdx.x; c < n / 16; c += blockDim.x) {
     const uint4* q = reinterpret_cast<const uint4*>(src + row * ld + c * 16);
@@ -960,7 +963,7 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const uint16_t* src, int
 template <bool H, bool FIT>
 __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int n,
                                                           uint16_t* dst, int64_t ld) {
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t row = act8_row();
   if (row >= rows) return;
   for (int c = threadIdx.x; c < n / 16; c += blockDim.x) {
     const uint4 v = *reinterpret_cast<const uint4*>(codes + row * n + c * 16);
@@ -1192,11 +1195,16 @@ static dim3 act8_block(int n) {
   while (x < 256 && (int)x < n / 16) x *= 2;
   return dim3(x, 256 / x);
 }
+// Blocks for `rows` in two dimensions: a grid's first one holds fewer than 2^32 threads.
+static dim3 act8_grid(int rows, unsigned per) {
+  const unsigned n = ((unsigned)rows + per - 1) / per, x = n < 65536 ? n : 65536;
+  return dim3(x, (n + x - 1) / x);
+}
 
 int launch_act8_pack(const uint16_t* src, int64_t ld, int rows, int n, bool half, uint8_t* codes, uint8_t* scales,
                      void* stream) {
   if (rows <= 0) return FT_OK;
-  const dim3 b = act8_block(n), g((unsigned)((rows + b.y - 1) / b.y));
+  const dim3 b = act8_block(n), g = act8_grid(rows, b.y);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (half)
     hipLaunchKernelGGL(act8_pack_kernel<true>, g, b, 0, s, src, ld, rows, n, codes, scales);
@@ -1207,7 +1215,7 @@ int launch_act8_pack(const uint16_t* src, int64_t ld, int rows, int n, bool half
 int launch_act8_unpack(const uint8_t* codes, const uint8_t* scales, int rows, int n, bool half, bool fit,
                        uint16_t* dst, int64_t ld, void* stream) {
   if (rows <= 0) return FT_OK;
-  const dim3 b = act8_block(n), g((unsigned)((rows + b.y - 1) / b.y));
+  const dim3 b = act8_block(n), g = act8_grid(rows, b.y);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (half)
     hipLaunchKernelGGL((act8_unpack_kernel<true, true>), g, b, 0, s, codes, scales, rows, n, dst, ld);

@@ -117,3 +117,28 @@ def test_backward_from_the_largest_mx8_x():
     want = R.ffn_bwd((X, torch.zeros_like(X)), *b.exact()[1:], A, U, R.exactly(b.dy), "silu", b.dt)
     for g, k in zip(got, ("dx", "dwg", "dwu", "dwd")):
         R.check(g, want[k], k)
+
+
+@pytest.mark.parametrize("n", [32, 96])
+def test_act8_of_many_rows(n):
+    """More blocks than the first dimension of a grid takes: every row is packed and unpacked once, the last ones too."""
+    torch = torch_mod()
+    rows = 65536 * 128 * 2 + 77
+    src = torch.randint(-448, 449, (rows, n), device="cuda", dtype=torch.int16).to(torch.bfloat16)
+    codes = torch.empty((rows + 1, n), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((rows + 1, n // 32), dtype=torch.uint8, device="cuda")
+    out = torch.empty((rows + 1, n), dtype=torch.bfloat16, device="cuda")
+    codes[-1], scales[-1], out[-1] = 33, 44, 55
+    ft.ft_act8_pack(src, n, rows, n, FT["bf16"], codes, scales)
+    ft.ft_act8_unpack(codes, scales, rows, n, FT["bf16"], out, n)
+    torch.cuda.synchronize()
+    assert (codes[-1] == 33).all() and (scales[-1] == 44).all() and (out[-1] == 55).all()
+    for at in (0, 65536 * 128 - 1, 65536 * 128, rows - 300):
+        wc, ws = R.mx8_pack(src[at:at + 300].cpu().double())
+        m = wc.shape[0]
+        assert torch.equal(codes[at:at + m].cpu(), wc) and torch.equal(scales[at:at + m].cpu(), ws)
+    # every row: off by half a step of its own at most (2^-4), zeros as zeros
+    for at in range(0, rows, 1 << 20):
+        v, w = src[at:min(at + (1 << 20), rows)].float(), out[at:min(at + (1 << 20), rows)].float()
+        e = torch.exp2(scales[at:min(at + (1 << 20), rows)].float() - 127 - 10).repeat_interleave(32, 1)
+        assert ((w - v).abs() <= torch.maximum(v.abs() * 2.0 ** -4, e)).all()
