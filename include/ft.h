@@ -396,7 +396,7 @@ typedef enum { FT_SAVE_NONE = 0, FT_SAVE_16 = 1, FT_SAVE_MX8 = 2 } ft_save;
  * holds them one after the other); all of `dtype` (bf16 or fp16).  y [T, d] and
  * residual (may be NULL) of y_dtype: `dtype` or FT_T_FP32.  Sums, the activation and the
  * residual's addition are fp32; h is rounded to `dtype` between the two products.
- * d, d_ff multiples of 8; T >= 0, any number of rows (from one token on).
+ * d, d_ff multiples of 8 up to 2^20; T from 0 to 2^31 - 512 rows.
  * save_fmt keeps a and u for ft_gated_ffn_bwd in `saved`
  * (ft_gated_ffn_saved_bytes bytes):
  *   FT_SAVE_NONE  nothing (saved may be NULL)
@@ -458,7 +458,7 @@ int ft_act8_unpack(const uint8_t* codes, const uint8_t* scales, int32_t rows, in
  * codes: uint8 [N, K / 2], unsigned codes 0..15, the lower k in the low nibble;
  * scales: [N, K / group] of the activations' dtype; zeros: uint8 [N, K / group], 0..15
  * (larger values are undefined), or NULL for 8 everywhere.  group 32, 64 or 128;
- * K % group == 0; any N.  scales need 2-byte alignment, zeros none. */
+ * K % group == 0, K up to 2^20; N up to 2^27 - 16.  scales need 2-byte alignment, zeros none. */
 typedef struct {
   const uint8_t* codes;
   const void* scales;

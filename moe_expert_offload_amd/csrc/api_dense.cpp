@@ -13,6 +13,9 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 constexpr int64_t kMaxLd = 1 << 21;  // a tile's rows stay inside 32-bit byte offsets
+// Rows whose tiles' ends, stages and grids (512 threads a tile of 256) stay inside 32 bits.
+constexpr int32_t kMaxRows = 0x7fffffff - 511;
+bool bad_rows(int32_t T) { return T < 0 || T > kMaxRows; }
 
 bool bad_ld(int64_t ld, int64_t n) { return ld < n || ld > kMaxLd || (ld & 7); }
 
@@ -25,7 +28,7 @@ bool bad_width(int32_t n, int32_t m) { return n <= 0 || n % m || n > kMaxLd / 2;
 int check_block(const char* fn, int32_t T, int32_t d, int32_t d_ff, int32_t dtype, int32_t act, const void* wg,
                 const void* wu, const void* wd, int32_t save_fmt) {
   const std::string f(fn);
-  if (T < 0) return fail(FT_EINVAL, f + ": T must be >= 0");
+  if (bad_rows(T)) return fail(FT_EINVAL, f + ": T must be 0 .. 2^31 - 512");
   if (bad_width(d, 8) || bad_width(d_ff, 8)) return fail(FT_EINVAL, f + ": d and d_ff must be multiples of 8 up to 2^20");
   if (!is16(dtype)) return fail(FT_EINVAL, f + ": dtype must be bf16 or fp16");
   if (!is_act(act)) return fail(FT_EINVAL, f + ": unknown activation");
@@ -60,11 +63,15 @@ void lay_saved(ft::DenseFfn& F, const void* saved) {
   }
 }
 
+// A grid of 512 threads for 16 rows has fewer than 2^32.
+constexpr int32_t kMaxW4Rows = (1 << 27) - 16;
+
 int check_w4(const char* fn, const ft_w4_matrix* w) {
   const std::string f(fn);
   if (!w || !w->codes || !w->scales) return fail(FT_EINVAL, f + ": null weights");
   if (w->group != 32 && w->group != 64 && w->group != 128) return fail(FT_EINVAL, f + ": group must be 32, 64 or 128");
-  if (w->N <= 0 || bad_width(w->K, w->group)) return fail(FT_EINVAL, f + ": need N > 0 and K a multiple of the group, up to 2^20");
+  if (w->N <= 0 || w->N > kMaxW4Rows) return fail(FT_EINVAL, f + ": N must be 1 .. 2^27 - 16");
+  if (bad_width(w->K, w->group)) return fail(FT_EINVAL, f + ": K must be a multiple of the group, up to 2^20");
   if (misaligned(w->codes, 16) || misaligned(w->scales, 2)) return fail(FT_EINVAL, f + ": unaligned weights");
   return FT_OK;
 }
@@ -89,12 +96,12 @@ int check_io(const std::string& f, const void* x, int64_t ldx, int64_t K, const 
 extern "C" {
 
 size_t ft_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t d_ff) {
-  if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8)) return 0;
+  if (bad_rows(T) || bad_width(d, 8) || bad_width(d_ff, 8)) return 0;
   return ffn_bytes(T, d_ff, ft::gated_ffn_part_bound(T, d, d_ff, false));
 }
 
 size_t ft_gated_ffn_saved_bytes(int32_t T, int32_t d_ff, int32_t save_fmt) {
-  if (T < 0 || bad_width(d_ff, 8)) return 0;
+  if (bad_rows(T) || bad_width(d_ff, 8)) return 0;
   const size_t n = (size_t)T * d_ff;
   if (save_fmt == FT_SAVE_16) return 4 * n;
   if (save_fmt == FT_SAVE_MX8 && d_ff % 32 == 0) return 2 * (n + n / 32);
@@ -137,7 +144,7 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
 }
 
 size_t ft_gated_ffn_bwd_workspace_bytes(int32_t T, int32_t d, int32_t d_ff, int32_t save_fmt, int32_t x_mx8) {
-  if (T < 0 || bad_width(d, 8) || bad_width(d_ff, 8) || save_fmt < FT_SAVE_NONE || save_fmt > FT_SAVE_MX8) return 0;
+  if (bad_rows(T) || bad_width(d, 8) || bad_width(d_ff, 8) || save_fmt < FT_SAVE_NONE || save_fmt > FT_SAVE_MX8) return 0;
   return ffn_bwd_bytes(T, d, d_ff, save_fmt, x_mx8 != 0, ft::gated_ffn_part_bound(T, d, d_ff, true));
 }
 

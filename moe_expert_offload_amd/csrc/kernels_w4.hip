@@ -315,7 +315,7 @@ int w4_group(const W4Args& A, hipStream_t s) {
 
 int launch_w4(const W4Args& A, bool gate_up, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if ((int64_t)(A.T + 63) / 64 > 65535) return fail(FT_EINVAL, "w4: more than 4194240 tokens");
+  if (A.T > 65535 * 64) return fail(FT_EINVAL, "w4: more than 4194240 tokens");
   if (gate_up) return A.half ? w4_group<true, true>(A, s) : w4_group<true, false>(A, s);
   return A.half ? w4_group<false, true>(A, s) : w4_group<false, false>(A, s);
 }

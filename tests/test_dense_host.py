@@ -137,6 +137,25 @@ def test_w4_gated_ffn_refuses():
     _fails(ft.FT_ENOMEM, ft.ft_w4_gated_ffn, **{**a, "workspace_bytes": need - 1})
 
 
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 511, 2 ** 31 - 64])
+def test_rows_past_32_bits_are_refused(T):
+    """Row counts whose sums with a tile's size pass 32 bits."""
+    assert ft.ft_gated_ffn_workspace_bytes(T, 64, 96) == 0 and ft.ft_gated_ffn_saved_bytes(T, 96, ft.FT_SAVE_16) == 0
+    assert ft.ft_gated_ffn_bwd_workspace_bytes(T, 64, 96, ft.FT_SAVE_16, False) == 0
+    _fails(ft.FT_EINVAL, ft.ft_gated_ffn, **_ffn(T=T))
+    _fails(ft.FT_EINVAL, ft.ft_gated_ffn_bwd, **_bwd(T=T))
+    _fails(ft.FT_EINVAL, ft.ft_w4_gemv, A, 64, T, ft.FT_T_BF16, _m(), None, 24, A, 24, ft.FT_T_BF16)
+    up, down = _m(N=96, K=64), _m(N=64, K=96)
+    _fails(ft.FT_EINVAL, ft.ft_w4_gated_ffn, A, 64, T, ft.FT_T_BF16, ft.FT_ACT_SILU, up, up, down, None, 64, A, 64,
+           ft.FT_T_BF16, A, BIG)
+
+
+def test_w4_limits():
+    _fails(ft.FT_EINVAL, ft.ft_w4_gemv, A, 64, 65535 * 64 + 1, ft.FT_T_BF16, _m(), None, 24, A, 24, ft.FT_T_BF16)
+    n = 2 ** 27 - 15  # a grid of 2^32 threads
+    _fails(ft.FT_EINVAL, ft.ft_w4_gemv, A, 64, 1, ft.FT_T_BF16, _m(N=n), None, n, A, n, ft.FT_T_BF16)
+
+
 # rows at the ends of tiles, of stages and of rounds of tiles, and in between
 ROWS = (1, 2, 16, 17, 63, 64, 65, 127, 128, 129, 192, 193, 256, 300, 512, 640, 700, 1000, 1021, 1024, 1300, 2048, 2053, 2816,
         4096, 4100, 4416, 4928, 5000, 7616, 8192, 8200, 11072, 16383, 16384, 16385, 20000, 65536, 270000)
