@@ -477,9 +477,10 @@ int ft_w4_gemv(const void* x, int64_t ldx, int32_t T, int32_t dtype, const ft_w4
                const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
                void* stream);
 
-/* The gated block of ft_gated_ffn on 4-bit weights: gate and up [d_ff, d], down
- * [d, d_ff], one group size or several.  h is rounded to `dtype` between the products.
- * workspace: ft_w4_gated_ffn_workspace_bytes(T, d_ff). */
+/* The gated block of ft_gated_ffn on 4-bit weights: gate and up [d_ff, d] with one
+ * group size, down [d, d_ff] with that or another.  h is rounded to `dtype` between the
+ * products; an h that is not finite (fp16: past 65504) makes its row of y NaN.  T as for
+ * ft_w4_gemv.  workspace: ft_w4_gated_ffn_workspace_bytes(T, d_ff). */
 size_t ft_w4_gated_ffn_workspace_bytes(int32_t T, int32_t d_ff);
 int ft_w4_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_t act,
                     const ft_w4_matrix* gate, const ft_w4_matrix* up, const ft_w4_matrix* down,
