@@ -395,7 +395,8 @@ typedef enum { FT_SAVE_NONE = 0, FT_SAVE_16 = 1, FT_SAVE_MX8 = 2 } ft_save;
  * x [T, d]; w_gate, w_up [d_ff, d]; w_down [d, d_ff] (contiguous; a bf16 expert record
  * holds them one after the other); all of `dtype` (bf16 or fp16).  y [T, d] and
  * residual (may be NULL) of y_dtype: `dtype` or FT_T_FP32.  Sums, the activation and the
- * residual's addition are fp32; h is rounded to `dtype` between the two products.
+ * residual's addition are fp32; h is rounded to `dtype` between the two products, whatever
+ * y's type (in fp16 an h past 65504 becomes infinite; so does a kept a or u).
  * d, d_ff multiples of 8 up to 2^20; T from 0 to 2^31 - 512 rows.
  * save_fmt keeps a and u for ft_gated_ffn_bwd in `saved`
  * (ft_gated_ffn_saved_bytes bytes):
@@ -416,8 +417,9 @@ int ft_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t d, int32_t d_ff,
  *   dh = dy w_down, du = dh act(a), da = dh u act'(a), h = act(a) u
  *   dx = da w_gate + du w_up, dw_gate = da^T x, dw_up = du^T x, dw_down = dy^T h
  * dy, dx and the weights' gradients (contiguous, shaped as the weights) are of
- * `dtype`.  h, da and du are rounded to `dtype` before the products that read them;
- * sums are fp32.  Gradients are written, not added to.  dx may be NULL (not wanted),
+ * `dtype`.  h, da and du are rounded to `dtype` before the products that read them (in
+ * fp16 they become infinite past 65504 and lose bits below 2^-14: scale dy as the loss is
+ * scaled); sums are fp32.  Gradients are written, not added to.  dx may be NULL (not wanted),
  * and so may the three weight gradients together.  With T = 0 the weights' gradients
  * are zeros.
  * saved, save_fmt: a and u as the forward call kept them; FT_SAVE_NONE computes them

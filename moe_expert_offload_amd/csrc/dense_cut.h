@@ -33,6 +33,8 @@ struct Cut {
 // Sharing cuts groups of tiles alike (all into 2 .. 16 parts, or 2 tiles into 3, or 3 into 4), so that blocks
 // at the same place of their groups still walk k in step: cutting one line of all tiles into equal
 // pieces left M = 2053, N = 4096, K = 11008 at 235 us, as slow as not sharing.
+// The constants were fitted at M = 1021, 2053 and 8192 rows. Between 65 and about 500 rows they say too much (65 and
+// 128 rows, d = 4096, d_ff = 2048: 50 us for both products, measured 35 and 36), and other cuts have not been timed there.
 inline Cut cut_of(int64_t M, int64_t n, int stages) {
   Cut c{};
   double cost = 1e30;

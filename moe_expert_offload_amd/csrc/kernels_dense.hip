@@ -4,6 +4,11 @@
 //   a = x Wg^T, u = x Wu^T, h = act(a) * u, y = h Wd^T (+ residual)
 //   dh = dy Wd, du = dh act(a), da = dh u act'(a)
 //   dWd = dy^T h, dWg = da^T x, dWu = du^T x, dx = da Wg + du Wu
+//
+// h, da and du are rounded to the activations' type as they leave their product's epilogue, because they
+// are the operands of the next 16-bit MFMA: keeping them in fp32 would take two or three products (high and low
+// parts) for one. Together with the result's rounding that is 1.4 times the error of fp32 rounded once (bf16
+// 2.3e-3 against 1.7e-3, fp16 2.9e-4 against 2.1e-4, over the elements' rms). Everything else is fp32.
 #include <type_traits>
 
 #include "dense_common.h"
@@ -930,7 +935,7 @@ __global__ __launch_bounds__(64 * W) void skinny_kernel(SkinnyArgs p) {
 
 // ---- 8-bit activations --------------------------------------------------------------
 // One thread per 16 elements (half a block of 32): 32 bytes in, 16 out, the block's largest by one
-// exchange with its neighbour; bound by memory (8192 x 4096: 18 us, 5.6 TB/s; unpacking 20 us, 5.1 TB/s).
+// exchange with its neighbour; bound by memory (8192 x 4096: 17-18 us, 5.6-6.0 TB/s; unpacking 19-20 us, 5.1-5.4 TB/s).
 __device__ __forceinline__ int64_t act8_row() {
   return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
 }

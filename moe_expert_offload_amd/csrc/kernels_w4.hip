@@ -13,7 +13,10 @@
 // is exact too, takes the offset away again within the same fp32 sum; the matrix cores are
 // idle in this memory-bound kernel, so that costs nothing.  Scales multiply the group's fp32 sum:
 // the weights are second operand, so a lane's results all belong to one weight row and
-// it needs one scale per group.
+// it needs one scale per group.  The price: an infinite x gives infinity - infinity, NaN, where the definition has
+// an infinity (or NaN, for a weight of 0).
+//
+// A gate/up product's h is rounded to the activations' type, as the next product's MFMA operand.
 #include "dense_common.h"
 
 namespace ft {
