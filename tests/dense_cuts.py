@@ -81,16 +81,21 @@ int main() {
 FIELDS = ("tile", "tiles_m", "tiles_n", "whole", "rest", "group", "blocks", "per", "parts", "part_bytes")
 
 
-def cuts(products, folder):
-    """The library's cut of each (M, n, stages), by a program made of its own header."""
+def program(text, lines, folder):
+    """The numbers that a program made of the library's own header prints for each line of numbers."""
     src, exe = os.path.join(folder, "cut.cpp"), os.path.join(folder, "cut")
     with open(src, "w") as f:
-        f.write(_PROGRAM)
+        f.write(text)
     cxx = build.CXX if shutil.which(build.CXX) or os.path.exists(build.CXX) else "g++"
     subprocess.run([cxx, "-O1", "-std=c++17", f"-I{build.CSRC}", "-o", exe, src], check=True, timeout=300)
-    lines = "\n".join(" ".join(map(str, p)) for p in products)
+    lines = "\n".join(" ".join(map(str, p)) for p in lines)
     out = subprocess.run([exe], input=lines, capture_output=True, text=True, check=True, timeout=300).stdout
-    return [dict(zip(FIELDS, map(int, v.split()))) for v in out.splitlines()]
+    return [tuple(map(int, v.split())) for v in out.splitlines()]
+
+
+def cuts(products, folder):
+    """The library's cut of each (M, n, stages)."""
+    return [dict(zip(FIELDS, v)) for v in program(_PROGRAM, products, folder)]
 
 
 def products(T, d, f, backward, again):

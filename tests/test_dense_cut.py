@@ -78,6 +78,30 @@ def test_every_stage_once(tmp_path):
     assert {"128", "128/k", "256", "256:1/k", "256+1/k", "384", "384:1/k", "384+1/k"} <= seen
 
 
+def test_sizes_cover_every_smaller_call(tmp_path):
+    """What the size queries count for the sums never falls with T and covers each call of T rows."""
+    rng = random.Random(6)
+    lines, shapes = [], [(4096, 2048), (2048, 768), (4096, 11008), (2048, 5632), (8192, 8), (8, 12312), (264, 11264)]
+    for d, f in shapes:
+        for T in sorted({rng.randrange(0, 20000) for _ in range(150)} | {0, 1, 64, 65, 128, 129, 16384, 16385, 2 ** 31 - 512}):
+            lines += [(T, d, f, b) for b in (0, 1)]
+    out = C.program("""
+#include <cstdio>
+#include "dense_cut.h"
+int main() {
+  long long T;
+  int d, f, b;
+  while (scanf("%lld %d %d %d", &T, &d, &f, &b) == 4)
+    printf("%zu %zu\\n", ft::gated_ffn_part_bytes(T, d, f, b), ft::gated_ffn_part_bound(T, d, f, b));
+}
+""", lines, str(tmp_path))
+    last = {}
+    for (T, d, f, b), (need, bound) in zip(lines, out):
+        assert need <= bound and last.get((d, f, b), 0) <= bound, (T, d, f, b)
+        last[d, f, b] = bound
+        assert T > 0 or need == 0
+
+
 @pytest.mark.parametrize("cases,backward", [(C.FORWARD, False), (C.BACKWARD, True)])
 def test_cases_reach_what_they_are_for(cases, backward, tmp_path):
     names, shapes = [], []

@@ -142,3 +142,106 @@ def test_act8_of_many_rows(n):
         v, w = src[at:min(at + (1 << 20), rows)].float(), out[at:min(at + (1 << 20), rows)].float()
         e = torch.exp2(scales[at:min(at + (1 << 20), rows)].float() - 127 - 10).repeat_interleave(32, 1)
         assert ((w - v).abs() <= torch.maximum(v.abs() * 2.0 ** -4, e)).all()
+
+
+def _every_call(b, mats, out, ws, wsb):
+    """One pass through each entry point from b.x and b.dy into the tensors of `out`; allocates nothing."""
+    T, d, f, t = b.T, b.d, b.f, FT[b.t]
+    act = ACT[b.kind]
+    ft.ft_gated_ffn(b.x, d, T, d, f, t, act, b.wg, b.wu, b.wd, b.dy, d, out["y"], d, t, out["saved"], ft.FT_SAVE_MX8, ws, wsb)
+    ft.ft_act8_pack(b.x, d, T, d, t, out["codes"], out["scales"])
+    ft.ft_act8_unpack(out["codes"], out["scales"], T, d, t, out["x"], d)
+    ft.ft_gated_ffn_bwd(out["codes"], d, out["scales"], T, d, f, t, act, b.wg, b.wu, b.wd, out["saved"], ft.FT_SAVE_MX8, b.dy,
+                        d, out["dx"], d, out["dwg"], out["dwu"], out["dwd"], ws, wsb)
+    ft.ft_gated_ffn_bwd(b.x, d, None, T, d, f, t, act, b.wg, b.wu, b.wd, None, ft.FT_SAVE_NONE, b.dy, d, out["dx2"], d, None,
+                        None, None, ws, wsb)
+    ft.ft_gated_ffn(b.x, d, 5, d, f, t, act, b.wg, b.wu, b.wd, None, d, out["y5"], d, t, None, ft.FT_SAVE_NONE, ws, wsb)
+    ft.ft_w4_gated_ffn(b.x, d, T, t, act, *(m[1] for m in mats), None, d, out["w4"], d, t, ws, wsb)
+    ft.ft_w4_gemv(b.x, d, 7, t, mats[0][1], None, f, out["g4"], f, FT["fp32"])
+
+
+def _setup(T, d, f, seed):
+    torch = torch_mod()
+    from tests.test_gpu_w4_exact import _ints, _pack
+    b = Block(T, d, f, "bf16", "silu", seed=seed)
+    mats = [_pack(_ints(b.g, -8, 7, n, k), None, torch.rand(n, k // 64, generator=b.g) * 0.01 + 0.002, 64, "bf16")
+            for n, k in ((f, d), (f, d), (d, f))]
+    wsb = max(ft.ft_gated_ffn_workspace_bytes(T, d, f), ft.ft_w4_gated_ffn_workspace_bytes(T, f),
+              *(ft.ft_gated_ffn_bwd_workspace_bytes(T, d, f, s, True) for s in SAVE.values()))
+    return b, mats, wsb
+
+
+def _outputs(b):
+    torch = torch_mod()
+    T, d, f, dt = b.T, b.d, b.f, b.dt
+    e = lambda *s, dtype=dt: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    u8 = torch.uint8
+    return dict(y=e(T, d), saved=e(ft.ft_gated_ffn_saved_bytes(T, f, ft.FT_SAVE_MX8), dtype=u8), codes=e(T, d, dtype=u8),
+                scales=e(T, d // 32, dtype=u8), x=e(T, d), dx=e(T, d), dwg=e(f, d), dwu=e(f, d), dwd=e(d, f), dx2=e(T, d),
+                y5=e(5, d), w4=e(T, d), g4=e(7, f, dtype=torch.float32))
+
+
+def test_captured_with_shared_tiles():
+    """Every entry point in one graph, on tiles that several blocks share, replayed with other inputs between eager calls
+    in a workspace of their own."""
+    torch = torch_mod()
+    b, mats, wsb = _setup(300, 2048, 1024, 25)
+    ws, ws_eager = (torch.empty(wsb, dtype=torch.uint8, device="cuda") for _ in range(2))
+    out, want = _outputs(b), _outputs(b)
+    _every_call(b, mats, out, ws, wsb)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _every_call(b, mats, out, ws, wsb)
+    for i in range(4):
+        b.x.copy_(b.rnd(b.T, b.d))
+        b.dy.copy_(b.rnd(b.T, b.d, std=0.3))
+        _every_call(b, mats, want, ws_eager, wsb)
+        torch.cuda.synchronize()
+        for v in out.values():
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in out:
+            assert torch.equal(out[k], want[k]), (i, k)
+
+
+def test_two_calls_at_once():
+    """Two streams with a workspace and outputs each, the same weights and inputs: the bits of one call alone."""
+    torch = torch_mod()
+    b, mats, wsb = _setup(300, 2048, 1024, 26)
+    want = _outputs(b)
+    ws = [torch.empty(wsb, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [_outputs(b) for _ in range(2)]
+    _every_call(b, mats, want, ws[0], wsb)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, o, w in zip(streams, outs, ws):
+            with torch.cuda.stream(s):
+                _every_call(b, mats, o, w, wsb)
+    torch.cuda.synchronize()
+    for o in outs:
+        for k in o:
+            assert torch.equal(o[k], want[k]), k
+
+
+def test_rows_alone_and_in_a_batch():
+    """A row's y, dx and 4-bit product have the same bits whatever rows stand beside it, within one form (the same
+    number of rows): a padded batch's padding does not reach the others."""
+    torch = torch_mod()
+    for T in (7, 40, 300):
+        _say("padding", T)
+        b, mats, wsb = _setup(T, 512, 256, 27)
+        ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+        outs = []
+        for pad in (0.0, float("nan"), 3e4):
+            o = _outputs(b)
+            b.x[T - 2:] = pad
+            b.dy[T - 2:] = pad
+            _every_call(b, mats, o, ws, wsb)
+            torch.cuda.synchronize()
+            outs.append({k: o[k][:T - 2] for k in ("y", "dx", "dx2", "x", "codes", "scales", "w4")})
+        for o in outs[1:]:
+            for k in o:
+                assert torch.equal(o[k], outs[0][k]), (T, k)
