@@ -36,6 +36,7 @@ SOURCES = [
     ("kernels_w4.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("api.cpp", CXX, HOST_FLAGS),
     ("api_dense.cpp", CXX, HOST_FLAGS),
+    ("dense_cut.cpp", CXX, HOST_FLAGS),
     ("cache.cpp", CXX, HOST_FLAGS),
     ("qstar.cpp", CXX, HOST_FLAGS),
     ("bwprofile.cpp", CXX, HOST_FLAGS),

@@ -82,12 +82,13 @@ FIELDS = ("tile", "tiles_m", "tiles_n", "whole", "rest", "group", "blocks", "per
 
 
 def program(text, lines, folder):
-    """The numbers that a program made of the library's own header prints for each line of numbers."""
+    """The numbers that a program made of the library's own dense_cut prints for each line of numbers."""
     src, exe = os.path.join(folder, "cut.cpp"), os.path.join(folder, "cut")
     with open(src, "w") as f:
         f.write(text)
     cxx = build.CXX if shutil.which(build.CXX) or os.path.exists(build.CXX) else "g++"
-    subprocess.run([cxx, "-O1", "-std=c++17", f"-I{build.CSRC}", "-o", exe, src], check=True, timeout=300)
+    subprocess.run([cxx, "-O1", "-std=c++17", f"-I{build.CSRC}", "-o", exe, src,
+                    os.path.join(build.CSRC, "dense_cut.cpp")], check=True, timeout=300)
     lines = "\n".join(" ".join(map(str, p)) for p in lines)
     out = subprocess.run([exe], input=lines, capture_output=True, text=True, check=True, timeout=300).stdout
     return [tuple(map(int, v.split())) for v in out.splitlines()]
