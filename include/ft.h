@@ -489,6 +489,50 @@ int ft_w4_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
                     const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- products in 8-bit integers ---------------------------------------------------
+ * As the dense operators above: stateless, asynchronous, to be captured, nothing
+ * allocated; equal calls give equal bits.
+ *
+ * Rows in 8 bits.  src: `dtype` (bf16 or fp16) [rows, n], n a multiple of 16 up to 2^16, ld as
+ * for the dense operators; codes int8 [rows, n], contiguous; scales fp32 [rows] (4-byte
+ * alignment).  scale = max|x| / 127 rounded to fp32; code = x / scale to nearest, ties to
+ * even, of the exact quotient (-127 .. 127).  A row of zeros has scale 0; a row with an infinity or
+ * NaN has scale NaN and codes 0, which makes its products' rows NaN.  Quantises weights
+ * too: a channel is a row. */
+int ft_i8_quant(const void* src, int64_t ld, int32_t rows, int32_t n, int32_t dtype, int8_t* codes,
+                float* scales, void* stream);
+
+/* A matrix [N, K] of 8-bit weights with a scale for each channel: w[n, k] = codes[n, k] * scales[n].
+ * codes contiguous, any int8 value (-128 too), 16-byte aligned; scales fp32 [N], 4-byte aligned.
+ * K a multiple of 16 up to 2^16; N up to 2^26 - 256. */
+typedef struct {
+  const int8_t* codes;
+  const float* scales;
+  int32_t N, K;
+} ft_i8_matrix;
+
+/* y[t, n] = ((sum over k of q[t, k] codes[n, k]) * scales[n]) * s[t] (+ residual): the sum exact
+ * in whole numbers, the rest in fp32, then rounded to y's type.
+ * x: with x_scales NULL `dtype` [T, K], quantised as ft_i8_quant does; else int8 codes [T, K] with
+ * their scales [T] (ldx a multiple of 16), as ft_i8_quant gives them or of any other rule (-128
+ * allowed).  y [T, N] and residual (may be NULL) of y_dtype, `dtype` or FT_T_FP32; ldy and ldr
+ * are any strides >= N, and y and residual need their element's alignment only.  T from 0 to
+ * 2^31 - 512, with up to 2^36 results.  workspace: ft_i8_gemm_workspace_bytes(T, N, K, x_scales != NULL). */
+size_t ft_i8_gemm_workspace_bytes(int32_t T, int32_t N, int32_t K, int32_t x_codes);
+int ft_i8_gemm(const void* x, int64_t ldx, const float* x_scales, int32_t T, int32_t dtype,
+               const ft_i8_matrix* w, const void* residual, int64_t ldr, void* y, int64_t ldy,
+               int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gated block of ft_gated_ffn on 8-bit weights: gate and up [d_ff, d], down [d, d_ff].  x is
+ * quantised, h = act(a) * u rounded to `dtype` and then quantised (a row of h that is not
+ * finite, in fp16 past 65504, makes its row of y NaN).  d, d_ff multiples of 16 up to 2^16; T as for ft_i8_gemm, T * 2 d_ff results.
+ * workspace: ft_i8_gated_ffn_workspace_bytes(T, d, d_ff). */
+size_t ft_i8_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t d_ff);
+int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_t act,
+                    const ft_i8_matrix* gate, const ft_i8_matrix* up, const ft_i8_matrix* down,
+                    const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- expert cache -------------------------------------------------------------- */
 
 /* Decisions of one decode call for routed ids idx_host (host int32 [T, k]):

@@ -99,14 +99,25 @@ size_t gated_ffn_part_bytes(int64_t T, int d, int d_ff, bool backward) {
 // Rows count by tiles of 128 and, where k runs over them, by stages of 64: every 64th number stands for all (60 us for
 // 8192 rows).  Past 16384 rows: what no cut passes, a slot of 256 KB for each unit's piece and each shared tile
 // (128 x 128 tiles: 2 kUnits pieces of 64 KB).
-size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward) {
+template <class Bytes>
+static size_t part_bound(int64_t T, Bytes bytes) {
   if (T > 16384) return (size_t)2 * kUnits * (256 << 10);
   size_t m = 0;
   for (int64_t t = 64; t < T + 64; t += 64) {
-    const size_t v = gated_ffn_part_bytes(t, d, d_ff, backward);
+    const size_t v = bytes(t);
     m = v > m ? v : m;
   }
   return m;
+}
+size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward) {
+  return part_bound(T, [&](int64_t t) { return gated_ffn_part_bytes(t, d, d_ff, backward); });
+}
+
+size_t i8_part_bytes(int64_t T, int64_t n, int K) {
+  return T <= kSkinnyRows ? 0 : cut_of(T, n, i8_stages(K)).part_bytes;
+}
+size_t i8_part_bound(int64_t T, int64_t n, int K) {
+  return part_bound(T, [&](int64_t t) { return i8_part_bytes(t, n, K); });
 }
 
 }  // namespace ft

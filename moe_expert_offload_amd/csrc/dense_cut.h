@@ -1,5 +1,5 @@
-// How the dense operators' tiled products (kernels_dense.hip) are cut over the compute units, and what
-// that takes of a workspace.  Host code, compiled once (dense_cut.cpp): sizes and launches go by the same cut.
+// How the dense operators' tiled products (kernels_dense.hip, kernels_i8.hip) are cut over the compute units, and
+// what that takes of a workspace.  Host code, compiled once (dense_cut.cpp): sizes and launches go by the same cut.
 #pragma once
 
 #include <cstddef>
@@ -28,5 +28,10 @@ Cut cut_of(int64_t M, int64_t n, int stages);  // stages: of 64 k
 size_t gated_ffn_part_bytes(int64_t T, int d, int d_ff, bool backward);
 // The most of that over 1 .. T rows, so that a workspace for the largest batch serves every smaller one.
 size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward);
+
+// The same for one product in 8-bit integers, whose stages are 128 k: the same bytes, multiplied in the same time.
+inline int i8_stages(int K) { return (K + 127) / 128; }
+size_t i8_part_bytes(int64_t T, int64_t n, int K);
+size_t i8_part_bound(int64_t T, int64_t n, int K);
 
 }  // namespace ft

@@ -191,6 +191,31 @@ struct W4Args {
 };
 int launch_w4(const W4Args& A, bool gate_up, void* stream);
 
+// ---- products in 8-bit integers (kernels_i8.hip) -----------------------------------
+struct I8Rows {  // tokens' codes [T, ld] and scales [T]
+  const int8_t* codes;
+  const float* scales;
+  int64_t ld;
+  int T;
+};
+struct I8Mat {  // channels' codes [N, K] and scales [N]
+  const int8_t* codes;
+  const float* scales;
+  int N, K;
+};
+struct I8Out {
+  void* y;
+  int64_t ldy;
+  int f32;
+  const void* res;
+  int64_t ldr;
+};
+int launch_i8_quant(const uint16_t* src, int64_t ld, int rows, int n, bool half, int8_t* codes, float* scales, void* stream);
+// part: i8_part_bytes (dense_cut.h) of the product.
+int launch_i8_gemm(const I8Rows& x, const I8Mat& w, const I8Out& o, bool half, int* part, void* stream);
+int launch_i8_gate_up(const I8Rows& x, const I8Mat& gate, const I8Mat& up, int act, uint16_t* h, bool half, int* part,
+                      void* stream);
+
 // ---- host expert kernel (cpu_exec.cpp) ----------------------------------------
 // One batch of CPU-branch work: experts `n_exp`, each with a record pointer and a
 // list of (token, gate) uses.  Computes partial[t] += sum gate * FFN_e(x[t]).

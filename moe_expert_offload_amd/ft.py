@@ -54,7 +54,8 @@ EXPORTED = [
     "ft_decode_graph_launch", "ft_decode_graph_status", "ft_decode_graph_destroy", "ft_permute_noalloc", "ft_permute_noalloc_max_scratch_bytes",
     "ft_gated_ffn_workspace_bytes", "ft_gated_ffn_saved_bytes", "ft_gated_ffn", "ft_gated_ffn_bwd_workspace_bytes",
     "ft_gated_ffn_bwd", "ft_act8_pack", "ft_act8_unpack", "ft_w4_gemv", "ft_w4_gated_ffn_workspace_bytes",
-    "ft_w4_gated_ffn",
+    "ft_w4_gated_ffn", "ft_i8_quant", "ft_i8_gemm_workspace_bytes", "ft_i8_gemm", "ft_i8_gated_ffn_workspace_bytes",
+    "ft_i8_gated_ffn",
 ]
 
 
@@ -116,6 +117,10 @@ class ft_profile(C.Structure):
 class ft_w4_matrix(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("zeros", C.c_void_p), ("N", C.c_int32),
                 ("K", C.c_int32), ("group", C.c_int32)]
+
+
+class ft_i8_matrix(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("N", C.c_int32), ("K", C.c_int32)]
 
 
 class FtError(RuntimeError):
@@ -184,6 +189,12 @@ def lib():
             "ft_w4_gated_ffn_workspace_bytes": (Z, [I, I]),
             "ft_w4_gated_ffn": (C.c_int, [P, L64, I, I, I, C.POINTER(ft_w4_matrix), C.POINTER(ft_w4_matrix),
                                           C.POINTER(ft_w4_matrix), P, L64, P, L64, I, P, Z, P]),
+            "ft_i8_quant": (C.c_int, [P, L64, I, I, I, P, P, P]),
+            "ft_i8_gemm_workspace_bytes": (Z, [I, I, I, I]),
+            "ft_i8_gemm": (C.c_int, [P, L64, P, I, I, C.POINTER(ft_i8_matrix), P, L64, P, L64, I, P, Z, P]),
+            "ft_i8_gated_ffn_workspace_bytes": (Z, [I, I, I]),
+            "ft_i8_gated_ffn": (C.c_int, [P, L64, I, I, I, C.POINTER(ft_i8_matrix), C.POINTER(ft_i8_matrix),
+                                          C.POINTER(ft_i8_matrix), P, L64, P, L64, I, P, Z, P]),
             "ft_combine": (C.c_int, [P, P, P, P, I, I, I, P, P]),
             "ft_expert_cache_lookup": (C.c_int, [P, I, P, I, C.POINTER(ft_plan)]),
             "ft_expert_cache_fill": (C.c_int, [P, C.POINTER(ft_plan), P, P, P]),
@@ -483,6 +494,37 @@ def ft_w4_gated_ffn_workspace_bytes(T, d_ff):
 def ft_w4_gated_ffn(x, ldx, T, dtype, act, gate, up, down, residual, ldr, y, ldy, y_dtype, workspace, workspace_bytes,
                     stream=None):
     return _check("ft_w4_gated_ffn", lib().ft_w4_gated_ffn(
+        _ptr(x), ldx, T, dtype, act, C.byref(gate), C.byref(up), C.byref(down), _ptr(residual), ldr, _ptr(y), ldy,
+        y_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ft_i8_quant(src, ld, rows, n, dtype, codes, scales, stream=None):
+    return _check("ft_i8_quant", lib().ft_i8_quant(_ptr(src), ld, rows, n, dtype, _ptr(codes), _ptr(scales),
+                                                   _stream(stream)))
+
+
+def make_i8_matrix(codes, scales, N, K):
+    """An 8-bit matrix of device tensors (or addresses); the caller keeps them alive."""
+    return ft_i8_matrix(_ptr(codes), _ptr(scales), N, K)
+
+
+def ft_i8_gemm_workspace_bytes(T, N, K, x_codes):
+    return lib().ft_i8_gemm_workspace_bytes(T, N, K, 1 if x_codes else 0)
+
+
+def ft_i8_gemm(x, ldx, x_scales, T, dtype, w, residual, ldr, y, ldy, y_dtype, workspace, workspace_bytes, stream=None):
+    return _check("ft_i8_gemm", lib().ft_i8_gemm(
+        _ptr(x), ldx, _ptr(x_scales), T, dtype, C.byref(w), _ptr(residual), ldr, _ptr(y), ldy, y_dtype, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def ft_i8_gated_ffn_workspace_bytes(T, d, d_ff):
+    return lib().ft_i8_gated_ffn_workspace_bytes(T, d, d_ff)
+
+
+def ft_i8_gated_ffn(x, ldx, T, dtype, act, gate, up, down, residual, ldr, y, ldy, y_dtype, workspace, workspace_bytes,
+                    stream=None):
+    return _check("ft_i8_gated_ffn", lib().ft_i8_gated_ffn(
         _ptr(x), ldx, T, dtype, act, C.byref(gate), C.byref(up), C.byref(down), _ptr(residual), ldr, _ptr(y), ldy,
         y_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
 
