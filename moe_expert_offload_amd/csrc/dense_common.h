@@ -76,6 +76,19 @@ __device__ __forceinline__ uint2 buf_ld8b(__amdgpu_buffer_rsrc_t r, uint32_t off
   return make_uint2((uint32_t)v.x, (uint32_t)v.y);
 }
 
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
+}
+
+// Quads q = 2j and 2j + 1 of a 32x32 result (4 consecutive n each, in two words of two 16-bit
+// elements) exchanged between lanes l and l + 32: lane l < 32 gets n = 16j .. 16j + 7, lane
+// l + 32 gets 16j + 8 .. 16j + 15.  Its own inverse.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r.x;
+  b = r.y;
+}
+
 // ---- activations --------------------------------------------------------------------
 // act(z) and act'(z).  Every value that leaves these is rounded to 16 bits (or 8) after, so
 // exp and the reciprocal are the hardware's (a few ulp of fp32).

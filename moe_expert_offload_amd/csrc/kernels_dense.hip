@@ -125,19 +125,6 @@ __device__ __forceinline__ TilePos tile_pos(const GemmArgs& p, int t) {
   return {first + in % rows, in / rows};
 }
 
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
-}
-
-// Quads q = 2j and 2j + 1 of a 32x32 result (4 consecutive n each, in two words of two 16-bit
-// elements) exchanged between lanes l and l + 32: lane l < 32 gets n = 16j .. 16j + 7, lane
-// l + 32 gets 16j + 8 .. 16j + 15.  Its own inverse.
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-  const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r.x;
-  b = r.y;
-}
-
 // What becomes of one 32-row piece of a wave's result: c0 and c1 are its 32x32 results at columns
 // nb0 and nb1 (kGateUp: a and u of the same columns).  The lane holds row m of those from mu on, and in
 // quad q the columns 8 q + 4 hi + 0..3 of each.

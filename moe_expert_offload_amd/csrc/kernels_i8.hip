@@ -101,7 +101,7 @@ __device__ __forceinline__ void store1(const I8Args& p, int64_t m, int n, float 
 }
 
 // ---- few rows: the weights stream once --------------------------------------------------
-// Up to 16 * NT tokens a pass.  A block owns 16 channels (kGateUp: 8 of each matrix), its waves split k
+// Up to 16 * NT tokens.  A block owns 16 channels (kGateUp: 8 of each matrix), its waves split k
 // in steps of 64 and add their sums in LDS.  v_mfma_i32_16x16x64: the weights are the second operand, so
 // each byte is loaded once, straight into registers; tokens past the last repeat it and their
 // sums are dropped.
@@ -112,13 +112,13 @@ __global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
   __shared__ int red[W][NT * 16][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.x * RB, t0 = blockIdx.y * (16 * NT);
+  const int r0 = blockIdx.x * RB;
   const int row = r0 + (GU ? (n & 7) : n);
   const int8_t* wp = GU && n >= 8 ? p.b2 : p.b;
   wp += (int64_t)min(row, p.N - 1) * p.K;
   const int8_t* xp[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xp[i] = p.a + (int64_t)min(t0 + i * 16 + n, p.M - 1) * p.lda;
+  for (int i = 0; i < NT; ++i) xp[i] = p.a + (int64_t)min(i * 16 + n, p.M - 1) * p.lda;
   i32x4_t acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = i32x4_t{};
@@ -147,10 +147,9 @@ __global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
     for (int r = 0; r < 4; ++r) red[wave][i * 16 + g * 4 + r][n] = acc[i][r];
   __syncthreads();
   for (int e = threadIdx.x; e < NT * 16 * RB; e += 64 * W) {
-    const int t = e / RB, c = e % RB;
-    const int tt = t0 + t, nn = r0 + c;
-    if (tt >= p.M || nn >= p.N) continue;
-    const float ts = p.ta[tt];
+    const int t = e / RB, c = e % RB, nn = r0 + c;
+    if (t >= p.M || nn >= p.N) continue;
+    const float ts = p.ta[t];
     int s = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) s += red[w][t][c];
@@ -159,35 +158,485 @@ __global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
 #pragma unroll
       for (int w = 0; w < W; ++w) u += red[w][t][c + 8];
       const float v = act_f(i8_value(s, p.sb[nn], ts), p.act) * i8_value(u, p.sb2[nn], ts);
-      p.h[(int64_t)tt * p.N + nn] = (uint16_t)pack2<H>(v, 0.0f);
+      p.h[(int64_t)t * p.N + nn] = (uint16_t)pack2<H>(v, 0.0f);
     } else {
-      store1<H>(p, tt, nn, i8_value(s, p.sb[nn], ts));
+      store1<H>(p, t, nn, i8_value(s, p.sb[nn], ts));
     }
   }
 }
 
+// ---- many rows: tiles -------------------------------------------------------------------
+// What becomes of one 32-row piece of a wave's sums: c0 and c1 are its 32x32 results at channels nb0 and nb1
+// (kGateUp: gate and up of the same ones).  The lane holds token m, and in quad q the channels
+// 8 q + 4 hi + 0..3 of each.
+template <int MODE, bool H>
+__device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0, const i32x16_t& c1, int m, int nb0,
+                                            int nb1, int hi) {
+  const bool mok = m < p.M;
+  const float ts = p.ta[mok ? m : p.M - 1];
+  if constexpr (MODE == kGateUp) {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = nb0 + 8 * (q + e) + 4 * hi, k = 4 * (q + e);
+        const float4 sg = scales4(p.sb, n, p.N), su = scales4(p.sb2, n, p.N);
+        const float h0 = act_f(i8_value(c0[k], sg.x, ts), p.act) * i8_value(c1[k], su.x, ts);
+        const float h1 = act_f(i8_value(c0[k + 1], sg.y, ts), p.act) * i8_value(c1[k + 1], su.y, ts);
+        const float h2 = act_f(i8_value(c0[k + 2], sg.z, ts), p.act) * i8_value(c1[k + 2], su.z, ts);
+        const float h3 = act_f(i8_value(c0[k + 3], sg.w, ts), p.act) * i8_value(c1[k + 3], su.w, ts);
+        w[2 * e] = pack2<H>(h0, h1);
+        w[2 * e + 1] = pack2<H>(h2, h3);
+      }
+      swap_halves(w[0], w[2]);
+      swap_halves(w[1], w[3]);
+      const int n = nb0 + 8 * q + 8 * hi;  // N % 16 == 0
+      if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int nb = j ? nb1 : nb0;
+      const i32x16_t& c = j ? c1 : c0;
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        float v[8];  // after the exchange: channels nb + 8 (q + hi) .. + 7
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 sc = scales4(p.sb, nb + 8 * (q + e) + 4 * hi, p.N);
+          const int k = 4 * (q + e);
+          v[4 * e] = i8_value(c[k], sc.x, ts);
+          v[4 * e + 1] = i8_value(c[k + 1], sc.y, ts);
+          v[4 * e + 2] = i8_value(c[k + 2], sc.z, ts);
+          v[4 * e + 3] = i8_value(c[k + 3], sc.w, ts);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t x = __float_as_uint(v[e]), y = __float_as_uint(v[4 + e]);
+          swap_halves(x, y);
+          v[e] = __uint_as_float(x);
+          v[4 + e] = __uint_as_float(y);
+        }
+        const int n = nb + 8 * q + 8 * hi;
+        if (!mok || n >= p.N) continue;
+        if (!p.wide) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < p.N) store1<H>(p, m, n + e, v[e]);
+        } else if (p.c_f32) {  // wide: N % 8 == 0
+          float* o = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n;
+          if (p.res) {
+            const float* r = static_cast<const float*>(p.res) + (int64_t)m * p.ldr + n;
+            const float4 a = *reinterpret_cast<const float4*>(r), b = *reinterpret_cast<const float4*>(r + 4);
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+          }
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc + n;
+          if (p.res) {
+            const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (int64_t)m * p.ldr + n);
+            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[2 * e] += lo16<H>(rw[e]);
+              v[2 * e + 1] += hi16<H>(rw[e]);
+            }
+          }
+          *reinterpret_cast<uint4*>(o) =
+              make_uint4(pack2<H>(v[0], v[1]), pack2<H>(v[2], v[3]), pack2<H>(v[4], v[5]), pack2<H>(v[6], v[7]));
+        }
+      }
+    }
+  }
+}
+
+// Tile index to its place: consecutive tiles walk 8 tile rows per column of tiles.
+struct TilePos {
+  int m, n;
+};
+__device__ __forceinline__ TilePos tile_pos(const I8Args& p, int t) {
+  const int per = 8 * p.tiles_n, grp = t / per, first = grp * 8;
+  const int rows = min(8, p.tiles_m - first), in = t - grp * per;
+  return {first + in % rows, in / rows};
+}
+
+// Two 32x32 sums of a wave among a piece's: 2048 whole numbers, quads of 4 channels by lane.
+__device__ __forceinline__ void store_part(int* at, const i32x16_t (&c)[2], int lane) {
+  i32x4_t* d = reinterpret_cast<i32x4_t*>(at) + lane;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[(j * 4 + q) * 64] = i32x4_t{c[j][4 * q], c[j][4 * q + 1], c[j][4 * q + 2], c[j][4 * q + 3]};
+}
+__device__ __forceinline__ void add_part(i32x16_t (&c)[2], const int* at, int lane) {
+  const i32x4_t* d = reinterpret_cast<const i32x4_t*>(at) + lane;
+  i32x4_t v[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[j][q] = d[(j * 4 + q) * 64];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[j][4 * q + e] += v[j][q][e];
+}
+
+// The places of operands in LDS, the walk over k and the cut into shared tiles are those of the 16-bit
+// products (kernels_dense.hip, gemm_kernel and gemm256_kernel, for operands along k): an LDS row is 128 bytes,
+// here 128 k, and an MFMA of 32 k takes the cycles of one of 16 there, so the same bytes are
+// loaded and read in the same time for twice the operations.
+
+// 128 x 128 tiles, 4 waves of 64 x 64: both operands straight into one of two LDS buffers, a stage ahead.
+template <int MODE, bool H>
+__global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
+  constexpr bool GU = MODE == kGateUp;
+  constexpr int SBYTES = 32768;
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[2 * SBYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, hi = lane >> 5, l31 = lane & 31;
+  const int stages = (p.K + 127) >> 7;
+  // consecutive blocks share an XCD; `blocks` of them share each tile's stages (rest > 0)
+  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int tile = p.rest ? lb / p.blocks : lb;
+  const int s_begin = p.rest ? (lb - tile * p.blocks) * p.per : 0;
+  const int s_end = p.rest ? min(stages, s_begin + p.per) : stages;
+  const TilePos tp = tile_pos(p, tile);
+  const int m0 = tp.m * 128, n0 = tp.n * (GU ? 64 : 128);
+
+  uint32_t offA[4], offB[4];
+  int kq[4];  // first k of the piece within the stage
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = (wave * 4 + j) * 8 + (lane >> 3), pc = (lane & 7) ^ ((r >> 1) & 7);
+    const int n = GU ? (r >> 6) * 32 + (r & 31) : r;  // blocks of 32 rows alternate between gate and up
+    kq[j] = pc * 16;
+    offA[j] = m0 + r < p.M ? (uint32_t)(r * p.lda + pc * 16) : kOOB;
+    offB[j] = n0 + n < p.N ? (uint32_t)(n * p.K + pc * 16) : kOOB;
+  }
+  const uint32_t sm0 = lds_addr(sm);
+  auto load_stage = [&](int s) {
+    const int k0 = s << 7, left = p.K - k0;
+    const uint32_t dst = sm0 + (s & 1) * SBYTES;
+    const auto ra = rsrc_of(p.a + m0 * p.lda + k0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lds_load16(ra, kq[j] < left ? offA[j] : kOOB, 0, dst + (wave * 4 + j) * 1024);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int8_t* w = GU && ((wave * 4 + j) & 4) ? p.b2 : p.b;
+      lds_load16(rsrc_of(w + (int64_t)n0 * p.K + k0), kq[j] < left ? offB[j] : kOOB, 0, dst + 16384 + (wave * 4 + j) * 1024);
+    }
+  };
+  auto frag = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
+  };
+  i32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
+  if (s_begin < s_end) load_stage(s_begin);
+  for (int s = s_begin; s < s_end; ++s) {
+    // this wave's loads of stage s have landed; past the barrier everyone's have, and nobody
+    // reads the other buffer any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + 1 < s_end) load_stage(s + 1);
+    const uint8_t *sa = sm + (s & 1) * SBYTES, *sb = sa + 16384;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      i32x4_t fa[2], fb[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[j] = frag(sb, wn * 64 + j * 32, k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i] = frag(sa, wm * 64 + i * 32, k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(fb[j], fa[i], acc[i][j]);
+    }
+    // the reads above are done before anyone passes the next barrier
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (p.rest) {
+      store_part(p.part + (size_t)lb * (128 * 128) + (wave * 2 + i) * 2048, acc[i], lane);
+    } else {
+      const int nb = n0 + wn * (GU ? 32 : 64);
+      i8_epilogue<MODE, H>(p, acc[i][0], acc[i][1], m0 + wm * 64 + i * 32 + l31, nb, nb + 32, hi);
+    }
+  }
+}
+
+// The shared tiles of the kernel above: a block per tile and 32-row piece of the waves.
+template <int MODE, bool H>
+__global__ __launch_bounds__(256) void i8_join128_kernel(I8Args p) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, t = blockIdx.x >> 1, i = blockIdx.x & 1;
+  const TilePos tp = tile_pos(p, t);
+  const int m = tp.m * 128 + wm * 64 + i * 32;
+  if (m >= p.M) return;
+  i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
+  for (int b = 0; b < p.blocks; ++b)
+    add_part(acc, p.part + (size_t)(t * p.blocks + b) * (128 * 128) + (wave * 2 + i) * 2048, lane);
+  const int nb = tp.n * (MODE == kGateUp ? 64 : 128) + wn * (MODE == kGateUp ? 32 : 64);
+  i8_epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 32, lane >> 5);
+}
+
+// 128 MH x 256 tiles, 8 waves, each 64 rows and 32 channels of every 128 x 128 quarter.  A stage is regions of
+// 16 KB (A0, B0, B1 and with MH = 2 A1); the waves 4..7 run one section behind the waves 0..3, so on every
+// SIMD one wave multiplies while the other reads.  Sections of a stage for the first group:
+//   MH = 2 (two stages in LDS)   read A0, B0, B1 of s; load A1 of s + 1; wait for A1 of s
+//                                A0 x B0, A0 x B1
+//                                read A1 of s; load A0, B0, B1 of s + 2; wait for A0, B0, B1 of s + 1
+//                                A1 x B1, A1 x B0
+//   MH = 1 (three stages)        read A0, B0, B1 of s; load those of s + 2; wait for those of s + 1
+//                                A0 x B0, A0 x B1
+// Every section ends with a barrier.  A region is loaded again two sections after the first group read it, one
+// after the second did (both end a read section with their reads done), and is waited for by both groups
+// at least one barrier before its first read.  Loads past the last stage are masked (they write
+// zeros nobody reads), which keeps the counts of the waits.
+template <int MODE, bool H, int MH>
+__global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
+  constexpr bool GU = MODE == kGateUp;
+  constexpr int REG = 16384;
+  enum { A0 = 0, B0 = REG, B1 = 2 * REG, A1 = 3 * REG, STAGE = (2 + MH) * REG, PLACES = MH == 2 ? 2 : 3 };
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[PLACES * STAGE];
+  constexpr int BM = 128 * MH, PART = BM * 256;  // rows of a tile, numbers of its sums
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, hi = lane >> 5, l31 = lane & 31;
+  const int stages = (p.K + 127) >> 7;
+
+  // This block's piece of work: a whole tile, or stages [at, end) of the rest's, which touch at
+  // most two tiles (per < stages).
+  int tile, at = 0, end = 1, b = 0;
+  const bool piece = (int)blockIdx.x >= p.whole;
+  if (!piece) {
+    tile = xcd_logical_block(blockIdx.x, p.whole);
+  } else {
+    b = xcd_logical_block(blockIdx.x - p.whole, p.parts);
+    const int g = b / p.blocks, line = p.group * stages;
+    at = g * line + (b - g * p.blocks) * p.per;
+    end = min(min(at + p.per, (g + 1) * line), p.rest * stages);
+    tile = p.whole;
+  }
+  while (at < end) {
+    int s_begin = 0, s_end = stages, slot = -1;
+    if (piece) {
+      const int t = at / stages;
+      tile = p.whole + t;
+      s_begin = at - t * stages;
+      s_end = min(stages, end - t * stages);
+      if (s_end - s_begin < stages) slot = b + t;
+      at = t * stages + s_end;
+    } else {
+      at = end;
+    }
+    const TilePos tp = tile_pos(p, tile);
+    const int m0 = tp.m * BM, n0 = tp.n * (GU ? 128 : 256);
+    // rows of a wave in the two halves: those past the end are neither read nor multiplied
+    const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
+
+    // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
+    uint32_t offA[MH][2], offB[2][2];  // [half][chunk]
+    int kq[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = (wave * 2 + j) * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);
+      kq[j] = pk * 16;
+#pragma unroll
+      for (int h = 0; h < MH; ++h) offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda + pk * 16) : kOOB;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int nh = n0 + (GU ? 0 : h * 128);
+        offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.K + pk * 16) : kOOB;
+      }
+    }
+    // Each region's source moves on by a stage per load.
+    const uint32_t sm0 = lds_addr(sm) + wave * 2048;
+    const int k0 = s_begin << 7;
+    const int8_t* pa[2] = {p.a + m0 * p.lda + k0, p.a + (m0 + 128) * p.lda + k0};
+    const int8_t* pb[2] = {p.b + (int64_t)n0 * p.K + k0, (GU ? p.b2 + (int64_t)n0 * p.K : p.b + (int64_t)(n0 + 128) * p.K) + k0};
+    auto load = [&](int s, const int8_t*& src, const uint32_t (&off)[2], uint32_t region, int place) {
+      const int left = s < s_end ? p.K - (s << 7) : 0;
+      const auto rs = rsrc_of(src);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) lds_load16(rs, kq[j] < left ? off[j] : kOOB, 0, sm0 + place * STAGE + region + j * 1024);
+      src += 128;
+    };
+    auto load_a = [&](int s, int h, int place) { load(s, pa[h], offA[h], h ? A1 : A0, place); };
+    auto load_b = [&](int s, int h, int place) { load(s, pb[h], offB[h], h ? B1 : B0, place); };
+
+    // ---- fragments of a region: 32 rows from `row`, slice of 32 k ----
+    auto frag = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
+      return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
+    };
+    i32x16_t acc[2 * MH][2];  // [2 half + 32-row piece][half of the channels]
+#pragma unroll
+    for (int i = 0; i < 2 * MH; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
+    i32x4_t fa[2][4], fb0[4], fb1[4];
+    auto read_a = [&](const uint8_t* base) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fa[i][k] = frag(base, wm * 64 + i * 32, k);
+    };
+    auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = frag(base, wn * 32, k);
+    };
+    auto multiply = [&](int half) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[2 * half + i][0] = mfma32(fb0[k], fa[i][k], acc[2 * half + i][0]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[2 * half + i][1] = mfma32(fb1[k], fa[i][k], acc[2 * half + i][1]);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+    // The end of a section: nothing moves across.
+    auto meet = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+
+    if (s_begin < s_end) {
+      load_a(s_begin, 0, 0);
+      load_b(s_begin, 0, 0);
+      load_b(s_begin, 1, 0);
+      if constexpr (MH == 2) load_a(s_begin, 1, 0);
+      load_a(s_begin + 1, 0, 1);
+      load_b(s_begin + 1, 0, 1);
+      load_b(s_begin + 1, 1, 1);
+      constexpr int WAIT = MH == 2 ? 8 : 6;
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(WAIT) : "memory");  // A0, B0 and B1 of the first stage
+      meet();
+      if (wm) meet();
+      // RAGGED: the tile has rows past the end.
+      auto walk = [&](auto ragged) {
+        constexpr bool RAGGED = decltype(ragged)::value;
+        int here = 0;
+        for (int s = s_begin; s < s_end; ++s) {
+          const uint8_t* st = sm + here * STAGE;
+          const int other = here == 0 ? PLACES - 1 : here - 1;
+          if (!RAGGED || any[0]) read_a(st + A0);
+          read_b(st + B0, fb0);
+          read_b(st + B1, fb1);
+          if constexpr (MH == 2) {
+            load_a(s + 1, 1, other);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
+          } else {
+            load_a(s + 2, 0, other);
+            load_b(s + 2, 0, other);
+            load_b(s + 2, 1, other);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(6)" ::: "memory");  // the next stage
+          }
+          meet();
+          if (!RAGGED || any[0]) multiply(0);
+          meet();
+          if constexpr (MH == 2) {
+            if (!RAGGED || any[1]) read_a(st + A1);
+            load_a(s + 2, 0, here);
+            load_b(s + 2, 0, here);
+            load_b(s + 2, 1, here);
+            reads_done();
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
+            meet();
+            if (!RAGGED || any[1]) multiply(1);
+            meet();
+          }
+          here = here == PLACES - 1 ? 0 : here + 1;
+        }
+      };
+      if (m0 + BM - 64 < p.M)
+        walk(std::false_type{});
+      else
+        walk(std::true_type{});
+      if (!wm) meet();
+      // the masked loads' writes too: a wave's next loads go where its own last ones went
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * MH; ++i) {
+      const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+      if (slot >= 0) {
+        if (m < p.M) store_part(p.part + (size_t)slot * PART + (wave * 2 * MH + i) * 2048, acc[i], lane);
+      } else {
+        i8_epilogue<MODE, H>(p, acc[i][0], acc[i][1], m + l31, n0 + wn * 32, n0 + wn * 32 + 128, hi);
+      }
+    }
+  }
+}
+
+// The tiles whose stages several blocks shared: a block per tile and 32-row piece of the waves; bound by memory.
+template <int MODE, bool H, int MH>
+__global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x % (2 * MH), t = blockIdx.x / (2 * MH);
+  const int stages = (p.K + 127) >> 7;
+  const int g = t / p.group, from = (t - g * p.group) * stages;
+  const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
+  if (first == last) return;  // one block had it all
+  const TilePos tp = tile_pos(p, p.whole + t);
+  const int m = tp.m * 128 * MH + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+  if (m >= p.M) return;
+  i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
+  for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * (MH * 128 * 256) + (wave * 2 * MH + i) * 2048, lane);
+  const int nb = tp.n * (MODE == kGateUp ? 128 : 256) + wn * 32;
+  i8_epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 128, lane >> 5);
+}
+
 // ---- launches -------------------------------------------------------------------------
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <int MODE, bool H>
 int i8_go(I8Args& A, hipStream_t s) {
-  constexpr int RB = MODE == kGateUp ? 8 : 16;
-  const unsigned nb = (unsigned)((A.N + RB - 1) / RB);
-  for (int t = 0; t < A.M; t += 64 * 65535) {
-    I8Args P = A;
-    P.M = A.M - t < 64 * 65535 ? A.M - t : 64 * 65535;
-    P.a += t * A.lda;
-    P.ta += t;
-    P.c = P.c ? static_cast<uint8_t*>(P.c) + t * A.ldc * (A.c_f32 ? 4 : 2) : nullptr;
-    P.res = P.res ? static_cast<const uint8_t*>(P.res) + t * A.ldr * (A.c_f32 ? 4 : 2) : nullptr;
-    P.h = P.h ? P.h + (int64_t)t * A.N : nullptr;
-    if (P.M <= 16)
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 1, 16>), dim3(nb, 1), dim3(1024), 0, s, P);
-    else if (P.M <= 32)
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 2, 8>), dim3(nb, 1), dim3(512), 0, s, P);
+  if (A.M <= kSkinnyRows) {
+    constexpr int RB = MODE == kGateUp ? 8 : 16;
+    const unsigned nb = (unsigned)((A.N + RB - 1) / RB);
+    if (A.M <= 16)
+      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 1, 16>), dim3(nb), dim3(1024), 0, s, A);
+    else if (A.M <= 32)
+      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 2, 8>), dim3(nb), dim3(512), 0, s, A);
     else
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 4, 8>), dim3(nb, (unsigned)((P.M + 63) / 64)), dim3(512), 0, s, P);
+      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 4, 8>), dim3(nb), dim3(512), 0, s, A);
+    return launched("i8_skinny_kernel");
   }
-  return launched("i8_skinny_kernel");
+  const size_t es = A.c_f32 ? 4 : 2;
+  A.wide = A.N % 8 == 0 && aligned(A.c, 16) && aligned(A.res, 16) && A.ldc * es % 16 == 0 && (!A.res || A.ldr * es % 16 == 0);
+  const Cut c = cut_of(A.M, MODE == kGateUp ? 2 * (int64_t)A.N : A.N, i8_stages(A.K));
+  A.tiles_m = c.tiles_m;
+  A.tiles_n = c.tiles_n;
+  A.whole = c.whole;
+  A.rest = c.rest;
+  A.group = c.group;
+  A.blocks = c.blocks;
+  A.per = c.per;
+  A.parts = c.parts;
+  if (c.tile == 256) {
+    hipLaunchKernelGGL((i8_tile256_kernel<MODE, H, 2>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 2>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
+  } else if (c.tile == 384) {
+    hipLaunchKernelGGL((i8_tile256_kernel<MODE, H, 1>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 1>), dim3((unsigned)c.rest * 2), dim3(512), 0, s, A);
+  } else {
+    hipLaunchKernelGGL((i8_tile128_kernel<MODE, H>), dim3((unsigned)c.parts), dim3(256), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((i8_join128_kernel<MODE, H>), dim3((unsigned)c.rest * 2), dim3(256), 0, s, A);
+  }
+  return launched("i8_tile_kernel");
 }
 
 template <int MODE>
