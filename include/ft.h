@@ -39,6 +39,11 @@
  *               one E8M0 scale per 32 consecutive elements along each matrix's
  *               reduction axis (d for gate/up, d_ff for down); weight value =
  *               e2m1(code) * 2^(scale - 127).  S = 3*d*d_ff/2 + 3*d*d_ff/32 bytes.
+ *   FT_W_I8 (for ft_moe_layer alone; a context refuses it): bytes
+ *               [ gate codes d_ff x d | up codes d_ff x d | down codes d x d_ff |
+ *                 gate scales fp32 d_ff | up scales fp32 d_ff | down scales fp32 d ],
+ *               int8 codes, one scale for each row; weight value = code * scale.
+ *               S = 3*d*d_ff + 4*(2*d_ff + d) bytes.
  * S = ft_record_bytes(shape).  The host pool holds L_phys*E records; logical
  * layer l, expert e reads record (l mod L_phys)*E + e.
  *
@@ -77,11 +82,12 @@ extern "C" {
 
 #define FT_PLAN_CAP 512       /* max routed pairs T*k in one decode call */
 
-typedef enum { FT_W_BF16 = 0, FT_W_MXFP4 = 1 } ft_wfmt;
+typedef enum { FT_W_BF16 = 0, FT_W_MXFP4 = 1, FT_W_I8 = 2 } ft_wfmt;
 
 /* Layer-stack shape.  L layers, E routed experts per layer, hidden size d,
  * expert hidden size d_ff, k experts per token.  d and d_ff must be multiples of 8
- * (FT_W_BF16); FT_W_MXFP4 needs d % 256 == 0 and d_ff % 128 == 0. */
+ * (FT_W_BF16); FT_W_MXFP4 needs d % 256 == 0 and d_ff % 128 == 0, FT_W_I8 d % 16 == 0 and
+ * d_ff % 16 == 0. */
 typedef struct {
   int32_t L, E, d, d_ff, k;
   int32_t fmt; /* ft_wfmt: expert record format */
@@ -532,6 +538,31 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
                     const ft_i8_matrix* gate, const ft_i8_matrix* up, const ft_i8_matrix* down,
                     const void* residual, int64_t ldr, void* y, int64_t ldy, int32_t y_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- a routed layer for a few tokens, its experts on the device -------------------
+ * Stateless, asynchronous, to be captured, nothing allocated; equal calls give equal bits.
+ *
+ * Router, top-k, gates, the routed experts and their weighted sum in one call:
+ *   y[t] = sum over j of gates[t, j] * W_down (silu(W_gate x_t) * (W_up x_t)) (+ residual[t])
+ * over the experts idx[t, j], in the order of j.  shape: E, d, d_ff, k and the records' format (L is not
+ * used); d <= 16384, d_ff <= 65536, a record below 2 GiB.  x: device bf16 [T, d], 0 <= T <= 64,
+ * T * k <= FT_PLAN_CAP.  w_router, allowed, idx, gates: as for ft_router_topk, and with its bits (a row
+ * that allows fewer than k experts gets idx -1 and gate 0 in the places left).
+ * records: n_slots records one after another, 16-byte aligned.  slot_of: device int32 [E], the
+ * record of each expert, or NULL: record e is expert e's (n_slots >= E).  An expert whose slot is
+ * outside [0, n_slots) is left out of the sum (its gate stands): with the cache's residency as slot_of,
+ * y is the device's part of the layer.
+ * y [T, d] and residual (may be NULL, may be y) of y_dtype, FT_T_BF16 or FT_T_FP32.
+ * Arithmetic: FT_W_BF16 and FT_W_MXFP4 (weights dequantised exactly) apply to the bf16 x and to h in
+ * fp32, fp32 sums.  FT_W_I8: x, and h rounded to bf16, are quantised as ft_i8_quant does, a product is
+ * that of ft_i8_gemm.  The gates' sum and the residual are fp32, rounded once to y's type.
+ * x, w_router, records 16-byte aligned; workspace: ft_moe_layer_workspace_bytes(shape, T),
+ * 256-byte aligned; one for the most tokens serves fewer. */
+size_t ft_moe_layer_workspace_bytes(const ft_shape* shape, int32_t T);
+int ft_moe_layer(const ft_shape* shape, const void* x, int32_t T, const void* w_router,
+                 const uint8_t* allowed, const void* records, int32_t n_slots, const int32_t* slot_of,
+                 const void* residual, void* y, int32_t y_dtype, int32_t* idx, float* gates,
+                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- expert cache -------------------------------------------------------------- */
 

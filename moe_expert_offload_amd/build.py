@@ -35,9 +35,11 @@ SOURCES = [
     ("kernels_dense.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("kernels_w4.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("kernels_i8.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
+    ("kernels_moe.hip", HIPCC, [f"--offload-arch={ARCH}"] + DEVICE_FLAGS),
     ("api.cpp", CXX, HOST_FLAGS),
     ("api_dense.cpp", CXX, HOST_FLAGS),
     ("api_i8.cpp", CXX, HOST_FLAGS),
+    ("api_moe.cpp", CXX, HOST_FLAGS),
     ("dense_cut.cpp", CXX, HOST_FLAGS),
     ("cache.cpp", CXX, HOST_FLAGS),
     ("qstar.cpp", CXX, HOST_FLAGS),

@@ -301,6 +301,12 @@ const char* ft_strerror(int st) {
 const char* ft_last_error(void) { return ft::g_last_error.c_str(); }
 
 size_t ft_record_bytes(const ft_shape* s) {
+  if (s && s->fmt == FT_W_I8) {
+    ft_shape b = *s;
+    b.fmt = FT_W_BF16;
+    if (!shape_ok(&b) || s->d % 16 || s->d_ff % 16) return 0;
+    return (size_t)3 * s->d * s->d_ff + 4 * (2 * (size_t)s->d_ff + s->d);
+  }
   if (!shape_ok(s)) return 0;
   if (is_mx(s)) return ft::mx_record_bytes(s->d, s->d_ff);
   return (size_t)6 * s->d * s->d_ff;

@@ -216,6 +216,27 @@ int launch_i8_gemm(const I8Rows& x, const I8Mat& w, const I8Out& o, bool half, i
 int launch_i8_gate_up(const I8Rows& x, const I8Mat& gate, const I8Mat& up, int act, uint16_t* h, bool half, int* part,
                       void* stream);
 
+// ---- the routed layer for a few tokens (kernels_moe.hip) ----------------------------
+// Its tensors checked and its workspace laid out.
+struct MoeLayer {
+  const uint16_t *x, *w_router;
+  const uint8_t *allowed, *records;
+  int n_slots;
+  const int32_t* slot_of;
+  size_t S;  // bytes of a record
+  int T, d, d_ff, E, k, fmt;
+  const void* res;
+  void* y;
+  int y_f32;
+  int32_t* idx;
+  float* gates;
+  float* logits;  // [T, E]
+  int8_t *xq, *hq;  // 8-bit records: codes and scales of x [T, d] and h [T k, d_ff]
+  float *xs, *hs;
+  void* h;  // [T k, d_ff] fp32, 8-bit records bf16
+};
+int launch_moe_layer(const MoeLayer& L, void* stream);
+
 // ---- host expert kernel (cpu_exec.cpp) ----------------------------------------
 // One batch of CPU-branch work: experts `n_exp`, each with a record pointer and a
 // list of (token, gate) uses.  Computes partial[t] += sum gate * FFN_e(x[t]).

@@ -1,0 +1,565 @@
+// A whole routed layer for a few tokens whose experts are all on the device.  gfx950 only.
+//
+//   logits = x W_r^T; the k largest of the allowed experts; gates = softmax over those
+//   y[t] = sum over j of gates[t, j] * Wd_e (silu(Wg_e x[t]) * (Wu_e x[t])), e = idx[t, j] (+ residual[t])
+//
+// Three launches: the logits, gate/up and down.  The second does the top-k of every token and groups
+// the routed pairs by expert, every block by itself (in LDS; a layer of 64 tokens has 512 pairs at most),
+// so that no launch and no wait across blocks lies between; the third sums a token's experts where they
+// leave their product, so there is no combine.  Both stream the routed experts' rows once, whatever
+// number of tokens takes them: a wavefront holds a few rows in registers and applies each token of
+// the expert to them (lane l takes the 16-byte pieces l, l + 64, ... of a row, 1 KB a load).  Bound by
+// memory.
+//
+// Records (bf16, MXFP4) as in include/ft.h; MXFP4 weights are dequantised exactly and applied to the bf16
+// x and the fp32 h.  8-bit records: x and h in 8 bits as ft_i8_quant gives them (h rounded to bf16 before),
+// whole-number sums, as the blocks of kernels_i8.hip.
+#include "i8_common.h"
+#include "router_device.h"
+
+namespace ft {
+
+using namespace dev;
+
+namespace {
+
+constexpr int NT = 512, NW = NT / 64;  // threads and wavefronts of a block
+
+struct MoeArgs {
+  const uint16_t* x;
+  const float* logits;
+  const uint8_t* allowed;
+  const uint8_t* rec;
+  const int32_t* slot_of;
+  int T, d, f, E, k, n_slots;
+  size_t S;
+  int32_t* idx;
+  float* gates;
+  const int8_t* xq;  // 8-bit records: x in 8 bits
+  const float* xs;
+  int8_t* hq;  // h in 8 bits
+  float* hs;
+  void* h;  // [T k, f]: fp32, 8-bit records bf16
+  const void* res;
+  void* y;
+  int y_f32;
+  int rows;     // down: rows of a block
+  int lds_vec;  // the tokens' rows (gate/up: x, down: h) are staged in LDS
+};
+
+// ---- 16-byte pieces of rows, by format --------------------------------------------------
+// E elements a piece; gate/up multiplies it by NU 16-byte parts of x, down by ND parts of h.
+template <int FMT>
+struct Fmt;
+template <>
+struct Fmt<FT_W_BF16> {
+  static constexpr int E = 8, NU = 1, ND = 2;
+  typedef float Acc;
+};
+template <>
+struct Fmt<FT_W_MXFP4> {
+  static constexpr int E = 32, NU = 4, ND = 8;
+  typedef float Acc;
+};
+template <>
+struct Fmt<FT_W_I8> {
+  static constexpr int E = 16, NU = 1, ND = 1;
+  typedef int Acc;
+};
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float dot_bf16(uint4 a, uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, x[i]), __builtin_bit_cast(bf16x2_t, y[i]), acc, false);
+  return acc;
+}
+__device__ __forceinline__ float dot_f32(uint4 a, uint4 h0, uint4 h1, float acc) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  const uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc = fmaf(bf_lo(w[i]), __uint_as_float(h[2 * i]), acc);
+    acc = fmaf(bf_hi(w[i]), __uint_as_float(h[2 * i + 1]), acc);
+  }
+  return acc;
+}
+// 2^(s - 127) for an E8M0 byte.
+__device__ __forceinline__ float e8m0(uint32_t s) { return s ? __uint_as_float(s << 23) : 0x1p-127f; }
+template <int B>
+__device__ __forceinline__ bf16x2_t mx_pair(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, B);
+}
+template <int B>
+__device__ __forceinline__ f32x2_t mx_pair32(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B);
+}
+__device__ __forceinline__ float mx_word_bf16(uint32_t w, uint4 x, float acc) {
+  acc = __builtin_amdgcn_fdot2_f32_bf16(mx_pair<0>(w), __builtin_bit_cast(bf16x2_t, x.x), acc, false);
+  acc = __builtin_amdgcn_fdot2_f32_bf16(mx_pair<1>(w), __builtin_bit_cast(bf16x2_t, x.y), acc, false);
+  acc = __builtin_amdgcn_fdot2_f32_bf16(mx_pair<2>(w), __builtin_bit_cast(bf16x2_t, x.z), acc, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(mx_pair<3>(w), __builtin_bit_cast(bf16x2_t, x.w), acc, false);
+}
+__device__ __forceinline__ float mx_word_f32(uint32_t w, uint4 a, uint4 b, float acc) {
+  f32x2_t v = mx_pair32<0>(w);
+  acc = fmaf(v.x, __uint_as_float(a.x), acc);
+  acc = fmaf(v.y, __uint_as_float(a.y), acc);
+  v = mx_pair32<1>(w);
+  acc = fmaf(v.x, __uint_as_float(a.z), acc);
+  acc = fmaf(v.y, __uint_as_float(a.w), acc);
+  v = mx_pair32<2>(w);
+  acc = fmaf(v.x, __uint_as_float(b.x), acc);
+  acc = fmaf(v.y, __uint_as_float(b.y), acc);
+  v = mx_pair32<3>(w);
+  acc = fmaf(v.x, __uint_as_float(b.z), acc);
+  return fmaf(v.y, __uint_as_float(b.w), acc);
+}
+__device__ __forceinline__ int dot_i8(uint4 a, uint4 b, int acc) {
+  acc = __builtin_amdgcn_sdot4((int)a.x, (int)b.x, acc, false);
+  acc = __builtin_amdgcn_sdot4((int)a.y, (int)b.y, acc, false);
+  acc = __builtin_amdgcn_sdot4((int)a.z, (int)b.z, acc, false);
+  return __builtin_amdgcn_sdot4((int)a.w, (int)b.w, acc, false);
+}
+// acc + piece w (MXFP4: under scale byte sc) times the parts v of x (DOWN: of h).
+template <int FMT, bool DOWN, int NV>
+__device__ __forceinline__ typename Fmt<FMT>::Acc piece_dot(uint4 w, uint32_t sc, const uint4 (&v)[NV],
+                                                            typename Fmt<FMT>::Acc acc) {
+  if constexpr (FMT == FT_W_I8) {
+    return dot_i8(w, v[0], acc);
+  } else if constexpr (FMT == FT_W_BF16) {
+    if constexpr (DOWN)
+      return dot_f32(w, v[0], v[1], acc);
+    else
+      return dot_bf16(w, v[0], acc);
+  } else {
+    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s = DOWN ? mx_word_f32(c[q], v[2 * q], v[2 * q + 1], s) : mx_word_bf16(c[q], v[q], s);
+    return fmaf(s, e8m0(sc), acc);
+  }
+}
+
+__device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
+  return v;
+}
+
+// A record's parts (byte offsets).
+struct Rec {
+  uint32_t up, down, gs, us, ds;  // codes (the gate's at 0), scales
+};
+template <int FMT>
+__device__ __forceinline__ Rec rec_of(int d, int f) {
+  Rec r;
+  const size_t n = (size_t)d * f;
+  if constexpr (FMT == FT_W_BF16) {
+    r = Rec{(uint32_t)(2 * n), (uint32_t)(4 * n), 0, 0, 0};
+  } else if constexpr (FMT == FT_W_MXFP4) {
+    const size_t c = n / 2, s = n / 32;
+    r = Rec{(uint32_t)c, (uint32_t)(2 * c), (uint32_t)(3 * c), (uint32_t)(3 * c + s), (uint32_t)(3 * c + 2 * s)};
+  } else {
+    r = Rec{(uint32_t)n, (uint32_t)(2 * n), (uint32_t)(3 * n), (uint32_t)(3 * n + 4 * (size_t)f), (uint32_t)(3 * n + 8 * (size_t)f)};
+  }
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ int row_bytes(int n) {
+  return FMT == FT_W_BF16 ? 2 * n : FMT == FT_W_MXFP4 ? n / 2 : n;
+}
+
+// ---- the routed pairs by expert, in LDS ---------------------------------------------------
+struct Plan {
+  int32_t id[FT_PLAN_CAP];  // expert of a pair
+  float gate[FT_PLAN_CAP];
+  int32_t grp[FT_PLAN_CAP];    // its group, -1: left out (no expert, or none of the given ones)
+  int32_t slot[FT_PLAN_CAP];   // of a group
+  int32_t off[FT_PLAN_CAP + 1];  // first of a group's pairs in `pair`
+  int32_t pair[FT_PLAN_CAP];   // pairs by (group, pair)
+  int32_t wave_first[NW];
+  int32_t n_groups, n_pairs;
+};
+
+// Groups in the order of their first pair.  id and gate are set; all threads of the block.
+__device__ void make_plan(Plan& P, const MoeArgs& p) {
+  const int n = p.T * p.k, i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  int id = -1, slot = -1, before = 0;
+  if (i < n) {
+    id = P.id[i];
+    if (id >= 0 && id < p.E) {
+      slot = p.slot_of ? p.slot_of[id] : id;
+      if (slot < 0 || slot >= p.n_slots) slot = -1;
+    }
+    for (int q = 0; q < i; ++q) before += P.id[q] == id;
+  }
+  const bool first = slot >= 0 && before == 0;
+  const unsigned long long m = __ballot(first);
+  if (lane == 0) P.wave_first[wave] = __popcll(m);
+  __syncthreads();
+  int rank = __popcll(m & ((1ull << lane) - 1)), total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    rank += w < wave ? P.wave_first[w] : 0;
+    total += P.wave_first[w];
+  }
+  if (i < n) P.grp[i] = -1;
+  if (first) {
+    P.grp[i] = rank;
+    P.slot[rank] = slot;
+  }
+  if (i == 0) P.n_groups = total;
+  __syncthreads();
+  // the other pairs of an expert take its first one's group
+  int grp = i < n ? P.grp[i] : -1;
+  if (i < n && slot >= 0 && !first)
+    for (int q = 0; q < i; ++q)
+      if (P.id[q] == id) {
+        grp = P.grp[q];
+        break;
+      }
+  __syncthreads();
+  if (i < n) P.grp[i] = grp;
+  __syncthreads();
+  // pairs of groups before this thread's (as a pair: its group; as a group: i)
+  int base = 0, off = 0, all = 0;
+  for (int q = 0; q < n; ++q) {
+    const int g = P.grp[q];
+    base += g >= 0 && g < grp;
+    off += g >= 0 && g < i;
+    all += g >= 0;
+  }
+  if (grp >= 0) P.pair[base + before] = i;
+  if (i <= total) P.off[i] = off;
+  if (i == 0) P.n_pairs = all;
+  if (i == 0 && total == NT) P.off[total] = all;
+  __syncthreads();
+}
+
+// Rows of x (h): `rows` rows of `pieces` pieces of NV 16-byte parts.  In LDS the parts of a row lie in planes (part
+// v of piece i at v * pieces + i), so that 64 lanes read 64 consecutive 16-byte places.
+template <int NV>
+__device__ __forceinline__ void stage_rows(uint4* dst, const uint4* src, int rows, int pieces) {
+  const int per = pieces * NV;
+  for (int i = threadIdx.x; i < rows * per; i += NT) {
+    if constexpr (NV == 1) {
+      dst[i] = src[i];
+    } else {
+      const int r = i / per, e = i - r * per;
+      dst[r * per + (e % NV) * pieces + e / NV] = src[i];
+    }
+  }
+}
+template <int NV, bool LV>
+__device__ __forceinline__ void load_parts(uint4 (&v)[NV], const uint4* row, int pieces, int i) {
+#pragma unroll
+  for (int q = 0; q < NV; ++q) v[q] = row[LV ? q * pieces + i : i * NV + q];
+}
+
+// ---- logits ---------------------------------------------------------------------------------
+template <int TT, int TE>
+__global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
+                                                         int T, int d, int E, float* __restrict__ logits) {
+  router_logits_wave<TT, TE>(x, w, T, d, E, blockIdx.y * TT, (blockIdx.x * 4 + (threadIdx.x >> 6)) * TE, threadIdx.x & 63,
+                             logits);
+}
+
+// ---- gate/up ----------------------------------------------------------------------------------
+// A wavefront takes units of RG row pairs (gate and up), a consecutive share of all of them.
+template <int FMT, int JC, int RG, bool LV>
+__device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const uint4* sx) {
+  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU, TB = 4;
+  typedef typename Fmt<FMT>::Acc Acc;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Rec R = rec_of<FMT>(p.d, p.f);
+  const int pieces = p.d / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.d);
+  const int per_group = (p.f + RG - 1) / RG;
+  const int64_t units = (int64_t)P.n_groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
+  const int u_end = (int)(units * (w + 1) / nw);
+  for (int u = (int)(units * w / nw); u < u_end; ++u) {
+    const int g = u / per_group, r0 = (u - g * per_group) * RG;
+    const auto rec = buf_rsrc(p.rec + (size_t)P.slot[g] * p.S, (uint32_t)p.S);
+    const int first = P.off[g], n = P.off[g + 1] - first;
+    uint4 wv[2 * RG][JC];
+    uint32_t sc[2 * RG][JC];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int r = 0; r < 2 * RG; ++r) {
+        const int row = r0 + (r >> 1);
+        const uint32_t base = (r & 1 ? R.up : 0u) + (uint32_t)row * (uint32_t)rb;
+#pragma unroll
+        for (int j = 0; j < JC; ++j) {
+          const int i = (j0 + j) * 64 + lane;
+          const bool in = row < p.f && i < pieces;
+          wv[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
+          sc[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? (r & 1 ? R.us : R.gs) + (uint32_t)row * (uint32_t)pieces + i : kOOB) : 0;
+        }
+      }
+    };
+    load(0);
+    for (int tb = 0; tb < n; tb += TB) {
+      Acc acc[TB][2 * RG];
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int r = 0; r < 2 * RG; ++r) acc[t][r] = 0;
+      for (int j0 = 0; j0 < J; j0 += JC) {
+        if (J > JC && (j0 > 0 || tb > 0)) load(j0);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          if (tb + t >= n) continue;
+          const int tok = P.pair[first + tb + t] / p.k;
+          const uint4* row = LV ? sx + (size_t)tok * pieces * NV
+                                : reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)(p.xq + (size_t)tok * p.d)
+                                                                                : (const void*)(p.x + (size_t)tok * p.d));
+#pragma unroll
+          for (int j = 0; j < JC; ++j) {
+            const int i = (j0 + j) * 64 + lane;
+            if (i >= pieces) continue;
+            uint4 v[NV];
+            load_parts<NV, LV>(v, row, pieces, i);
+#pragma unroll
+            for (int r = 0; r < 2 * RG; ++r) acc[t][r] = piece_dot<FMT, false, NV>(wv[r][j], sc[r][j], v, acc[t][r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        if (tb + t >= n) continue;
+        const int pair = P.pair[first + tb + t];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          const Acc a = wave_total(acc[t][2 * r]), b = wave_total(acc[t][2 * r + 1]);
+          const int row = r0 + r;
+          if (lane != 0 || row >= p.f) continue;
+          if constexpr (FMT == FT_W_I8) {
+            const float *gs = reinterpret_cast<const float*>(p.rec + (size_t)P.slot[g] * p.S + R.gs) + row, ts = p.xs[pair / p.k];
+            const float v = act_f(i8_value(a, gs[0], ts), FT_ACT_SILU) * i8_value(b, gs[p.f], ts);
+            static_cast<uint16_t*>(p.h)[(size_t)pair * p.f + row] = (uint16_t)pack2<false>(v, 0.0f);
+          } else {
+            static_cast<float*>(p.h)[(size_t)pair * p.f + row] = silu(a) * b;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, int JC, int RG>
+__global__ __launch_bounds__(NT, 2) void moe_up_kernel(MoeArgs p) {
+  __shared__ Plan P;
+  extern __shared__ uint4 vec[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (p.lds_vec) {
+    constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU;
+    stage_rows<NV>(vec, reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.xq : (const void*)p.x), p.T, p.d / E);
+  }
+  topk_tokens(p.logits, p.allowed, p.T, p.E, p.k, wave, NW, lane, P.id, P.gate);
+  __syncthreads();
+  if (blockIdx.x == 0 && (int)threadIdx.x < p.T * p.k) {
+    p.idx[threadIdx.x] = P.id[threadIdx.x];
+    p.gates[threadIdx.x] = P.gate[threadIdx.x];
+  }
+  make_plan(P, p);
+  if (p.lds_vec)
+    up_units<FMT, JC, RG, true>(p, P, vec);
+  else
+    up_units<FMT, JC, RG, false>(p, P, nullptr);
+}
+
+// ---- down --------------------------------------------------------------------------------------
+// A block owns p.rows rows of every expert's W_down and so of y; its wavefronts take units of RR rows of one
+// group.  A pair's results wait in LDS until all are there, then each token's are added in the order of j.
+constexpr int kDownRows = 16;
+
+template <int FMT, int JC, int RR, bool LV>
+__device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, const uint4* sh, float* out) {
+  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND, TB = 4;
+  typedef typename Fmt<FMT>::Acc Acc;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Rec R = rec_of<FMT>(p.d, p.f);
+  const int pieces = p.f / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.f);
+  const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0), per_group = (nr + RR - 1) / RR;
+  for (int u = wave; u < P.n_groups * per_group; u += NW) {
+    const int g = u / per_group, q0 = (u - g * per_group) * RR;
+    const uint8_t* rp = p.rec + (size_t)P.slot[g] * p.S;
+    const auto rec = buf_rsrc(rp, (uint32_t)p.S);
+    const int first = P.off[g], n = P.off[g + 1] - first;
+    uint4 wv[RR][JC];
+    uint32_t sc[RR][JC];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int r = 0; r < RR; ++r) {
+        const uint32_t base = R.down + (uint32_t)(b0 + q0 + r) * (uint32_t)rb;
+#pragma unroll
+        for (int j = 0; j < JC; ++j) {
+          const int i = (j0 + j) * 64 + lane;
+          const bool in = q0 + r < nr && i < pieces;
+          wv[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
+          sc[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? R.ds + (uint32_t)(b0 + q0 + r) * (uint32_t)pieces + i : kOOB) : 0;
+        }
+      }
+    };
+    load(0);
+    for (int tb = 0; tb < n; tb += TB) {
+      Acc acc[TB][RR];
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int r = 0; r < RR; ++r) acc[t][r] = 0;
+      for (int j0 = 0; j0 < J; j0 += JC) {
+        if (J > JC && (j0 > 0 || tb > 0)) load(j0);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          if (tb + t >= n) continue;
+          const int pair = P.pair[first + tb + t];
+          const uint4* row = LV ? sh + (size_t)pair * pieces * NV
+                                : reinterpret_cast<const uint4*>(FMT == FT_W_I8
+                                                                     ? (const void*)(p.hq + (size_t)pair * p.f)
+                                                                     : (const void*)(static_cast<const float*>(p.h) + (size_t)pair * p.f));
+#pragma unroll
+          for (int j = 0; j < JC; ++j) {
+            const int i = (j0 + j) * 64 + lane;
+            if (i >= pieces) continue;
+            uint4 v[NV];
+            load_parts<NV, LV>(v, row, pieces, i);
+#pragma unroll
+            for (int r = 0; r < RR; ++r) acc[t][r] = piece_dot<FMT, true, NV>(wv[r][j], sc[r][j], v, acc[t][r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        if (tb + t >= n) continue;
+        const int pair = P.pair[first + tb + t];
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+          const Acc a = wave_total(acc[t][r]);
+          if (lane != 0 || q0 + r >= nr) continue;
+          float v;
+          if constexpr (FMT == FT_W_I8)
+            v = i8_value(a, reinterpret_cast<const float*>(rp + R.ds)[b0 + q0 + r], p.hs[pair]);
+          else
+            v = a;
+          out[pair * kDownRows + q0 + r] = v;
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, int JC, int RR>
+__global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs p) {
+  __shared__ Plan P;
+  extern __shared__ uint4 vec[];  // results [pairs][kDownRows], then rows of h
+  const int n = p.T * p.k;
+  float* out = reinterpret_cast<float*>(vec);
+  uint4* sh = vec + n * kDownRows / 4;
+  if ((int)threadIdx.x < n) {
+    P.id[threadIdx.x] = p.idx[threadIdx.x];
+    P.gate[threadIdx.x] = p.gates[threadIdx.x];
+  }
+  if (p.lds_vec) {
+    constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND;
+    stage_rows<NV>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / E);
+  }
+  __syncthreads();
+  make_plan(P, p);
+  if (p.lds_vec)
+    down_units<FMT, JC, RR, true>(p, P, sh, out);
+  else
+    down_units<FMT, JC, RR, false>(p, P, nullptr, out);
+  __syncthreads();
+  const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
+  for (int i = threadIdx.x; i < p.T * nr; i += NT) {
+    const int t = i / nr, r = i - t * nr;
+    const size_t at = (size_t)t * p.d + b0 + r;
+    float s = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const int q = t * p.k + j;
+      if (P.grp[q] >= 0) s = fmaf(P.gate[q], out[q * kDownRows + r], s);
+    }
+    if (p.y_f32) {
+      if (p.res) s += static_cast<const float*>(p.res)[at];
+      static_cast<float*>(p.y)[at] = s;
+    } else {
+      if (p.res) s += to_f32<false>(static_cast<const uint16_t*>(p.res)[at]);
+      static_cast<uint16_t*>(p.y)[at] = (uint16_t)pack2<false>(s, 0.0f);
+    }
+  }
+}
+
+// ---- launches -----------------------------------------------------------------------------------
+constexpr int kUnits = 256;           // compute units
+constexpr size_t kVecLds = 96 << 10;  // most of a block's LDS for rows of x or h
+
+template <int FMT, int JU, int RG, int JD, int RR>
+int moe_go(MoeArgs A, hipStream_t s) {
+  const size_t P = (size_t)A.T * A.k;
+  const size_t xb = (size_t)A.T * A.d * (FMT == FT_W_I8 ? 1 : 2);
+  A.lds_vec = xb <= kVecLds;
+  hipLaunchKernelGGL((moe_up_kernel<FMT, JU, RG>), dim3(kUnits), dim3(NT), A.lds_vec ? xb : 0, s, A);
+  if (int st = launched("moe_up_kernel")) return st;
+  if (FMT == FT_W_I8)
+    if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s)) return st;
+  const size_t hb = P * A.f * (FMT == FT_W_I8 ? 1 : 4), ob = P * kDownRows * 4;
+  A.lds_vec = hb <= kVecLds - ob;
+  A.rows = (A.d + kUnits - 1) / kUnits;
+  if (A.rows > kDownRows) A.rows = kDownRows;
+  hipLaunchKernelGGL((moe_down_kernel<FMT, JD, RR>), dim3((unsigned)((A.d + A.rows - 1) / A.rows)), dim3(NT),
+                     ob + (A.lds_vec ? hb : 0), s, A);
+  return launched("moe_down_kernel");
+}
+
+}  // namespace
+
+int launch_moe_layer(const MoeLayer& L, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (L.T <= 0) return FT_OK;
+  // as the decode router: all tokens a wavefront up to 8, a few tens of blocks
+  const int tt = L.T == 1 ? 1 : L.T <= 4 ? 4 : 8, te = L.T == 1 ? (L.E <= 64 ? 1 : 2) : (L.E <= 128 ? 1 : 2);
+  const dim3 grid((unsigned)((L.E + 4 * te - 1) / (4 * te)), (unsigned)((L.T + tt - 1) / tt));
+  auto logits = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, L.x, L.w_router, L.T, L.d, L.E, L.logits); };
+  if (tt == 1)
+    te == 1 ? logits(moe_logits_kernel<1, 1>) : logits(moe_logits_kernel<1, 2>);
+  else if (tt == 4)
+    te == 1 ? logits(moe_logits_kernel<4, 1>) : logits(moe_logits_kernel<4, 2>);
+  else
+    te == 1 ? logits(moe_logits_kernel<8, 1>) : logits(moe_logits_kernel<8, 2>);
+  if (int st = launched("moe_logits_kernel")) return st;
+  MoeArgs A{};
+  A.x = L.x;
+  A.logits = L.logits;
+  A.allowed = L.allowed;
+  A.rec = L.records;
+  A.slot_of = L.slot_of;
+  A.T = L.T;
+  A.d = L.d;
+  A.f = L.d_ff;
+  A.E = L.E;
+  A.k = L.k;
+  A.n_slots = L.n_slots;
+  A.S = L.S;
+  A.idx = L.idx;
+  A.gates = L.gates;
+  A.xq = L.xq;
+  A.xs = L.xs;
+  A.hq = L.hq;
+  A.hs = L.hs;
+  A.h = L.h;
+  A.res = L.res;
+  A.y = L.y;
+  A.y_f32 = L.y_f32;
+  if (L.fmt == FT_W_I8) {
+    if (int st = launch_i8_quant(L.x, L.d, L.T, L.d, false, L.xq, L.xs, stream)) return st;
+    return moe_go<FT_W_I8, 4, 2, 2, 8>(A, s);
+  }
+  if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 2, 2, 1, 8>(A, s);
+  return moe_go<FT_W_BF16, 8, 2, 4, 4>(A, s);
+}
+
+}  // namespace ft

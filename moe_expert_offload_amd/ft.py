@@ -27,6 +27,7 @@ FT_WOVERLAP_OFF = 1
 FT_PLAN_CAP = 512
 FT_W_BF16 = 0
 FT_W_MXFP4 = 1
+FT_W_I8 = 2
 FT_T_BF16 = 0
 FT_T_FP16 = 1
 FT_T_FP32 = 2
@@ -55,7 +56,7 @@ EXPORTED = [
     "ft_gated_ffn_workspace_bytes", "ft_gated_ffn_saved_bytes", "ft_gated_ffn", "ft_gated_ffn_bwd_workspace_bytes",
     "ft_gated_ffn_bwd", "ft_act8_pack", "ft_act8_unpack", "ft_w4_gemv", "ft_w4_gated_ffn_workspace_bytes",
     "ft_w4_gated_ffn", "ft_i8_quant", "ft_i8_gemm_workspace_bytes", "ft_i8_gemm", "ft_i8_gated_ffn_workspace_bytes",
-    "ft_i8_gated_ffn",
+    "ft_i8_gated_ffn", "ft_moe_layer_workspace_bytes", "ft_moe_layer",
 ]
 
 
@@ -195,6 +196,8 @@ def lib():
             "ft_i8_gated_ffn_workspace_bytes": (Z, [I, I, I]),
             "ft_i8_gated_ffn": (C.c_int, [P, L64, I, I, I, C.POINTER(ft_i8_matrix), C.POINTER(ft_i8_matrix),
                                           C.POINTER(ft_i8_matrix), P, L64, P, L64, I, P, Z, P]),
+            "ft_moe_layer_workspace_bytes": (Z, [C.POINTER(ft_shape), I]),
+            "ft_moe_layer": (C.c_int, [C.POINTER(ft_shape), P, I, P, P, P, I, P, P, P, I, P, P, P, Z, P]),
             "ft_combine": (C.c_int, [P, P, P, P, I, I, I, P, P]),
             "ft_expert_cache_lookup": (C.c_int, [P, I, P, I, C.POINTER(ft_plan)]),
             "ft_expert_cache_fill": (C.c_int, [P, C.POINTER(ft_plan), P, P, P]),
@@ -527,6 +530,17 @@ def ft_i8_gated_ffn(x, ldx, T, dtype, act, gate, up, down, residual, ldr, y, ldy
     return _check("ft_i8_gated_ffn", lib().ft_i8_gated_ffn(
         _ptr(x), ldx, T, dtype, act, C.byref(gate), C.byref(up), C.byref(down), _ptr(residual), ldr, _ptr(y), ldy,
         y_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def ft_moe_layer_workspace_bytes(shape, T):
+    return lib().ft_moe_layer_workspace_bytes(C.byref(shape), T)
+
+
+def ft_moe_layer(shape, x, T, w_router, allowed, records, n_slots, slot_of, residual, y, y_dtype, idx, gates, workspace,
+                 workspace_bytes, stream=None):
+    return _check("ft_moe_layer", lib().ft_moe_layer(
+        C.byref(shape), _ptr(x), T, _ptr(w_router), _ptr(allowed), _ptr(records), n_slots, _ptr(slot_of), _ptr(residual),
+        _ptr(y), y_dtype, _ptr(idx), _ptr(gates), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def ft_combine(out, inv, gates, cpu_partial, T, k, d, y, stream=None):
