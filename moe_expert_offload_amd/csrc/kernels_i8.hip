@@ -80,15 +80,6 @@ struct I8Args {
   int* part;  // sums of pieces
 };
 
-// Four scales from n on; those past the end are not used.
-__device__ __forceinline__ float4 scales4(const float* s, int n, int N) {
-  struct __attribute__((packed, aligned(4))) Any {
-    float4 v;
-  };
-  if (n + 4 <= N) return reinterpret_cast<const Any*>(s + n)->v;
-  return make_float4(s[min(n, N - 1)], s[min(n + 1, N - 1)], s[min(n + 2, N - 1)], s[min(n + 3, N - 1)]);
-}
-
 template <bool H>
 __device__ __forceinline__ void store1(const I8Args& p, int64_t m, int n, float v) {
   if (p.c_f32) {
@@ -166,22 +157,64 @@ __global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
 }
 
 // ---- many rows: tiles -------------------------------------------------------------------
-// What becomes of one 32-row piece of a wave's sums: c0 and c1 are its 32x32 results at channels nb0 and nb1
-// (kGateUp: gate and up of the same ones).  The lane holds token m, and in quad q the channels
-// 8 q + 4 hi + 0..3 of each.
-template <int MODE, bool H>
-__device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0, const i32x16_t& c1, int m, int nb0,
-                                            int nb1, int hi) {
+// A tile's scales: of its BM tokens, then of its BN channels (kGateUp: BN / 2 of gate, then of up); those past
+// the ends are not used.  Read in the epilogue from LDS: from memory, each group of four waited for its
+// own round trip (8192 x 4096 x 4096: 172 us, so 145 us).
+template <int MODE, int BM, int BN, int THREADS>
+__device__ __forceinline__ void stage_scales(const I8Args& p, float* s, int m0, int n0) {
+  for (int i = threadIdx.x; i < BM + BN; i += THREADS) {
+    float v;
+    if (i < BM) {
+      v = p.ta[min(m0 + i, p.M - 1)];
+    } else if (MODE == kGateUp) {
+      const int c = i - BM;
+      v = c < BN / 2 ? p.sb[min(n0 + c, p.N - 1)] : p.sb2[min(n0 + c - BN / 2, p.N - 1)];
+    } else {
+      v = p.sb[min(n0 + i - BM, p.N - 1)];
+    }
+    s[i] = v;
+  }
+}
+
+// The same by one load of each wave straight into LDS, so that nobody waits for it by itself.
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ void load_scales(const I8Args& p, uint32_t lds, int m0, int n0, int wave, int lane) {
+  const int i = wave * 64;
+  const float* src;
+  int left;
+  if (i < BM) {
+    src = p.ta + m0 + i;
+    left = p.M - m0 - i;
+  } else if (i < BM + BN) {
+    const int c = i - BM;
+    const bool up = MODE == kGateUp && c >= BN / 2;
+    const int n = n0 + (up ? c - BN / 2 : c);
+    src = (up ? p.sb2 : p.sb) + n;
+    left = p.N - n;
+  } else {
+    return;
+  }
+  lds_load4(rsrc_of(src), lane < left ? (uint32_t)lane * 4 : kOOB, 0, lds + i * 4);
+}
+
+// What becomes of one 32-row piece of a wave's sums: c0 and c1 are its 32x32 results at channels n0 + b0 and
+// n0 + b1 (kGateUp: gate and up of the same ones).  The lane holds row `r` of the tile, and in quad q the
+// channels 8 q + 4 hi + 0..3 of each.  ts: the tile's scales, of BM tokens first.
+template <int MODE, bool H, int BM, int BN>
+__device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0, const i32x16_t& c1, const float* scales,
+                                            int m0, int r, int n0, int b0, int b1, int hi) {
+  const int m = m0 + r;
   const bool mok = m < p.M;
-  const float ts = p.ta[mok ? m : p.M - 1];
+  const float ts = scales[r];
+  const float4* cs = reinterpret_cast<const float4*>(scales + BM);
   if constexpr (MODE == kGateUp) {
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int n = nb0 + 8 * (q + e) + 4 * hi, k = 4 * (q + e);
-        const float4 sg = scales4(p.sb, n, p.N), su = scales4(p.sb2, n, p.N);
+        const int c = (b0 + 8 * (q + e) + 4 * hi) >> 2, k = 4 * (q + e);
+        const float4 sg = cs[c], su = cs[c + BN / 8];
         const float h0 = act_f(i8_value(c0[k], sg.x, ts), p.act) * i8_value(c1[k], su.x, ts);
         const float h1 = act_f(i8_value(c0[k + 1], sg.y, ts), p.act) * i8_value(c1[k + 1], su.y, ts);
         const float h2 = act_f(i8_value(c0[k + 2], sg.z, ts), p.act) * i8_value(c1[k + 2], su.z, ts);
@@ -191,20 +224,20 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
       }
       swap_halves(w[0], w[2]);
       swap_halves(w[1], w[3]);
-      const int n = nb0 + 8 * q + 8 * hi;  // N % 16 == 0
+      const int n = n0 + b0 + 8 * q + 8 * hi;  // N % 16 == 0
       if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int nb = j ? nb1 : nb0;
+      const int b = j ? b1 : b0;
       const i32x16_t& c = j ? c1 : c0;
 #pragma unroll
       for (int q = 0; q < 4; q += 2) {
-        float v[8];  // after the exchange: channels nb + 8 (q + hi) .. + 7
+        float v[8];  // after the exchange: channels b + 8 (q + hi) .. + 7
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float4 sc = scales4(p.sb, nb + 8 * (q + e) + 4 * hi, p.N);
+          const float4 sc = cs[(b + 8 * (q + e) + 4 * hi) >> 2];
           const int k = 4 * (q + e);
           v[4 * e] = i8_value(c[k], sc.x, ts);
           v[4 * e + 1] = i8_value(c[k + 1], sc.y, ts);
@@ -218,7 +251,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
           v[e] = __uint_as_float(x);
           v[4 + e] = __uint_as_float(y);
         }
-        const int n = nb + 8 * q + 8 * hi;
+        const int n = n0 + b + 8 * q + 8 * hi;
         if (!mok || n >= p.N) continue;
         if (!p.wide) {
 #pragma unroll
@@ -297,6 +330,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   constexpr bool GU = MODE == kGateUp;
   constexpr int SBYTES = 32768;
   __shared__ __attribute__((aligned(1024))) uint8_t sm[2 * SBYTES];
+  __shared__ __attribute__((aligned(16))) float scales[256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, hi = lane >> 5, l31 = lane & 31;
   const int stages = (p.K + 127) >> 7;
@@ -337,6 +371,7 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   i32x16_t acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
+  load_scales<MODE, 128, 128>(p, lds_addr(scales), m0, n0, wave, lane);
   if (s_begin < s_end) load_stage(s_begin);
   for (int s = s_begin; s < s_end; ++s) {
     // this wave's loads of stage s have landed; past the barrier everyone's have, and nobody
@@ -366,8 +401,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
     if (p.rest) {
       store_part(p.part + (size_t)lb * (128 * 128) + (wave * 2 + i) * 2048, acc[i], lane);
     } else {
-      const int nb = n0 + wn * (GU ? 32 : 64);
-      i8_epilogue<MODE, H>(p, acc[i][0], acc[i][1], m0 + wm * 64 + i * 32 + l31, nb, nb + 32, hi);
+      const int b = wn * (GU ? 32 : 64);
+      i8_epilogue<MODE, H, 128, 128>(p, acc[i][0], acc[i][1], scales, m0, wm * 64 + i * 32 + l31, n0, b, b + 32, hi);
     }
   }
 }
@@ -377,14 +412,17 @@ template <int MODE, bool H>
 __global__ __launch_bounds__(256) void i8_join128_kernel(I8Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, t = blockIdx.x >> 1, i = blockIdx.x & 1;
+  __shared__ __attribute__((aligned(16))) float scales[256];
   const TilePos tp = tile_pos(p, t);
-  const int m = tp.m * 128 + wm * 64 + i * 32;
-  if (m >= p.M) return;
+  const int m0 = tp.m * 128, n0 = tp.n * (MODE == kGateUp ? 64 : 128), r = wm * 64 + i * 32;
+  stage_scales<MODE, 128, 128, 256>(p, scales, m0, n0);
+  __syncthreads();
+  if (m0 + r >= p.M) return;
   i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
   for (int b = 0; b < p.blocks; ++b)
     add_part(acc, p.part + (size_t)(t * p.blocks + b) * (128 * 128) + (wave * 2 + i) * 2048, lane);
-  const int nb = tp.n * (MODE == kGateUp ? 64 : 128) + wn * (MODE == kGateUp ? 32 : 64);
-  i8_epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 32, lane >> 5);
+  const int c = wn * (MODE == kGateUp ? 32 : 64);
+  i8_epilogue<MODE, H, 128, 128>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, c, c + 32, lane >> 5);
 }
 
 // 128 MH x 256 tiles, 8 waves, each 64 rows and 32 channels of every 128 x 128 quarter.  A stage is regions of
@@ -407,6 +445,7 @@ __global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
   enum { A0 = 0, B0 = REG, B1 = 2 * REG, A1 = 3 * REG, STAGE = (2 + MH) * REG, PLACES = MH == 2 ? 2 : 3 };
   __shared__ __attribute__((aligned(1024))) uint8_t sm[PLACES * STAGE];
   constexpr int BM = 128 * MH, PART = BM * 256;  // rows of a tile, numbers of its sums
+  __shared__ __attribute__((aligned(16))) float scales[BM + 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3, hi = lane >> 5, l31 = lane & 31;
   const int stages = (p.K + 127) >> 7;
@@ -511,6 +550,7 @@ __global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
     auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
 
     if (s_begin < s_end) {
+      load_scales<MODE, BM, 256>(p, lds_addr(scales), m0, n0, wave, lane);  // the oldest: waited for with the first stage
       load_a(s_begin, 0, 0);
       load_b(s_begin, 0, 0);
       load_b(s_begin, 1, 0);
@@ -574,9 +614,10 @@ __global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
       if (slot >= 0) {
         if (m < p.M) store_part(p.part + (size_t)slot * PART + (wave * 2 * MH + i) * 2048, acc[i], lane);
       } else {
-        i8_epilogue<MODE, H>(p, acc[i][0], acc[i][1], m + l31, n0 + wn * 32, n0 + wn * 32 + 128, hi);
+        i8_epilogue<MODE, H, BM, 256>(p, acc[i][0], acc[i][1], scales, m0, m - m0 + l31, n0, wn * 32, wn * 32 + 128, hi);
       }
     }
+    if (at < end) __syncthreads();  // the scales are no longer read
   }
 }
 
@@ -590,12 +631,14 @@ __global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
   const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
   if (first == last) return;  // one block had it all
   const TilePos tp = tile_pos(p, p.whole + t);
-  const int m = tp.m * 128 * MH + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
-  if (m >= p.M) return;
+  __shared__ __attribute__((aligned(16))) float scales[MH * 128 + 256];
+  const int m0 = tp.m * 128 * MH, n0 = tp.n * (MODE == kGateUp ? 128 : 256), r = (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+  stage_scales<MODE, MH * 128, 256, 512>(p, scales, m0, n0);
+  __syncthreads();
+  if (m0 + r >= p.M) return;
   i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
   for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * (MH * 128 * 256) + (wave * 2 * MH + i) * 2048, lane);
-  const int nb = tp.n * (MODE == kGateUp ? 128 : 256) + wn * 32;
-  i8_epilogue<MODE, H>(p, acc[0], acc[1], m + (lane & 31), nb, nb + 128, lane >> 5);
+  i8_epilogue<MODE, H, MH * 128, 256>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, wn * 32, wn * 32 + 128, lane >> 5);
 }
 
 // ---- launches -------------------------------------------------------------------------
