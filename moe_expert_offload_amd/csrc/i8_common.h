@@ -91,6 +91,39 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return v;
 }
 
+// One row of n elements to codes and its scale by ROWT threads, 64 or a whole block of 256 (`red`: 4 words of LDS). The row is
+// held in registers between its largest element and its codes, NP pieces of 8 elements a thread; what is
+// longer is read again.  codes may lie in LDS.
+template <bool H, int ROWT, int NP>
+__device__ __forceinline__ void quant_row(const uint16_t* src, int n, int8_t* codes, float* scale, uint32_t* red) {
+  const int at = threadIdx.x % ROWT, pieces = n >> 3;
+  const uint4* q = reinterpret_cast<const uint4*>(src);
+  uint4 v[NP];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) v[i] = at + i * ROWT < pieces ? q[at + i * ROWT] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) m = amax4(v[i], m);
+  for (int p = at + NP * ROWT; p < pieces; p += ROWT) m = amax4(q[p], m);
+  m = wave_umax(m);
+  if constexpr (ROWT > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = max(max(red[0], red[1]), max(red[2], red[3]));
+  }
+  const RowScale r = row_scale<H>(m);
+  uint2* d = reinterpret_cast<uint2*>(codes);
+  auto put = [&](int p, const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    d[p] = row_codes8<H>(w, r);
+  };
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (at + i * ROWT < pieces) put(at + i * ROWT, v[i]);
+  for (int p = at + NP * ROWT; p < pieces; p += ROWT) put(p, q[p]);
+  if (at == 0) *scale = r.scale;
+}
+
 // A product's value: the whole-number sum times the channel's scale, then the token's.
 __device__ __forceinline__ float i8_value(int acc, float channel, float token) { return ((float)acc * channel) * token; }
 

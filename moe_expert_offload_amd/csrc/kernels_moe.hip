@@ -14,6 +14,8 @@
 // Records (bf16, MXFP4) as in include/ft.h; MXFP4 weights are dequantised exactly and applied to the bf16
 // x and the fp32 h.  8-bit records: x and h in 8 bits as ft_i8_quant gives them (h rounded to bf16 before),
 // whole-number sums, as the blocks of kernels_i8.hip.
+#include <climits>
+
 #include "i8_common.h"
 #include "router_device.h"
 
@@ -23,7 +25,7 @@ using namespace dev;
 
 namespace {
 
-constexpr int NT = 512, NW = NT / 64;  // threads and wavefronts of a block
+constexpr int NT = 1024, NW = NT / 64;  // threads and wavefronts of a block, one block a compute unit
 
 struct MoeArgs {
   const uint16_t* x;
@@ -35,8 +37,8 @@ struct MoeArgs {
   size_t S;
   int32_t* idx;
   float* gates;
-  const int8_t* xq;  // 8-bit records: x in 8 bits
-  const float* xs;
+  int8_t* xq;  // 8-bit records: x in 8 bits
+  float* xs;
   int8_t* hq;  // h in 8 bits
   float* hs;
   void* h;  // [T k, f]: fp32, 8-bit records bf16
@@ -143,11 +145,50 @@ __device__ __forceinline__ typename Fmt<FMT>::Acc piece_dot(uint4 w, uint32_t sc
   }
 }
 
-__device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
-__device__ __forceinline__ int wave_total(int v) {
+// Sums over the wavefront of N values of each lane at once: halves of lanes that hold one value's parts take on
+// another's.  The lane gets in v[0] the total of value total_of<N>(lane) (of 8: v[0] that of the first four,
+// v[1] that of the last).
+template <int N>
+__device__ __forceinline__ int total_of(int lane) {
+  return N == 1 ? 0 : N == 2 ? lane >> 5 : ((lane >> 4) & 1) * 2 + (lane >> 5);
+}
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp_of(T v) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <class T>
+__device__ __forceinline__ T row_total(T v) {  // over 16 lanes
+  v += dpp_of<0xb1>(v);   // quad_perm [1,0,3,2]
+  v += dpp_of<0x4e>(v);   // quad_perm [2,3,0,1]
+  v += dpp_of<0x141>(v);  // row_half_mirror
+  return v + dpp_of<0x140>(v);  // row_mirror
+}
+template <class T>
+__device__ __forceinline__ T join32(T a, T b) {  // lanes 0..31: a's, 32..63: b's
+  const u32x2_t r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = r.x, y = r.y;
+  return __builtin_bit_cast(T, x) + __builtin_bit_cast(T, y);
+}
+template <class T>
+__device__ __forceinline__ T join16(T a, T b) {  // rows 0 and 2: a's, 1 and 3: b's
+  const u32x2_t r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = r.x, y = r.y;
+  return __builtin_bit_cast(T, x) + __builtin_bit_cast(T, y);
+}
+template <int N, class T>
+__device__ __forceinline__ void wave_totals(T (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
+  if constexpr (N == 1) {
+    const T a = row_total(v[0]), h = join32(a, a);
+    v[0] = join16(h, h);
+  } else if constexpr (N == 2) {
+    const T a = row_total(join32(v[0], v[1]));
+    v[0] = join16(a, a);
+  } else {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
-  return v;
+    for (int q = 0; q < N / 4; ++q)
+      v[q] = row_total(join16(join32(v[4 * q], v[4 * q + 1]), join32(v[4 * q + 2], v[4 * q + 3])));
+  }
 }
 
 // A record's parts (byte offsets).
@@ -177,67 +218,74 @@ __device__ __forceinline__ int row_bytes(int n) {
 struct Plan {
   int32_t id[FT_PLAN_CAP];  // expert of a pair
   float gate[FT_PLAN_CAP];
-  int32_t grp[FT_PLAN_CAP];    // its group, -1: left out (no expert, or none of the given ones)
-  int32_t slot[FT_PLAN_CAP];   // of a group
+  int32_t grp[FT_PLAN_CAP];      // its group, -1: left out (no expert, or none of the given ones)
+  int32_t slot[FT_PLAN_CAP];     // of a group
   int32_t off[FT_PLAN_CAP + 1];  // first of a group's pairs in `pair`
-  int32_t pair[FT_PLAN_CAP];   // pairs by (group, pair)
-  int32_t wave_first[NW];
-  int32_t n_groups, n_pairs;
+  int32_t pair[FT_PLAN_CAP];     // pairs by group
+  int32_t first[FT_E_MAX];       // an expert's first pair, then its group
+  int32_t count[FT_PLAN_CAP];
+  int32_t wave_sum[NW];
 };
 
-// Groups in the order of their first pair.  id and gate are set; all threads of the block.
-__device__ void make_plan(Plan& P, const MoeArgs& p) {
-  const int n = p.T * p.k, i = threadIdx.x, lane = i & 63, wave = i >> 6;
-  int id = -1, slot = -1, before = 0;
+// Exclusive prefix sums over the block's threads of at most 16 bits' worth each; returns this thread's.
+__device__ __forceinline__ int block_prefix(int v, int32_t* wave_sums, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int in = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(in, o, WAVE);
+    if (lane >= o) in += t;
+  }
+  if (lane == 63) wave_sums[wave] = in;
+  __syncthreads();
+  int base = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    base += w < wave ? wave_sums[w] : 0;
+    total += wave_sums[w];
+  }
+  __syncthreads();
+  return base + in - v;
+}
+
+// Groups in the order of their first pair; pairs within a group in any order (each one's results are its own).
+// id and gate are set; all threads of the block.  Returns the number of groups.
+__device__ int make_plan(Plan& P, const MoeArgs& p) {
+  const int n = p.T * p.k, i = threadIdx.x;
+  for (int e = i; e < p.E; e += NT) P.first[e] = INT_MAX;
+  if (i < FT_PLAN_CAP) P.count[i] = 0;
+  __syncthreads();
+  int id = -1, slot = -1;
   if (i < n) {
     id = P.id[i];
     if (id >= 0 && id < p.E) {
       slot = p.slot_of ? p.slot_of[id] : id;
       if (slot < 0 || slot >= p.n_slots) slot = -1;
+      if (slot >= 0) atomicMin(&P.first[id], i);
     }
-    for (int q = 0; q < i; ++q) before += P.id[q] == id;
   }
-  const bool first = slot >= 0 && before == 0;
-  const unsigned long long m = __ballot(first);
-  if (lane == 0) P.wave_first[wave] = __popcll(m);
   __syncthreads();
-  int rank = __popcll(m & ((1ull << lane) - 1)), total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    rank += w < wave ? P.wave_first[w] : 0;
-    total += P.wave_first[w];
-  }
-  if (i < n) P.grp[i] = -1;
+  const bool first = slot >= 0 && P.first[id] == i;
+  int groups;
+  const int rank = block_prefix(first, P.wave_sum, groups);
   if (first) {
-    P.grp[i] = rank;
+    P.first[id] = rank;
     P.slot[rank] = slot;
   }
-  if (i == 0) P.n_groups = total;
   __syncthreads();
-  // the other pairs of an expert take its first one's group
-  int grp = i < n ? P.grp[i] : -1;
-  if (i < n && slot >= 0 && !first)
-    for (int q = 0; q < i; ++q)
-      if (P.id[q] == id) {
-        grp = P.grp[q];
-        break;
-      }
-  __syncthreads();
+  int at = 0;
+  const int grp = slot >= 0 ? P.first[id] : -1;
   if (i < n) P.grp[i] = grp;
+  if (grp >= 0) at = atomicAdd(&P.count[grp], 1);
   __syncthreads();
-  // pairs of groups before this thread's (as a pair: its group; as a group: i)
-  int base = 0, off = 0, all = 0;
-  for (int q = 0; q < n; ++q) {
-    const int g = P.grp[q];
-    base += g >= 0 && g < grp;
-    off += g >= 0 && g < i;
-    all += g >= 0;
-  }
-  if (grp >= 0) P.pair[base + before] = i;
-  if (i <= total) P.off[i] = off;
-  if (i == 0) P.n_pairs = all;
-  if (i == 0 && total == NT) P.off[total] = all;
+  int pairs;
+  const int off = block_prefix(i < groups ? P.count[i] : 0, P.wave_sum, pairs);
+  if (i <= groups) P.off[i] = off;
   __syncthreads();
+  if (grp >= 0) P.pair[P.off[grp] + at] = i;
+  __syncthreads();
+  return groups;
 }
 
 // Rows of x (h): `rows` rows of `pieces` pieces of NV 16-byte parts.  In LDS the parts of a row lie in planes (part
@@ -260,59 +308,75 @@ __device__ __forceinline__ void load_parts(uint4 (&v)[NV], const uint4* row, int
   for (int q = 0; q < NV; ++q) v[q] = row[LV ? q * pieces + i : i * NV + q];
 }
 
-// ---- logits ---------------------------------------------------------------------------------
+// ---- logits (8-bit records: and x in 8 bits, a row by each of the last blocks) ---------------
 template <int TT, int TE>
-__global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                                                         int T, int d, int E, float* __restrict__ logits) {
-  router_logits_wave<TT, TE>(x, w, T, d, E, blockIdx.y * TT, (blockIdx.x * 4 + (threadIdx.x >> 6)) * TE, threadIdx.x & 63,
-                             logits);
+__global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs p, const uint16_t* __restrict__ w, float* logits, int eb,
+                                                         int blocks) {
+  __shared__ uint32_t red[4];
+  const int b = blockIdx.x;
+  if (b < blocks)
+    router_logits_wave<TT, TE>(p.x, w, p.T, p.d, p.E, b / eb * TT, (b % eb * 4 + (threadIdx.x >> 6)) * TE, threadIdx.x & 63, logits);
+  else
+    quant_row<false, 256, 2>(p.x + (size_t)(b - blocks) * p.d, p.d, p.xq + (size_t)(b - blocks) * p.d, p.xs + (b - blocks), red);
+}
+
+// Tokens wave, wave + NW, ... one at a time (two of 1024 experts' logits would not fit the registers).
+template <int NS>
+__device__ __forceinline__ void topk_rows(const MoeArgs& p, Plan& P, int lane, int wave) {
+  for (int t = wave; t < p.T; t += NW) {
+    TopkIn<NS> in;
+    topk_load<NS>(p.logits + (size_t)t * p.E, p.allowed ? p.allowed + (size_t)t * p.E : nullptr, p.E, lane, in);
+    topk_pick<NS>(in, p.k, lane, P.id + t * p.k, P.gate + t * p.k);
+  }
 }
 
 // ---- gate/up ----------------------------------------------------------------------------------
 // A wavefront takes units of RG row pairs (gate and up), a consecutive share of all of them.
 template <int FMT, int JC, int RG, bool LV>
-__device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const uint4* sx) {
-  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU, TB = 4;
+__device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, int groups, const uint4* sx) {
+  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU, TB = 2;
   typedef typename Fmt<FMT>::Acc Acc;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Rec R = rec_of<FMT>(p.d, p.f);
   const int pieces = p.d / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.d);
   const int per_group = (p.f + RG - 1) / RG;
-  const int64_t units = (int64_t)P.n_groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
+  const int64_t units = (int64_t)groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
   const int u_end = (int)(units * (w + 1) / nw);
   for (int u = (int)(units * w / nw); u < u_end; ++u) {
     const int g = u / per_group, r0 = (u - g * per_group) * RG;
-    const auto rec = buf_rsrc(p.rec + (size_t)P.slot[g] * p.S, (uint32_t)p.S);
-    const int first = P.off[g], n = P.off[g + 1] - first;
-    uint4 wv[2 * RG][JC];
-    uint32_t sc[2 * RG][JC];
+    const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(P.slot[g]) * p.S;
+    const auto rec = buf_rsrc(rp, (uint32_t)p.S);
+    const int first = __builtin_amdgcn_readfirstlane(P.off[g]), n = __builtin_amdgcn_readfirstlane(P.off[g + 1]) - first;
+    uint4 wg[RG][JC], wu[RG][JC];
+    uint32_t sg[RG][JC], su[RG][JC];
     auto load = [&](int j0) {
 #pragma unroll
-      for (int r = 0; r < 2 * RG; ++r) {
-        const int row = r0 + (r >> 1);
-        const uint32_t base = (r & 1 ? R.up : 0u) + (uint32_t)row * (uint32_t)rb;
+      for (int r = 0; r < RG; ++r) {
+        const uint32_t row = r0 + r, base = row * (uint32_t)rb, sb = row * (uint32_t)pieces;
 #pragma unroll
         for (int j = 0; j < JC; ++j) {
           const int i = (j0 + j) * 64 + lane;
-          const bool in = row < p.f && i < pieces;
-          wv[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
-          sc[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? (r & 1 ? R.us : R.gs) + (uint32_t)row * (uint32_t)pieces + i : kOOB) : 0;
+          const bool in = (int)row < p.f && i < pieces;
+          wg[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
+          wu[r][j] = buf_ld16(rec, in ? R.up + base + 16u * i : kOOB);
+          sg[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? R.gs + sb + i : kOOB) : 0;
+          su[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? R.us + sb + i : kOOB) : 0;
         }
       }
     };
     load(0);
     for (int tb = 0; tb < n; tb += TB) {
-      Acc acc[TB][2 * RG];
+      Acc ag[TB][RG], au[TB][RG];
 #pragma unroll
       for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int r = 0; r < 2 * RG; ++r) acc[t][r] = 0;
+        for (int r = 0; r < RG; ++r) ag[t][r] = au[t][r] = 0;
       for (int j0 = 0; j0 < J; j0 += JC) {
         if (J > JC && (j0 > 0 || tb > 0)) load(j0);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           if (tb + t >= n) continue;
-          const int tok = P.pair[first + tb + t] / p.k;
+          const int tok = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]) / p.k;
           const uint4* row = LV ? sx + (size_t)tok * pieces * NV
                                 : reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)(p.xq + (size_t)tok * p.d)
                                                                                 : (const void*)(p.x + (size_t)tok * p.d));
@@ -323,25 +387,30 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
             uint4 v[NV];
             load_parts<NV, LV>(v, row, pieces, i);
 #pragma unroll
-            for (int r = 0; r < 2 * RG; ++r) acc[t][r] = piece_dot<FMT, false, NV>(wv[r][j], sc[r][j], v, acc[t][r]);
+            for (int r = 0; r < RG; ++r) {
+              ag[t][r] = piece_dot<FMT, false, NV>(wg[r][j], sg[r][j], v, ag[t][r]);
+              au[t][r] = piece_dot<FMT, false, NV>(wu[r][j], su[r][j], v, au[t][r]);
+            }
           }
         }
       }
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         if (tb + t >= n) continue;
-        const int pair = P.pair[first + tb + t];
+        const int pair = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]);
+        wave_totals<RG>(ag[t]);
+        wave_totals<RG>(au[t]);
+        constexpr int LANES = RG >= 4 ? 16 : RG == 2 ? 32 : 64;  // that hold one total
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          const Acc a = wave_total(acc[t][2 * r]), b = wave_total(acc[t][2 * r + 1]);
-          const int row = r0 + r;
-          if (lane != 0 || row >= p.f) continue;
+        for (int q = 0; q < (RG + 3) / 4; ++q) {
+          const int row = r0 + 4 * q + total_of<RG>(lane);
+          if (lane % LANES != 0 || row >= p.f) continue;
           if constexpr (FMT == FT_W_I8) {
-            const float *gs = reinterpret_cast<const float*>(p.rec + (size_t)P.slot[g] * p.S + R.gs) + row, ts = p.xs[pair / p.k];
-            const float v = act_f(i8_value(a, gs[0], ts), FT_ACT_SILU) * i8_value(b, gs[p.f], ts);
+            const float *gs = reinterpret_cast<const float*>(rp + R.gs) + row, ts = p.xs[pair / p.k];
+            const float v = act_f(i8_value(ag[t][q], gs[0], ts), FT_ACT_SILU) * i8_value(au[t][q], gs[p.f], ts);
             static_cast<uint16_t*>(p.h)[(size_t)pair * p.f + row] = (uint16_t)pack2<false>(v, 0.0f);
           } else {
-            static_cast<float*>(p.h)[(size_t)pair * p.f + row] = silu(a) * b;
+            static_cast<float*>(p.h)[(size_t)pair * p.f + row] = silu(ag[t][q]) * au[t][q];
           }
         }
       }
@@ -350,7 +419,7 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
 }
 
 template <int FMT, int JC, int RG>
-__global__ __launch_bounds__(NT, 2) void moe_up_kernel(MoeArgs p) {
+__global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
   __shared__ Plan P;
   extern __shared__ uint4 vec[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -358,17 +427,24 @@ __global__ __launch_bounds__(NT, 2) void moe_up_kernel(MoeArgs p) {
     constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU;
     stage_rows<NV>(vec, reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.xq : (const void*)p.x), p.T, p.d / E);
   }
-  topk_tokens(p.logits, p.allowed, p.T, p.E, p.k, wave, NW, lane, P.id, P.gate);
+  if (p.E <= 64)
+    topk_rows<1>(p, P, lane, wave);
+  else if (p.E <= 128)
+    topk_rows<2>(p, P, lane, wave);
+  else if (p.E <= 256)
+    topk_rows<4>(p, P, lane, wave);
+  else
+    topk_rows<16>(p, P, lane, wave);
   __syncthreads();
   if (blockIdx.x == 0 && (int)threadIdx.x < p.T * p.k) {
     p.idx[threadIdx.x] = P.id[threadIdx.x];
     p.gates[threadIdx.x] = P.gate[threadIdx.x];
   }
-  make_plan(P, p);
+  const int groups = make_plan(P, p);
   if (p.lds_vec)
-    up_units<FMT, JC, RG, true>(p, P, vec);
+    up_units<FMT, JC, RG, true>(p, P, groups, vec);
   else
-    up_units<FMT, JC, RG, false>(p, P, nullptr);
+    up_units<FMT, JC, RG, false>(p, P, groups, nullptr);
 }
 
 // ---- down --------------------------------------------------------------------------------------
@@ -377,18 +453,19 @@ __global__ __launch_bounds__(NT, 2) void moe_up_kernel(MoeArgs p) {
 constexpr int kDownRows = 16;
 
 template <int FMT, int JC, int RR, bool LV>
-__device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, const uint4* sh, float* out) {
-  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND, TB = 4;
+__device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, int groups, const uint4* sh, const float* hs,
+                                           float* out) {
+  constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND, TB = 2;
   typedef typename Fmt<FMT>::Acc Acc;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Rec R = rec_of<FMT>(p.d, p.f);
   const int pieces = p.f / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.f);
   const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0), per_group = (nr + RR - 1) / RR;
-  for (int u = wave; u < P.n_groups * per_group; u += NW) {
+  for (int u = wave; u < groups * per_group; u += NW) {
     const int g = u / per_group, q0 = (u - g * per_group) * RR;
-    const uint8_t* rp = p.rec + (size_t)P.slot[g] * p.S;
+    const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(P.slot[g]) * p.S;
     const auto rec = buf_rsrc(rp, (uint32_t)p.S);
-    const int first = P.off[g], n = P.off[g + 1] - first;
+    const int first = __builtin_amdgcn_readfirstlane(P.off[g]), n = __builtin_amdgcn_readfirstlane(P.off[g + 1]) - first;
     uint4 wv[RR][JC];
     uint32_t sc[RR][JC];
     auto load = [&](int j0) {
@@ -416,7 +493,7 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, cons
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           if (tb + t >= n) continue;
-          const int pair = P.pair[first + tb + t];
+          const int pair = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]);
           const uint4* row = LV ? sh + (size_t)pair * pieces * NV
                                 : reinterpret_cast<const uint4*>(FMT == FT_W_I8
                                                                      ? (const void*)(p.hq + (size_t)pair * p.f)
@@ -435,17 +512,17 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, cons
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         if (tb + t >= n) continue;
-        const int pair = P.pair[first + tb + t];
+        const int pair = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]);
+        wave_totals<RR>(acc[t]);
+        constexpr int LANES = RR >= 4 ? 16 : RR == 2 ? 32 : 64;
 #pragma unroll
-        for (int r = 0; r < RR; ++r) {
-          const Acc a = wave_total(acc[t][r]);
-          if (lane != 0 || q0 + r >= nr) continue;
-          float v;
+        for (int q = 0; q < (RR + 3) / 4; ++q) {
+          const int r = q0 + 4 * q + total_of<RR>(lane);
+          if (lane % LANES != 0 || r >= nr) continue;
           if constexpr (FMT == FT_W_I8)
-            v = i8_value(a, reinterpret_cast<const float*>(rp + R.ds)[b0 + q0 + r], p.hs[pair]);
+            out[pair * kDownRows + r] = i8_value(acc[t][q], reinterpret_cast<const float*>(rp + R.ds)[b0 + r], hs[pair]);
           else
-            v = a;
-          out[pair * kDownRows + q0 + r] = v;
+            out[pair * kDownRows + r] = acc[t][q];
         }
       }
     }
@@ -453,8 +530,9 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, cons
 }
 
 template <int FMT, int JC, int RR>
-__global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs p) {
+__global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
   __shared__ Plan P;
+  __shared__ float s_hs[FMT == FT_W_I8 ? FT_PLAN_CAP : 1];
   extern __shared__ uint4 vec[];  // results [pairs][kDownRows], then rows of h
   const int n = p.T * p.k;
   float* out = reinterpret_cast<float*>(vec);
@@ -462,17 +540,24 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs p) {
   if ((int)threadIdx.x < n) {
     P.id[threadIdx.x] = p.idx[threadIdx.x];
     P.gate[threadIdx.x] = p.gates[threadIdx.x];
+    if (FMT == FT_W_I8 && p.hq) s_hs[threadIdx.x] = p.hs[threadIdx.x];
   }
   if (p.lds_vec) {
     constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND;
-    stage_rows<NV>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / E);
+    if (FMT == FT_W_I8 && !p.hq) {  // few pairs: each block makes the codes of h for itself
+      for (int q = threadIdx.x >> 6; q < n; q += NW)
+        quant_row<false, 64, 4>(static_cast<const uint16_t*>(p.h) + (size_t)q * p.f, p.f,
+                                reinterpret_cast<int8_t*>(sh) + (size_t)q * p.f, s_hs + q, nullptr);
+    } else {
+      stage_rows<NV>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / E);
+    }
   }
   __syncthreads();
-  make_plan(P, p);
+  const int groups = make_plan(P, p);
   if (p.lds_vec)
-    down_units<FMT, JC, RR, true>(p, P, sh, out);
+    down_units<FMT, JC, RR, true>(p, P, groups, sh, s_hs, out);
   else
-    down_units<FMT, JC, RR, false>(p, P, nullptr, out);
+    down_units<FMT, JC, RR, false>(p, P, groups, nullptr, s_hs, out);
   __syncthreads();
   const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
   for (int i = threadIdx.x; i < p.T * nr; i += NT) {
@@ -496,22 +581,45 @@ __global__ __launch_bounds__(NT, 2) void moe_down_kernel(MoeArgs p) {
 // ---- launches -----------------------------------------------------------------------------------
 constexpr int kUnits = 256;           // compute units
 constexpr size_t kVecLds = 96 << 10;  // most of a block's LDS for rows of x or h
+// Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
+constexpr size_t kOwnCodes = 32 << 10;
 
-template <int FMT, int JU, int RG, int JD, int RR>
+// A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
+template <int FMT, int W>
 int moe_go(MoeArgs A, hipStream_t s) {
   const size_t P = (size_t)A.T * A.k;
   const size_t xb = (size_t)A.T * A.d * (FMT == FT_W_I8 ? 1 : 2);
+  constexpr int E = Fmt<FMT>::E;
   A.lds_vec = xb <= kVecLds;
-  hipLaunchKernelGGL((moe_up_kernel<FMT, JU, RG>), dim3(kUnits), dim3(NT), A.lds_vec ? xb : 0, s, A);
+  auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(kUnits), dim3(NT), A.lds_vec ? xb : 0, s, A); };
+  const int ju = (A.d / E + 63) / 64;
+  if constexpr (FMT == FT_W_MXFP4) {
+    ju > 1 ? up(moe_up_kernel<FMT, 2, W / 4>) : up(moe_up_kernel<FMT, 1, W / 2>);
+  } else {
+    if (FMT == FT_W_BF16 && ju > 4)
+      up(moe_up_kernel<FT_W_BF16, 8, 1>);
+    else
+      ju > 2 ? up(moe_up_kernel<FMT, 4, W / 8>) : ju > 1 ? up(moe_up_kernel<FMT, 2, W / 4>) : up(moe_up_kernel<FMT, 1, W / 2>);
+  }
   if (int st = launched("moe_up_kernel")) return st;
-  if (FMT == FT_W_I8)
-    if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s)) return st;
   const size_t hb = P * A.f * (FMT == FT_W_I8 ? 1 : 4), ob = P * kDownRows * 4;
   A.lds_vec = hb <= kVecLds - ob;
+  if (FMT == FT_W_I8) {
+    if (P * A.f <= kOwnCodes && A.lds_vec)
+      A.hq = nullptr;
+    else if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s))
+      return st;
+  }
   A.rows = (A.d + kUnits - 1) / kUnits;
   if (A.rows > kDownRows) A.rows = kDownRows;
-  hipLaunchKernelGGL((moe_down_kernel<FMT, JD, RR>), dim3((unsigned)((A.d + A.rows - 1) / A.rows)), dim3(NT),
-                     ob + (A.lds_vec ? hb : 0), s, A);
+  auto down = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((A.d + A.rows - 1) / A.rows)), dim3(NT), ob + (A.lds_vec ? hb : 0), s, A);
+  };
+  const int jd = (A.f / E + 63) / 64;
+  if constexpr (FMT == FT_W_MXFP4)
+    jd > 1 ? down(moe_down_kernel<FMT, 2, W / 2>) : down(moe_down_kernel<FMT, 1, W>);
+  else
+    jd > 2 ? down(moe_down_kernel<FMT, 4, W / 4>) : jd > 1 ? down(moe_down_kernel<FMT, 2, W / 2>) : down(moe_down_kernel<FMT, 1, 8>);
   return launched("moe_down_kernel");
 }
 
@@ -520,17 +628,6 @@ int moe_go(MoeArgs A, hipStream_t s) {
 int launch_moe_layer(const MoeLayer& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (L.T <= 0) return FT_OK;
-  // as the decode router: all tokens a wavefront up to 8, a few tens of blocks
-  const int tt = L.T == 1 ? 1 : L.T <= 4 ? 4 : 8, te = L.T == 1 ? (L.E <= 64 ? 1 : 2) : (L.E <= 128 ? 1 : 2);
-  const dim3 grid((unsigned)((L.E + 4 * te - 1) / (4 * te)), (unsigned)((L.T + tt - 1) / tt));
-  auto logits = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, L.x, L.w_router, L.T, L.d, L.E, L.logits); };
-  if (tt == 1)
-    te == 1 ? logits(moe_logits_kernel<1, 1>) : logits(moe_logits_kernel<1, 2>);
-  else if (tt == 4)
-    te == 1 ? logits(moe_logits_kernel<4, 1>) : logits(moe_logits_kernel<4, 2>);
-  else
-    te == 1 ? logits(moe_logits_kernel<8, 1>) : logits(moe_logits_kernel<8, 2>);
-  if (int st = launched("moe_logits_kernel")) return st;
   MoeArgs A{};
   A.x = L.x;
   A.logits = L.logits;
@@ -554,12 +651,21 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
   A.res = L.res;
   A.y = L.y;
   A.y_f32 = L.y_f32;
-  if (L.fmt == FT_W_I8) {
-    if (int st = launch_i8_quant(L.x, L.d, L.T, L.d, false, L.xq, L.xs, stream)) return st;
-    return moe_go<FT_W_I8, 4, 2, 2, 8>(A, s);
-  }
-  if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 2, 2, 1, 8>(A, s);
-  return moe_go<FT_W_BF16, 8, 2, 4, 4>(A, s);
+  // few logits a wavefront: their sums run in a fixed order and so one behind the other
+  const int tt = L.T == 1 ? 1 : L.T <= 16 ? 2 : 4, te = L.T == 1 ? 1 : 2;
+  const int eb = (L.E + 4 * te - 1) / (4 * te), blocks = eb * ((L.T + tt - 1) / tt);
+  const dim3 grid((unsigned)(blocks + (L.fmt == FT_W_I8 ? L.T : 0)));
+  auto logits = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, A, L.w_router, L.logits, eb, blocks); };
+  if (tt == 1)
+    logits(moe_logits_kernel<1, 1>);
+  else if (tt == 2)
+    logits(moe_logits_kernel<2, 2>);
+  else
+    logits(moe_logits_kernel<4, 2>);
+  if (int st = launched("moe_logits_kernel")) return st;
+  if (L.fmt == FT_W_I8) return moe_go<FT_W_I8, 16>(A, s);
+  if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 8>(A, s);
+  return moe_go<FT_W_BF16, 16>(A, s);
 }
 
 }  // namespace ft
