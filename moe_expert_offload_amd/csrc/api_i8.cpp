@@ -102,12 +102,14 @@ int ft_i8_gemm(const void* x, int64_t ldx, const float* x_scales, int32_t T, int
     return st;
   const bool half = dtype == FT_T_FP16;
   Space ws{static_cast<uint8_t*>(workspace)};
-  I8Rows r{static_cast<const int8_t*>(x), x_scales, ldx, T};
-  if (!x_scales) {
+  I8Rows r{static_cast<const int8_t*>(x), x_scales, ldx, T, nullptr};
+  if (!x_scales && i8_own_codes(T, w->K)) {
+    r = I8Rows{nullptr, nullptr, ldx, T, static_cast<const uint16_t*>(x)};
+  } else if (!x_scales) {
     int8_t* codes = ws.take<int8_t>((size_t)T * w->K);
     float* scales = ws.take<float>((size_t)T * 4);
     if (int st = launch_i8_quant(static_cast<const uint16_t*>(x), ldx, T, w->K, half, codes, scales, stream)) return st;
-    r = I8Rows{codes, scales, w->K, T};
+    r = I8Rows{codes, scales, w->K, T, nullptr};
   }
   return launch_i8_gemm(r, mat(w), I8Out{y, ldy, y_dtype == FT_T_FP32, residual, ldr}, half, ws.take<int>(0), stream);
 }
@@ -140,11 +142,19 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
   float* scales = ws.take<float>((size_t)T * 4);
   uint16_t* h = ws.take<uint16_t>((size_t)T * d_ff * 2);
   int* part = ws.take<int>(0);
-  if (int st = launch_i8_quant(static_cast<const uint16_t*>(x), ldx, T, d, half, codes, scales, stream)) return st;
-  if (int st = launch_i8_gate_up(I8Rows{codes, scales, d, T}, mat(gate), mat(up), act, h, half, part, stream)) return st;
-  if (int st = launch_i8_quant(h, d_ff, T, d_ff, half, codes, scales, stream)) return st;
-  return launch_i8_gemm(I8Rows{codes, scales, d_ff, T}, mat(down), I8Out{y, ldy, y_dtype == FT_T_FP32, residual, ldr},
-                        half, part, stream);
+  auto rows = [&](const uint16_t* v, int64_t ld, int n, I8Rows& r) -> int {
+    if (i8_own_codes(T, n)) {
+      r = I8Rows{nullptr, nullptr, ld, T, v};
+      return FT_OK;
+    }
+    r = I8Rows{codes, scales, n, T, nullptr};
+    return launch_i8_quant(v, ld, T, n, half, codes, scales, stream);
+  };
+  I8Rows r;
+  if (int st = rows(static_cast<const uint16_t*>(x), ldx, d, r)) return st;
+  if (int st = launch_i8_gate_up(r, mat(gate), mat(up), act, h, half, part, stream)) return st;
+  if (int st = rows(h, d_ff, d_ff, r)) return st;
+  return launch_i8_gemm(r, mat(down), I8Out{y, ldy, y_dtype == FT_T_FP32, residual, ldr}, half, part, stream);
 }
 
 }  // extern "C"

@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return v;
 }
 
-// One row of n elements to codes and its scale by ROWT threads, 64 or a whole block of 256 (`red`: 4 words of LDS). The row is
+// One row of n elements to codes and its scale by ROWT threads, 64 or a whole block (`red`: a word of LDS for each wave). The row is
 // held in registers between its largest element and its codes, NP pieces of 8 elements a thread; what is
 // longer is read again.  codes may lie in LDS.
 template <bool H, int ROWT, int NP>
@@ -109,7 +109,8 @@ __device__ __forceinline__ void quant_row(const uint16_t* src, int n, int8_t* co
   if constexpr (ROWT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
-    m = max(max(red[0], red[1]), max(red[2], red[3]));
+#pragma unroll
+    for (int w = 0; w < ROWT / 64; ++w) m = max(m, red[w]);
   }
   const RowScale r = row_scale<H>(m);
   uint2* d = reinterpret_cast<uint2*>(codes);

@@ -192,12 +192,20 @@ struct W4Args {
 int launch_w4(const W4Args& A, bool gate_up, void* stream);
 
 // ---- products in 8-bit integers (kernels_i8.hip) -----------------------------------
-struct I8Rows {  // tokens' codes [T, ld] and scales [T]
+struct I8Rows {  // tokens' codes [T, ld] and scales [T], or the tokens in 16 bits (x16)
   const int8_t* codes;
   const float* scales;
   int64_t ld;
   int T;
+  const uint16_t* x16;
 };
+// Whether a product of T rows of n quantises them itself, every block for itself (one token, N = 4096: K = 4096 7.6 us
+// against 6.0 with codes in hand and 2.5 to 4 for a launch that makes them, K = 11008 14.8 against 12.6).
+constexpr int kOwnCodes = 16384;
+inline bool i8_own_codes(int T, int n) {
+  const int rows = T <= 2 ? T : T <= 4 ? 4 : 8;  // as many as waves share evenly
+  return T <= 8 && (int64_t)rows * n <= kOwnCodes;
+}
 struct I8Mat {  // channels' codes [N, K] and scales [N]
   const int8_t* codes;
   const float* scales;

@@ -23,11 +23,11 @@ namespace {
 // ---- rows to codes ------------------------------------------------------------------
 // ROWT threads a row (quant_row).
 template <bool H, int ROWT, int NP>
-__global__ __launch_bounds__(256) void i8_quant_kernel(const uint16_t* src, int64_t ld, int rows, int n, int8_t* codes,
-                                                       float* scales) {
-  __shared__ uint32_t red[4];
-  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (256 / ROWT) + threadIdx.x / ROWT;
-  if (row >= rows) return;  // ROWT = 256: the whole block; else whole waves
+__global__ __launch_bounds__(ROWT) void i8_quant_kernel(const uint16_t* src, int64_t ld, int rows, int n, int8_t* codes,
+                                                        float* scales) {
+  __shared__ uint32_t red[ROWT / 64];
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= rows) return;  // the whole block
   quant_row<H, ROWT, NP>(src + row * ld, n, codes + row * n, scales + row, red);
 }
 
@@ -40,6 +40,7 @@ enum {
 
 struct I8Args {
   const int8_t *a, *b, *b2;  // codes of the tokens [M, K], of the channels [N, K]; b2: up
+  const uint16_t* x16;       // the tokens in 16 bits instead, quantised by each block
   const float *ta, *sb, *sb2;  // scales of the tokens and of the channels
   int64_t lda;
   int M, N, K, act;
@@ -66,45 +67,136 @@ __device__ __forceinline__ void store1(const I8Args& p, int64_t m, int n, float 
 }
 
 // ---- few rows: the weights stream once --------------------------------------------------
-// Up to 16 * NT tokens.  A block owns 16 channels (kGateUp: 8 of each matrix), its waves split k
-// in steps of 64 and add their sums in LDS.  v_mfma_i32_16x16x64: the weights are the second operand, so
-// each byte is loaded once, straight into registers; tokens past the last repeat it and their
-// sums are dropped.
-template <int MODE, bool H, int NT, int W>
-__global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
+// A block owns 16 channels (kGateUp: 8 of each matrix), its waves take chunks of 256 k in turn and add their sums in
+// LDS.  v_mfma_i32_16x16x64: the weights are the second operand, so each byte is loaded once, straight into
+// registers; tokens past the last repeat it and their sums are dropped.
+//
+// Tokens' codes as fragments from memory would touch 16 rows a load, as dear to the load unit as the weights'. So
+//   QX            x comes in 16 bits and each block quantises it for itself, whole, into LDS, while its first
+//                 weights are on their way (i8_own_codes)
+//   TK up to 16   a chunk's codes come as whole rows of 256 bytes, 4 tokens a load, and go to their fragments through
+//                 a piece of LDS of the wave's own (a wave's LDS operations run in order: no barrier)
+//   32, 64        fragments from memory
+// One chunk a wave, loaded again as it is used up: two or more take registers that further waves use better (45 MB of
+// weights, 2 tokens: K = 4096 11.6 us, with two chunks 13.0, with four 14.3).
+template <int MODE, bool H, bool QX, int TK, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 6 : 4) void i8_skinny_kernel(I8Args p) {
   constexpr bool GU = MODE == kGateUp;
-  constexpr int RB = GU ? 8 : 16, U = NT <= 2 ? 4 : 2;
+  constexpr int RB = GU ? 8 : 16, NT = TK <= 16 ? 1 : TK / 16;
+  constexpr int NX = QX || TK > 16 ? 0 : (TK + 3) / 4;
+  constexpr int XS = 17;  // row stride of a chunk's codes in LDS, in 16 bytes: rows start on different banks
   __shared__ int red[W][NT * 16][16];
+  __shared__ uint4 sx[W][NX ? NX * 4 * XS : 1];
+  __shared__ uint32_t top[W];
+  __shared__ float own_scale[16];
+  extern __shared__ uint4 own[];  // QX: codes, rows of K + 16 bytes
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int r0 = blockIdx.x * RB;
   const int row = r0 + (GU ? (n & 7) : n);
-  const int8_t* wp = GU && n >= 8 ? p.b2 : p.b;
-  wp += (int64_t)min(row, p.N - 1) * p.K;
-  const int8_t* xp[NT];
+  const int8_t* wp = (GU && n >= 8 ? p.b2 : p.b) + (int64_t)min(row, p.N - 1) * p.K;
+  const int chunks = (p.K + 255) >> 8;
+  const int8_t* xp[NX ? NX : NT];
+  if constexpr (!QX) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xp[i] = p.a + (int64_t)min(i * 16 + n, p.M - 1) * p.lda;
+    for (int i = 0; i < (NX ? NX : NT); ++i)
+      xp[i] = p.a + (int64_t)min(NX ? i * 4 + g : i * 16 + n, p.M - 1) * p.lda;
+  }
+  struct Chunk {
+    i32x4_t w[4];
+    i32x4_t x[QX ? 1 : NX ? NX : 4 * NT];
+  };
+  Chunk ch;
+  auto load = [&](Chunk& c, int ci) {
+    const int k0 = ci << 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j * 64 + g * 16;  // K % 16 == 0
+      c.w[j] = *reinterpret_cast<const i32x4_t*>(wp + (k < p.K ? k : 0));
+      if (k >= p.K) c.w[j] = i32x4_t{};
+    }
+    if constexpr (NX > 0) {
+      const int k = k0 + n * 16;
+#pragma unroll
+      for (int i = 0; i < NX; ++i) c.x[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + (k < p.K ? k : 0));
+    } else if constexpr (!QX) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * 64 + g * 16;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) c.x[j * NT + i] = *reinterpret_cast<const i32x4_t*>(xp[i] + (k < p.K ? k : 0));
+      }
+    }
+  };
+  if (wave < chunks) load(ch, wave);
+
+  const int own_row = p.K + 16;  // bytes
+  if constexpr (QX) {
+    // W / (T to a power of two) waves a row (none left over: T <= W); a thread holds at most NP pieces of 8
+    constexpr int NP = kOwnCodes / 8 / (64 * W);
+    int per = W;
+    while (per > 1 && W / per < p.M) per >>= 1;
+    const int t = wave / per, first = wave - wave % per, at = (wave % per) * 64 + lane, pieces = p.K >> 3;
+    uint4 v[NP];
+    uint32_t m = 0;
+    const uint4* src = reinterpret_cast<const uint4*>(p.x16 + (int64_t)min(t, p.M - 1) * p.lda);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int q = at + i * per * 64;
+      v[i] = q < pieces ? src[q] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) m = amax4(v[i], m);
+    m = wave_umax(m);
+    if (lane == 0) top[wave] = m;
+    __syncthreads();
+    for (int w = 0; w < per; ++w) m = max(m, top[first + w]);
+    if (t < p.M) {
+      const RowScale r = row_scale<H>(m);
+      uint2* d = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(own) + t * own_row);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int q = at + i * per * 64;
+        const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if (q < pieces) d[q] = row_codes8<H>(e, r);
+      }
+      if (wave == first && lane == 0) own_scale[t] = r.scale;
+    }
+    __syncthreads();
+  }
+
   i32x4_t acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = i32x4_t{};
-  const int steps = (p.K + 63) >> 6;  // of 64 k; pairs of steps go to the waves in turn
-  for (int s0 = 2 * wave; s0 < steps; s0 += 2 * W * (U / 2)) {
-    i32x4_t fw[U], fx[U][NT];
+  uint4* const xw = sx[wave] + g * XS + n;
+  const uint4* const xr = sx[wave] + min(n, NX * 4 - 1) * XS + g;
+  const uint8_t* const xo = reinterpret_cast<const uint8_t*>(own) + min(n, p.M - 1) * own_row;
+  auto use = [&](const Chunk& c, int ci) {
+    if constexpr (NX > 0) {
 #pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int s = s0 + (v >> 1) * 2 * W + (v & 1);
-      const int k = s * 64 + g * 16;
-      const bool ok = k < p.K;  // K % 16 == 0
-      const int ka = ok ? k : 0;
-      fw[v] = *reinterpret_cast<const i32x4_t*>(wp + ka);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) fx[v][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + ka);
-      if (!ok) fw[v] = i32x4_t{};
+      for (int i = 0; i < NX; ++i) xw[i * 4 * XS] = __builtin_bit_cast(uint4, c.x[i]);
+      __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll
-    for (int v = 0; v < U; ++v)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = mfma16(fx[v][i], fw[v], acc[i]);
+      for (int i = 0; i < NT; ++i) {
+        i32x4_t x;
+        if constexpr (QX)
+          x = *reinterpret_cast<const i32x4_t*>(xo + min((ci << 8) + j * 64 + g * 16, p.K));  // past K: weights 0
+        else if constexpr (NX > 0)
+          x = __builtin_bit_cast(i32x4_t, xr[j * 4]);
+        else
+          x = c.x[j * NT + i];
+        acc[i] = mfma16(x, c.w[j], acc[i]);
+      }
+    if constexpr (NX > 0) __builtin_amdgcn_wave_barrier();
+  };
+  __builtin_amdgcn_sched_barrier(0);
+  for (int c = wave; c < chunks; c += W) {
+    use(ch, c);
+    if (c + W < chunks) load(ch, c + W);
+    __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -114,7 +206,7 @@ __global__ __launch_bounds__(64 * W) void i8_skinny_kernel(I8Args p) {
   for (int e = threadIdx.x; e < NT * 16 * RB; e += 64 * W) {
     const int t = e / RB, c = e % RB, nn = r0 + c;
     if (t >= p.M || nn >= p.N) continue;
-    const float ts = p.ta[t];
+    const float ts = QX ? own_scale[t] : p.ta[t];
     int s = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) s += red[w][t][c];
@@ -624,12 +716,25 @@ int i8_go(I8Args& A, hipStream_t s) {
   if (A.M <= kSkinnyRows) {
     constexpr int RB = MODE == kGateUp ? 8 : 16;
     const unsigned nb = (unsigned)((A.N + RB - 1) / RB);
-    if (A.M <= 16)
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 1, 16>), dim3(nb), dim3(1024), 0, s, A);
+    // 16 waves a block where there are few blocks (one token, K = N = 4096: 7.6 us, with 8 waves 9.0), else 8 (K = 4096,
+    // N = 11008: 13.1, with 16 waves 20.5)
+    const bool few = nb < 2 * kUnits;
+    auto go = [&](auto wide, auto slim, size_t lds) {
+      if (few)
+        hipLaunchKernelGGL(wide, dim3(nb), dim3(1024), lds, s, A);
+      else
+        hipLaunchKernelGGL(slim, dim3(nb), dim3(512), lds, s, A);
+    };
+    if (A.x16)
+      go(i8_skinny_kernel<MODE, H, true, 16, 16>, i8_skinny_kernel<MODE, H, true, 16, 8>, (size_t)A.M * (A.K + 16) + 16);
+    else if (A.M <= 4)
+      go(i8_skinny_kernel<MODE, H, false, 4, 16>, i8_skinny_kernel<MODE, H, false, 4, 8>, 0);
+    else if (A.M <= 16)
+      go(i8_skinny_kernel<MODE, H, false, 16, 16>, i8_skinny_kernel<MODE, H, false, 16, 8>, 0);
     else if (A.M <= 32)
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 2, 8>), dim3(nb), dim3(512), 0, s, A);
+      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, false, 32, 16>), dim3(nb), dim3(1024), 0, s, A);
     else
-      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, 4, 8>), dim3(nb), dim3(512), 0, s, A);
+      hipLaunchKernelGGL((i8_skinny_kernel<MODE, H, false, 64, 16>), dim3(nb), dim3(1024), 0, s, A);
     return launched("i8_skinny_kernel");
   }
   const size_t es = A.c_f32 ? 4 : 2;
@@ -674,15 +779,17 @@ void fill_out(I8Args& A, const I8Out& o) {
 int launch_i8_quant(const uint16_t* src, int64_t ld, int rows, int n, bool half, int8_t* codes, float* scales, void* stream) {
   if (rows <= 0) return FT_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  auto go = [&](auto kernel, int per) {
+  auto go = [&](auto kernel, int threads) {
     // a grid's first dimension holds fewer than 2^32 threads
-    const unsigned b = ((unsigned)rows + per - 1) / per, x = b < 65536 ? b : 65536;
-    hipLaunchKernelGGL(kernel, dim3(x, (b + x - 1) / x), dim3(256), 0, s, src, ld, rows, n, codes, scales);
+    const unsigned b = (unsigned)rows, x = b < 65536 ? b : 65536;
+    hipLaunchKernelGGL(kernel, dim3(x, (b + x - 1) / x), dim3(threads), 0, s, src, ld, rows, n, codes, scales);
   };
+  // few long rows: more threads on each, so that none reads its row twice
+  const bool few = rows <= 2 * kUnits && n > 4096;
   if (half)
-    go(i8_quant_kernel<true, 256, 2>, 1);
+    few ? go(i8_quant_kernel<true, 1024, 2>, 1024) : go(i8_quant_kernel<true, 256, 2>, 256);
   else
-    go(i8_quant_kernel<false, 256, 2>, 1);
+    few ? go(i8_quant_kernel<false, 1024, 2>, 1024) : go(i8_quant_kernel<false, 256, 2>, 256);
   return launched("i8_quant_kernel");
 }
 
@@ -690,6 +797,7 @@ int launch_i8_gemm(const I8Rows& x, const I8Mat& w, const I8Out& o, bool half, i
   if (x.T <= 0) return FT_OK;
   I8Args A{};
   A.a = x.codes;
+  A.x16 = x.x16;
   A.lda = x.ld;
   A.ta = x.scales;
   A.b = w.codes;
@@ -707,6 +815,7 @@ int launch_i8_gate_up(const I8Rows& x, const I8Mat& gate, const I8Mat& up, int a
   if (x.T <= 0) return FT_OK;
   I8Args A{};
   A.a = x.codes;
+  A.x16 = x.x16;
   A.lda = x.ld;
   A.ta = x.scales;
   A.b = gate.codes;

@@ -582,7 +582,7 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
 constexpr int kUnits = 256;           // compute units
 constexpr size_t kVecLds = 96 << 10;  // most of a block's LDS for rows of x or h
 // Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
-constexpr size_t kOwnCodes = 32 << 10;
+constexpr size_t kOwnRows = 32 << 10;
 
 // A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
 template <int FMT, int W>
@@ -605,7 +605,7 @@ int moe_go(MoeArgs A, hipStream_t s) {
   const size_t hb = P * A.f * (FMT == FT_W_I8 ? 1 : 4), ob = P * kDownRows * 4;
   A.lds_vec = hb <= kVecLds - ob;
   if (FMT == FT_W_I8) {
-    if (P * A.f <= kOwnCodes && A.lds_vec)
+    if (P * A.f <= kOwnRows && A.lds_vec)
       A.hq = nullptr;
     else if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s))
       return st;
