@@ -22,7 +22,7 @@ bool bad_shape(const ft_shape* s) {
 bool bad_tokens(const ft_shape* s, int32_t T) { return T < 0 || T > kMaxTokens || T * s->k > FT_PLAN_CAP; }
 
 struct Layout {
-  size_t logits, xq, xs, hq, hs, h, total;
+  size_t logits, grouped, xq, xs, hq, hs, h, total;
 };
 Layout layout(const ft_shape* s, int32_t T) {
   Layout l{};
@@ -34,6 +34,7 @@ Layout layout(const ft_shape* s, int32_t T) {
     return o;
   };
   l.logits = take((size_t)T * s->E * 4);
+  l.grouped = take(kMoeGroupedBytes);
   if (s->fmt == FT_W_I8) {
     l.xq = take((size_t)T * s->d);
     l.xs = take((size_t)T * 4);
@@ -94,6 +95,7 @@ int ft_moe_layer(const ft_shape* shape, const void* x, int32_t T, const void* w_
   L.idx = idx;
   L.gates = gates;
   L.logits = reinterpret_cast<float*>(ws + l.logits);
+  L.grouped = ws + l.grouped;
   L.xq = reinterpret_cast<int8_t*>(ws + l.xq);
   L.xs = reinterpret_cast<float*>(ws + l.xs);
   L.hq = reinterpret_cast<int8_t*>(ws + l.hq);

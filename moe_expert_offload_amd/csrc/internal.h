@@ -225,6 +225,7 @@ int launch_i8_gate_up(const I8Rows& x, const I8Mat& gate, const I8Mat& up, int a
                       void* stream);
 
 // ---- the routed layer for a few tokens (kernels_moe.hip) ----------------------------
+constexpr size_t kMoeGroupedBytes = 5 * 4 * FT_PLAN_CAP + 256;
 // Its tensors checked and its workspace laid out.
 struct MoeLayer {
   const uint16_t *x, *w_router;
@@ -238,7 +239,8 @@ struct MoeLayer {
   int y_f32;
   int32_t* idx;
   float* gates;
-  float* logits;  // [T, E]
+  float* logits;   // [T, E]
+  void* grouped;   // kMoeGroupedBytes
   int8_t *xq, *hq;  // 8-bit records: codes and scales of x [T, d] and h [T k, d_ff]
   float *xs, *hs;
   void* h;  // [T k, d_ff] fp32, 8-bit records bf16

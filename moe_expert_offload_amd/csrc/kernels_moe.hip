@@ -27,6 +27,17 @@ namespace {
 
 constexpr int NT = 1024, NW = NT / 64;  // threads and wavefronts of a block, one block a compute unit
 
+// The routed pairs by expert (of 512 pairs at most), as gate/up leaves them for down.
+struct Grouped {
+  int32_t groups;
+  int32_t grp[FT_PLAN_CAP];      // a pair's group, -1: left out (no expert, or none of the given ones)
+  int32_t slot[FT_PLAN_CAP];     // of a group
+  int32_t off[FT_PLAN_CAP + 1];  // first of a group's pairs in `pair`
+  int32_t pair[FT_PLAN_CAP];     // pairs by group
+  float gate[FT_PLAN_CAP];
+};
+static_assert(sizeof(Grouped) <= kMoeGroupedBytes, "the workspace's share");
+
 struct MoeArgs {
   const uint16_t* x;
   const float* logits;
@@ -37,6 +48,7 @@ struct MoeArgs {
   size_t S;
   int32_t* idx;
   float* gates;
+  Grouped* grouped;
   int8_t* xq;  // 8-bit records: x in 8 bits
   float* xs;
   int8_t* hq;  // h in 8 bits
@@ -215,14 +227,9 @@ __device__ __forceinline__ int row_bytes(int n) {
 }
 
 // ---- the routed pairs by expert, in LDS ---------------------------------------------------
-struct Plan {
+struct Plan : Grouped {
   int32_t id[FT_PLAN_CAP];  // expert of a pair
-  float gate[FT_PLAN_CAP];
-  int32_t grp[FT_PLAN_CAP];      // its group, -1: left out (no expert, or none of the given ones)
-  int32_t slot[FT_PLAN_CAP];     // of a group
-  int32_t off[FT_PLAN_CAP + 1];  // first of a group's pairs in `pair`
-  int32_t pair[FT_PLAN_CAP];     // pairs by group
-  int32_t first[FT_E_MAX];       // an expert's first pair, then its group
+  int32_t first[FT_E_MAX];  // an expert's first pair, then its group
   int32_t count[FT_PLAN_CAP];
   int32_t wave_sum[NW];
 };
@@ -249,22 +256,53 @@ __device__ __forceinline__ int block_prefix(int v, int32_t* wave_sums, int& tota
   return base + in - v;
 }
 
+// The record of a pair's expert, -1: none.
+__device__ __forceinline__ int slot_of(const MoeArgs& p, int id) {
+  if (id < 0 || id >= p.E) return -1;
+  const int slot = p.slot_of ? p.slot_of[id] : id;
+  return slot >= 0 && slot < p.n_slots ? slot : -1;
+}
+
 // Groups in the order of their first pair; pairs within a group in any order (each one's results are its own).
-// id and gate are set; all threads of the block.  Returns the number of groups.
-__device__ int make_plan(Plan& P, const MoeArgs& p) {
+// id and gate are set.  Up to 64 pairs, by one wavefront: a lane a pair.
+__device__ void plan_of_a_wave(Plan& P, const MoeArgs& p, int lane) {
+  const int n = p.T * p.k;
+  const int id = lane < n ? P.id[lane] : -1, slot = slot_of(p, id);
+  int before = 0, first_of = lane;
+  for (int q = n - 1; q >= 0; --q) {
+    const bool same = __builtin_amdgcn_readlane(id, q) == id;
+    before += same && q < lane;
+    if (same) first_of = q;
+  }
+  const unsigned long long firsts = __ballot(slot >= 0 && first_of == lane);
+  const int groups = __popcll(firsts), grp = slot >= 0 ? __popcll(firsts & ((1ull << first_of) - 1)) : -1;
+  int off = 0;  // pairs of the groups before this one
+  for (int q = 0; q < n; ++q) {
+    const int g = __builtin_amdgcn_readlane(grp, q);
+    off += g >= 0 && g < grp;
+  }
+  if (lane < n) P.grp[lane] = grp;
+  if (grp >= 0) {
+    P.pair[off + before] = lane;
+    if (first_of == lane) {
+      P.slot[grp] = slot;
+      P.off[grp] = off;
+    }
+  }
+  const int all = __popcll(__ballot(grp >= 0));
+  if (lane == 0) {
+    P.groups = groups;
+    P.off[groups] = all;
+  }
+}
+// More pairs, by the block (barriers before its first and after its last access).
+__device__ void plan_of_a_block(Plan& P, const MoeArgs& p) {
   const int n = p.T * p.k, i = threadIdx.x;
   for (int e = i; e < p.E; e += NT) P.first[e] = INT_MAX;
   if (i < FT_PLAN_CAP) P.count[i] = 0;
   __syncthreads();
-  int id = -1, slot = -1;
-  if (i < n) {
-    id = P.id[i];
-    if (id >= 0 && id < p.E) {
-      slot = p.slot_of ? p.slot_of[id] : id;
-      if (slot < 0 || slot >= p.n_slots) slot = -1;
-      if (slot >= 0) atomicMin(&P.first[id], i);
-    }
-  }
+  const int id = i < n ? P.id[i] : -1, slot = slot_of(p, id);
+  if (slot >= 0) atomicMin(&P.first[id], i);
   __syncthreads();
   const bool first = slot >= 0 && P.first[id] == i;
   int groups;
@@ -284,16 +322,16 @@ __device__ int make_plan(Plan& P, const MoeArgs& p) {
   if (i <= groups) P.off[i] = off;
   __syncthreads();
   if (grp >= 0) P.pair[P.off[grp] + at] = i;
+  if (i == 0) P.groups = groups;
   __syncthreads();
-  return groups;
 }
 
 // Rows of x (h): `rows` rows of `pieces` pieces of NV 16-byte parts.  In LDS the parts of a row lie in planes (part
 // v of piece i at v * pieces + i), so that 64 lanes read 64 consecutive 16-byte places.
 template <int NV>
-__device__ __forceinline__ void stage_rows(uint4* dst, const uint4* src, int rows, int pieces) {
+__device__ __forceinline__ void stage_rows(uint4* dst, const uint4* src, int rows, int pieces, int me, int threads) {
   const int per = pieces * NV;
-  for (int i = threadIdx.x; i < rows * per; i += NT) {
+  for (int i = me; i < rows * per; i += threads) {
     if constexpr (NV == 1) {
       dst[i] = src[i];
     } else {
@@ -326,21 +364,21 @@ __device__ __forceinline__ void topk_rows(const MoeArgs& p, Plan& P, int lane, i
   for (int t = wave; t < p.T; t += NW) {
     TopkIn<NS> in;
     topk_load<NS>(p.logits + (size_t)t * p.E, p.allowed ? p.allowed + (size_t)t * p.E : nullptr, p.E, lane, in);
-    topk_pick<NS>(in, p.k, lane, P.id + t * p.k, P.gate + t * p.k);
+    topk_pick32<NS>(in, p.k, lane, P.id + t * p.k, P.gate + t * p.k);
   }
 }
 
 // ---- gate/up ----------------------------------------------------------------------------------
 // A wavefront takes units of RG row pairs (gate and up), a consecutive share of all of them.
 template <int FMT, int JC, int RG, bool LV>
-__device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, int groups, const uint4* sx) {
+__device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const uint4* sx) {
   constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU, TB = 2;
   typedef typename Fmt<FMT>::Acc Acc;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Rec R = rec_of<FMT>(p.d, p.f);
   const int pieces = p.d / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.d);
   const int per_group = (p.f + RG - 1) / RG;
-  const int64_t units = (int64_t)groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
+  const int64_t units = (int64_t)P.groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
   const int u_end = (int)(units * (w + 1) / nw);
   for (int u = (int)(units * w / nw); u < u_end; ++u) {
     const int g = u / per_group, r0 = (u - g * per_group) * RG;
@@ -422,10 +460,14 @@ template <int FMT, int JC, int RG>
 __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
   __shared__ Plan P;
   extern __shared__ uint4 vec[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.T * p.k;
   if (p.lds_vec) {
     constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU;
-    stage_rows<NV>(vec, reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.xq : (const void*)p.x), p.T, p.d / E);
+    // with few tokens, by the wavefronts that have none to rank
+    const int skip = p.T <= NW / 2 ? p.T * 64 : 0;
+    if ((int)threadIdx.x >= skip)
+      stage_rows<NV>(vec, reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.xq : (const void*)p.x), p.T, p.d / E,
+                     threadIdx.x - skip, NT - skip);
   }
   if (p.E <= 64)
     topk_rows<1>(p, P, lane, wave);
@@ -435,16 +477,30 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
     topk_rows<4>(p, P, lane, wave);
   else
     topk_rows<16>(p, P, lane, wave);
-  __syncthreads();
-  if (blockIdx.x == 0 && (int)threadIdx.x < p.T * p.k) {
-    p.idx[threadIdx.x] = P.id[threadIdx.x];
-    p.gates[threadIdx.x] = P.gate[threadIdx.x];
+  if (p.T > 1) __syncthreads();
+  if (n <= 64) {
+    if (wave == 0) plan_of_a_wave(P, p, lane);
+    __syncthreads();
+  } else {
+    plan_of_a_block(P, p);
   }
-  const int groups = make_plan(P, p);
+  if (blockIdx.x == 0) {
+    const int i = threadIdx.x;
+    if (i < n) {
+      p.idx[i] = P.id[i];
+      p.gates[i] = P.gate[i];
+      p.grouped->grp[i] = P.grp[i];
+      p.grouped->gate[i] = P.gate[i];
+      p.grouped->pair[i] = P.pair[i];  // those past the last are not used
+      p.grouped->slot[i] = P.slot[i];
+    }
+    if (i <= n) p.grouped->off[i] = P.off[i];
+    if (i == 0) p.grouped->groups = P.groups;
+  }
   if (p.lds_vec)
-    up_units<FMT, JC, RG, true>(p, P, groups, vec);
+    up_units<FMT, JC, RG, true>(p, P, vec);
   else
-    up_units<FMT, JC, RG, false>(p, P, groups, nullptr);
+    up_units<FMT, JC, RG, false>(p, P, nullptr);
 }
 
 // ---- down --------------------------------------------------------------------------------------
@@ -452,36 +508,45 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
 // group.  A pair's results wait in LDS until all are there, then each token's are added in the order of j.
 constexpr int kDownRows = 16;
 
-template <int FMT, int JC, int RR, bool LV>
-__device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, int groups, const uint4* sh, const float* hs,
-                                           float* out) {
+template <int FMT, int JC, int RR, bool LV, class Stage>
+__device__ __forceinline__ void down_units(const MoeArgs& p, const Grouped& P, const uint4* sh, const float* hs, float* out,
+                                           Stage stage) {
   constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND, TB = 2;
   typedef typename Fmt<FMT>::Acc Acc;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Rec R = rec_of<FMT>(p.d, p.f);
   const int pieces = p.f / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.f);
   const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0), per_group = (nr + RR - 1) / RR;
-  for (int u = wave; u < groups * per_group; u += NW) {
-    const int g = u / per_group, q0 = (u - g * per_group) * RR;
-    const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(P.slot[g]) * p.S;
+  uint4 wv[RR][JC];
+  uint32_t sc[RR][JC];
+  auto load = [&](const uint8_t* rp, int q0, int j0) {
     const auto rec = buf_rsrc(rp, (uint32_t)p.S);
-    const int first = __builtin_amdgcn_readfirstlane(P.off[g]), n = __builtin_amdgcn_readfirstlane(P.off[g + 1]) - first;
-    uint4 wv[RR][JC];
-    uint32_t sc[RR][JC];
-    auto load = [&](int j0) {
 #pragma unroll
-      for (int r = 0; r < RR; ++r) {
-        const uint32_t base = R.down + (uint32_t)(b0 + q0 + r) * (uint32_t)rb;
+    for (int r = 0; r < RR; ++r) {
+      const uint32_t base = R.down + (uint32_t)(b0 + q0 + r) * (uint32_t)rb;
 #pragma unroll
-        for (int j = 0; j < JC; ++j) {
-          const int i = (j0 + j) * 64 + lane;
-          const bool in = q0 + r < nr && i < pieces;
-          wv[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
-          sc[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? R.ds + (uint32_t)(b0 + q0 + r) * (uint32_t)pieces + i : kOOB) : 0;
-        }
+      for (int j = 0; j < JC; ++j) {
+        const int i = (j0 + j) * 64 + lane;
+        const bool in = q0 + r < nr && i < pieces;
+        wv[r][j] = buf_ld16(rec, in ? base + 16u * i : kOOB);
+        sc[r][j] = FMT == FT_W_MXFP4 ? buf_ld8(rec, in ? R.ds + (uint32_t)(b0 + q0 + r) * (uint32_t)pieces + i : kOOB) : 0;
       }
-    };
-    load(0);
+    }
+  };
+  const int units = P.groups * per_group;
+  bool staged = false;
+  // (everyone stages, whether it has a unit or not)
+  for (int u = wave; u < units || !staged; u += NW) {
+    const bool any = u < units;
+    const int g = any ? u / per_group : 0, q0 = (u - g * per_group) * RR;
+    const uint8_t* rp = p.rec + (any ? (size_t)__builtin_amdgcn_readfirstlane(P.slot[g]) * p.S : 0);
+    if (any) load(rp, q0, 0);
+    if (!staged) {
+      stage();  // behind the first weights
+      staged = true;
+    }
+    if (!any) break;
+    const int first = __builtin_amdgcn_readfirstlane(P.off[g]), n = __builtin_amdgcn_readfirstlane(P.off[g + 1]) - first;
     for (int tb = 0; tb < n; tb += TB) {
       Acc acc[TB][RR];
 #pragma unroll
@@ -489,7 +554,7 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, int 
 #pragma unroll
         for (int r = 0; r < RR; ++r) acc[t][r] = 0;
       for (int j0 = 0; j0 < J; j0 += JC) {
-        if (J > JC && (j0 > 0 || tb > 0)) load(j0);
+        if (J > JC && (j0 > 0 || tb > 0)) load(rp, q0, j0);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
           if (tb + t >= n) continue;
@@ -531,37 +596,40 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Plan& P, int 
 
 template <int FMT, int JC, int RR>
 __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
-  __shared__ Plan P;
+  __shared__ Grouped P;
   __shared__ float s_hs[FMT == FT_W_I8 ? FT_PLAN_CAP : 1];
   extern __shared__ uint4 vec[];  // results [pairs][kDownRows], then rows of h
-  const int n = p.T * p.k;
+  const int n = p.T * p.k, i = threadIdx.x;
   float* out = reinterpret_cast<float*>(vec);
   uint4* sh = vec + n * kDownRows / 4;
-  if ((int)threadIdx.x < n) {
-    P.id[threadIdx.x] = p.idx[threadIdx.x];
-    P.gate[threadIdx.x] = p.gates[threadIdx.x];
-    if (FMT == FT_W_I8 && p.hq) s_hs[threadIdx.x] = p.hs[threadIdx.x];
+  const Grouped& G = *p.grouped;
+  if (i < n) {
+    P.grp[i] = G.grp[i];
+    P.gate[i] = G.gate[i];
+    P.pair[i] = G.pair[i];
+    P.slot[i] = G.slot[i];
+    if (FMT == FT_W_I8 && p.hq) s_hs[i] = p.hs[i];
   }
-  if (p.lds_vec) {
-    constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::ND;
-    if (FMT == FT_W_I8 && !p.hq) {  // few pairs: each block makes the codes of h for itself
-      for (int q = threadIdx.x >> 6; q < n; q += NW)
-        quant_row<false, 64, 4>(static_cast<const uint16_t*>(p.h) + (size_t)q * p.f, p.f,
-                                reinterpret_cast<int8_t*>(sh) + (size_t)q * p.f, s_hs + q, nullptr);
-    } else {
-      stage_rows<NV>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / E);
-    }
-  }
+  if (i <= n) P.off[i] = G.off[i];
+  if (i == 0) P.groups = G.groups;
   __syncthreads();
-  const int groups = make_plan(P, p);
   if (p.lds_vec)
-    down_units<FMT, JC, RR, true>(p, P, groups, sh, s_hs, out);
+    down_units<FMT, JC, RR, true>(p, P, sh, s_hs, out, [&]() {
+      if (FMT == FT_W_I8 && !p.hq) {  // few pairs: each block makes the codes of h for itself
+        for (int q = threadIdx.x >> 6; q < n; q += NW)
+          quant_row<false, 64, 4>(static_cast<const uint16_t*>(p.h) + (size_t)q * p.f, p.f,
+                                  reinterpret_cast<int8_t*>(sh) + (size_t)q * p.f, s_hs + q, nullptr);
+      } else {
+        stage_rows<Fmt<FMT>::ND>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / Fmt<FMT>::E, i, NT);
+      }
+      __syncthreads();
+    });
   else
-    down_units<FMT, JC, RR, false>(p, P, groups, nullptr, s_hs, out);
+    down_units<FMT, JC, RR, false>(p, P, nullptr, s_hs, out, []() {});
   __syncthreads();
   const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
-  for (int i = threadIdx.x; i < p.T * nr; i += NT) {
-    const int t = i / nr, r = i - t * nr;
+  for (int e = i; e < p.T * nr; e += NT) {
+    const int t = e / nr, r = e - t * nr;
     const size_t at = (size_t)t * p.d + b0 + r;
     float s = 0.0f;
     for (int j = 0; j < p.k; ++j) {
@@ -643,6 +711,7 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
   A.S = L.S;
   A.idx = L.idx;
   A.gates = L.gates;
+  A.grouped = static_cast<Grouped*>(L.grouped);
   A.xq = L.xq;
   A.xs = L.xs;
   A.hq = L.hq;

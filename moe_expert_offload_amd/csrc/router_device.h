@@ -206,6 +206,65 @@ __device__ __forceinline__ void topk_pick(const TopkIn<NS>& in, int k, int lane,
   }
 }
 
+// The same ranks through 32-bit maxima: a round's largest key by DPP maxima, then the least expert that has it by
+// ballots, in a third of the instructions.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
+  const uint32_t w = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xf, false);
+  return w > v ? w : v;
+}
+template <int NS>
+__device__ __forceinline__ void topk_pick32(const TopkIn<NS>& in, int k, int lane, int32_t* idx, float* gates) {
+  uint32_t key[NS];  // 0: not to be taken; else 1 + the upper word of rank_key (one NaN pattern shares another's)
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const uint32_t u = (uint32_t)(rank_key(in.v[s], 0) >> 32);
+    key[s] = in.ok[s] ? (u == 0xffffffffu ? u : u + 1u) : 0u;
+  }
+  float my_v = 0.0f, top = 0.0f;
+  int my_e = -1;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (r < k) {
+      uint32_t b = key[0];
+#pragma unroll
+      for (int s = 1; s < NS; ++s) b = key[s] > b ? key[s] : b;
+      b = dpp_umax<0xb1, 0xf>(b);
+      b = dpp_umax<0x4e, 0xf>(b);
+      b = dpp_umax<0x141, 0xf>(b);
+      b = dpp_umax<0x140, 0xf>(b);
+      b = dpp_umax<0x142, 0xa>(b);
+      b = dpp_umax<0x143, 0xc>(b);
+      b = (uint32_t)__builtin_amdgcn_readlane((int)b, 63);
+      if (b != 0u) {
+        int e = -1;
+#pragma unroll
+        for (int s = NS - 1; s >= 0; --s) {
+          const unsigned long long m = __ballot(key[s] == b);
+          if (m) e = 64 * s + __builtin_ctzll(m);
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if (lane + 64 * s == e) key[s] = 0u;
+        const float v = key_logit((unsigned long long)(b - 1u) << 32);
+        if (r == 0) top = v;
+        if (lane == r) {
+          my_v = v;
+          my_e = e;
+        }
+      }
+    }
+  }
+  const float z = (lane < k && my_e >= 0) ? expf(my_v - top) : 0.0f;
+  float sum = z;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor(sum, o, WAVE);
+  if (lane < k) {
+    idx[lane] = my_e;
+    gates[lane] = my_e >= 0 ? z / sum : 0.0f;
+  }
+}
+
 // Tokens first, first + step, ... of logits [T, E] by one wavefront, two at a time.
 template <int NS>
 __device__ __forceinline__ void topk_tokens_ns(const float* __restrict__ logits, const uint8_t* __restrict__ allowed,
