@@ -22,7 +22,7 @@ bool bad_shape(const ft_shape* s) {
 bool bad_tokens(const ft_shape* s, int32_t T) { return T < 0 || T > kMaxTokens || T * s->k > FT_PLAN_CAP; }
 
 struct Layout {
-  size_t logits, grouped, xq, xs, hq, hs, h, total;
+  size_t logits, grouped, xv, xs, hq, hs, h, total;
 };
 Layout layout(const ft_shape* s, int32_t T) {
   Layout l{};
@@ -36,12 +36,13 @@ Layout layout(const ft_shape* s, int32_t T) {
   l.logits = take((size_t)T * s->E * 4);
   l.grouped = take(kMoeGroupedBytes);
   if (s->fmt == FT_W_I8) {
-    l.xq = take((size_t)T * s->d);
+    l.xv = take((size_t)T * s->d);
     l.xs = take((size_t)T * 4);
     l.hq = take(P * s->d_ff);
     l.hs = take(P * 4);
     l.h = take(P * s->d_ff * 2);
   } else {
+    if (s->fmt == FT_W_MXFP4) l.xv = take((size_t)T * s->d * 2);
     l.h = take(P * s->d_ff * 4);
   }
   l.total = at + 256;
@@ -96,7 +97,7 @@ int ft_moe_layer(const ft_shape* shape, const void* x, int32_t T, const void* w_
   L.gates = gates;
   L.logits = reinterpret_cast<float*>(ws + l.logits);
   L.grouped = ws + l.grouped;
-  L.xq = reinterpret_cast<int8_t*>(ws + l.xq);
+  L.xv = ws + l.xv;
   L.xs = reinterpret_cast<float*>(ws + l.xs);
   L.hq = reinterpret_cast<int8_t*>(ws + l.hq);
   L.hs = reinterpret_cast<float*>(ws + l.hs);

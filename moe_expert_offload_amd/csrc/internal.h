@@ -241,7 +241,8 @@ struct MoeLayer {
   float* gates;
   float* logits;   // [T, E]
   void* grouped;   // kMoeGroupedBytes
-  int8_t *xq, *hq;  // 8-bit records: codes and scales of x [T, d] and h [T k, d_ff]
+  void* xv;        // MXFP4: x [T, d] in another order; 8-bit records: codes of x, of h [T k, d_ff], and their scales
+  int8_t* hq;
   float *xs, *hs;
   void* h;  // [T k, d_ff] fp32, 8-bit records bf16
 };

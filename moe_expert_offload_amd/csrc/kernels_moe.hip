@@ -49,11 +49,11 @@ struct MoeArgs {
   int32_t* idx;
   float* gates;
   Grouped* grouped;
-  int8_t* xq;  // 8-bit records: x in 8 bits
+  void* xv;    // x as it is multiplied: bf16 x itself, MXFP4 in planes, 8-bit records codes (scales xs)
   float* xs;
-  int8_t* hq;  // h in 8 bits
+  int8_t* hq;  // 8-bit records: h in 8 bits (scales hs)
   float* hs;
-  void* h;  // [T k, f]: fp32, 8-bit records bf16
+  void* h;  // [T k, f]: fp32 in planes, 8-bit records bf16
   const void* res;
   void* y;
   int y_f32;
@@ -326,36 +326,39 @@ __device__ void plan_of_a_block(Plan& P, const MoeArgs& p) {
   __syncthreads();
 }
 
-// Rows of x (h): `rows` rows of `pieces` pieces of NV 16-byte parts.  In LDS the parts of a row lie in planes (part
-// v of piece i at v * pieces + i), so that 64 lanes read 64 consecutive 16-byte places.
-template <int NV>
-__device__ __forceinline__ void stage_rows(uint4* dst, const uint4* src, int rows, int pieces, int me, int threads) {
-  const int per = pieces * NV;
-  for (int i = me; i < rows * per; i += threads) {
-    if constexpr (NV == 1) {
-      dst[i] = src[i];
-    } else {
-      const int r = i / per, e = i - r * per;
-      dst[r * per + (e % NV) * pieces + e / NV] = src[i];
-    }
-  }
+// Rows of x and h that are multiplied lie in planes: part v of piece i of a row at place v * pieces + i, so that the 64
+// lanes of a load read 64 consecutive 16-byte places.
+__device__ __forceinline__ int plane_of(int i, int parts, int pieces) { return i % parts * pieces + i / parts; }
+// Element r of a row of fp32 (4 a place).
+__device__ __forceinline__ int plane_of_f32(int r, int parts, int pieces) {
+  return plane_of(r >> 2, parts, pieces) * 4 + (r & 3);
 }
-template <int NV, bool LV>
+__device__ __forceinline__ void stage_rows(uint4* dst, const uint4* src, int places, int me, int threads) {
+  for (int i = me; i < places; i += threads) dst[i] = src[i];
+}
+template <int NV>
 __device__ __forceinline__ void load_parts(uint4 (&v)[NV], const uint4* row, int pieces, int i) {
 #pragma unroll
-  for (int q = 0; q < NV; ++q) v[q] = row[LV ? q * pieces + i : i * NV + q];
+  for (int q = 0; q < NV; ++q) v[q] = row[q * pieces + i];
 }
 
-// ---- logits (8-bit records: and x in 8 bits, a row by each of the last blocks) ---------------
-template <int TT, int TE>
+// ---- logits; MXFP4: and x in planes, 8-bit records: and x in 8 bits, a row by each of the last blocks ------
+template <int FMT, int TT, int TE>
 __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs p, const uint16_t* __restrict__ w, float* logits, int eb,
                                                          int blocks) {
   __shared__ uint32_t red[4];
   const int b = blockIdx.x;
   if (b < blocks)
     router_logits_wave<TT, TE>(p.x, w, p.T, p.d, p.E, b / eb * TT, (b % eb * 4 + (threadIdx.x >> 6)) * TE, threadIdx.x & 63, logits);
-  else
-    quant_row<false, 256, 2>(p.x + (size_t)(b - blocks) * p.d, p.d, p.xq + (size_t)(b - blocks) * p.d, p.xs + (b - blocks), red);
+  else if constexpr (FMT == FT_W_I8)
+    quant_row<false, 256, 2>(p.x + (size_t)(b - blocks) * p.d, p.d, static_cast<int8_t*>(p.xv) + (size_t)(b - blocks) * p.d,
+                             p.xs + (b - blocks), red);
+  else if constexpr (FMT == FT_W_MXFP4) {
+    constexpr int NV = Fmt<FMT>::NU;
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(b - blocks) * p.d);
+    uint4* dst = static_cast<uint4*>(p.xv) + (size_t)(b - blocks) * (p.d / 8);
+    for (int i = threadIdx.x; i < p.d / 8; i += 256) dst[plane_of(i, NV, p.d / Fmt<FMT>::E)] = src[i];
+  }
 }
 
 // Tokens wave, wave + NW, ... one at a time (two of 1024 experts' logits would not fit the registers).
@@ -369,7 +372,8 @@ __device__ __forceinline__ void topk_rows(const MoeArgs& p, Plan& P, int lane, i
 }
 
 // ---- gate/up ----------------------------------------------------------------------------------
-// A wavefront takes units of RG row pairs (gate and up), a consecutive share of all of them.
+// A wavefront takes units of RG row pairs (gate and up) in turn: every one gets of every group, whose numbers of
+// tokens differ.
 template <int FMT, int JC, int RG, bool LV>
 __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const uint4* sx) {
   constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU, TB = 2;
@@ -378,9 +382,8 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
   const Rec R = rec_of<FMT>(p.d, p.f);
   const int pieces = p.d / E, J = (pieces + 63) >> 6, rb = row_bytes<FMT>(p.d);
   const int per_group = (p.f + RG - 1) / RG;
-  const int64_t units = (int64_t)P.groups * per_group, w = (int64_t)blockIdx.x * NW + wave, nw = (int64_t)gridDim.x * NW;
-  const int u_end = (int)(units * (w + 1) / nw);
-  for (int u = (int)(units * w / nw); u < u_end; ++u) {
+  const int units = P.groups * per_group;
+  for (int u = blockIdx.x * NW + wave; u < units; u += gridDim.x * NW) {
     const int g = u / per_group, r0 = (u - g * per_group) * RG;
     const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(P.slot[g]) * p.S;
     const auto rec = buf_rsrc(rp, (uint32_t)p.S);
@@ -415,15 +418,13 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
         for (int t = 0; t < TB; ++t) {
           if (tb + t >= n) continue;
           const int tok = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]) / p.k;
-          const uint4* row = LV ? sx + (size_t)tok * pieces * NV
-                                : reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)(p.xq + (size_t)tok * p.d)
-                                                                                : (const void*)(p.x + (size_t)tok * p.d));
+          const uint4* row = (LV ? sx : static_cast<const uint4*>(p.xv)) + (size_t)tok * pieces * NV;
 #pragma unroll
           for (int j = 0; j < JC; ++j) {
             const int i = (j0 + j) * 64 + lane;
             if (i >= pieces) continue;
             uint4 v[NV];
-            load_parts<NV, LV>(v, row, pieces, i);
+            load_parts<NV>(v, row, pieces, i);
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
               ag[t][r] = piece_dot<FMT, false, NV>(wg[r][j], sg[r][j], v, ag[t][r]);
@@ -448,7 +449,7 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
             const float v = act_f(i8_value(ag[t][q], gs[0], ts), FT_ACT_SILU) * i8_value(au[t][q], gs[p.f], ts);
             static_cast<uint16_t*>(p.h)[(size_t)pair * p.f + row] = (uint16_t)pack2<false>(v, 0.0f);
           } else {
-            static_cast<float*>(p.h)[(size_t)pair * p.f + row] = silu(ag[t][q]) * au[t][q];
+            static_cast<float*>(p.h)[(size_t)pair * p.f + plane_of_f32(row, Fmt<FMT>::ND, p.f / E)] = silu(ag[t][q]) * au[t][q];
           }
         }
       }
@@ -462,12 +463,10 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
   extern __shared__ uint4 vec[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.T * p.k;
   if (p.lds_vec) {
-    constexpr int E = Fmt<FMT>::E, NV = Fmt<FMT>::NU;
     // with few tokens, by the wavefronts that have none to rank
     const int skip = p.T <= NW / 2 ? p.T * 64 : 0;
     if ((int)threadIdx.x >= skip)
-      stage_rows<NV>(vec, reinterpret_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.xq : (const void*)p.x), p.T, p.d / E,
-                     threadIdx.x - skip, NT - skip);
+      stage_rows(vec, static_cast<const uint4*>(p.xv), p.T * (p.d / Fmt<FMT>::E) * Fmt<FMT>::NU, threadIdx.x - skip, NT - skip);
   }
   if (p.E <= 64)
     topk_rows<1>(p, P, lane, wave);
@@ -559,16 +558,13 @@ __device__ __forceinline__ void down_units(const MoeArgs& p, const Grouped& P, c
         for (int t = 0; t < TB; ++t) {
           if (tb + t >= n) continue;
           const int pair = __builtin_amdgcn_readfirstlane(P.pair[first + tb + t]);
-          const uint4* row = LV ? sh + (size_t)pair * pieces * NV
-                                : reinterpret_cast<const uint4*>(FMT == FT_W_I8
-                                                                     ? (const void*)(p.hq + (size_t)pair * p.f)
-                                                                     : (const void*)(static_cast<const float*>(p.h) + (size_t)pair * p.f));
+          const uint4* row = (LV ? sh : static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h)) + (size_t)pair * pieces * NV;
 #pragma unroll
           for (int j = 0; j < JC; ++j) {
             const int i = (j0 + j) * 64 + lane;
             if (i >= pieces) continue;
             uint4 v[NV];
-            load_parts<NV, LV>(v, row, pieces, i);
+            load_parts<NV>(v, row, pieces, i);
 #pragma unroll
             for (int r = 0; r < RR; ++r) acc[t][r] = piece_dot<FMT, true, NV>(wv[r][j], sc[r][j], v, acc[t][r]);
           }
@@ -620,7 +616,7 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
           quant_row<false, 64, 4>(static_cast<const uint16_t*>(p.h) + (size_t)q * p.f, p.f,
                                   reinterpret_cast<int8_t*>(sh) + (size_t)q * p.f, s_hs + q, nullptr);
       } else {
-        stage_rows<Fmt<FMT>::ND>(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n, p.f / Fmt<FMT>::E, i, NT);
+        stage_rows(sh, static_cast<const uint4*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h), n * (p.f / Fmt<FMT>::E) * Fmt<FMT>::ND, i, NT);
       }
       __syncthreads();
     });
@@ -648,7 +644,7 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
 
 // ---- launches -----------------------------------------------------------------------------------
 constexpr int kUnits = 256;           // compute units
-constexpr size_t kVecLds = 96 << 10;  // most of a block's LDS for rows of x or h
+constexpr size_t kVecLds = 136 << 10;  // most of a block's LDS for rows of x, or for results and rows of h
 // Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
 constexpr size_t kOwnRows = 32 << 10;
 
@@ -712,7 +708,7 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
   A.idx = L.idx;
   A.gates = L.gates;
   A.grouped = static_cast<Grouped*>(L.grouped);
-  A.xq = L.xq;
+  A.xv = L.fmt == FT_W_BF16 ? const_cast<uint16_t*>(L.x) : L.xv;
   A.xs = L.xs;
   A.hq = L.hq;
   A.hs = L.hs;
@@ -723,14 +719,15 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
   // few logits a wavefront: their sums run in a fixed order and so one behind the other
   const int tt = L.T == 1 ? 1 : L.T <= 16 ? 2 : 4, te = L.T == 1 ? 1 : 2;
   const int eb = (L.E + 4 * te - 1) / (4 * te), blocks = eb * ((L.T + tt - 1) / tt);
-  const dim3 grid((unsigned)(blocks + (L.fmt == FT_W_I8 ? L.T : 0)));
+  const dim3 grid((unsigned)(blocks + (L.fmt == FT_W_BF16 ? 0 : L.T)));
   auto logits = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, A, L.w_router, L.logits, eb, blocks); };
+  auto by_format = [&](auto bf16, auto mx, auto i8) { L.fmt == FT_W_BF16 ? logits(bf16) : L.fmt == FT_W_MXFP4 ? logits(mx) : logits(i8); };
   if (tt == 1)
-    logits(moe_logits_kernel<1, 1>);
+    by_format(moe_logits_kernel<FT_W_BF16, 1, 1>, moe_logits_kernel<FT_W_MXFP4, 1, 1>, moe_logits_kernel<FT_W_I8, 1, 1>);
   else if (tt == 2)
-    logits(moe_logits_kernel<2, 2>);
+    by_format(moe_logits_kernel<FT_W_BF16, 2, 2>, moe_logits_kernel<FT_W_MXFP4, 2, 2>, moe_logits_kernel<FT_W_I8, 2, 2>);
   else
-    logits(moe_logits_kernel<4, 2>);
+    by_format(moe_logits_kernel<FT_W_BF16, 4, 2>, moe_logits_kernel<FT_W_MXFP4, 4, 2>, moe_logits_kernel<FT_W_I8, 4, 2>);
   if (int st = launched("moe_logits_kernel")) return st;
   if (L.fmt == FT_W_I8) return moe_go<FT_W_I8, 16>(A, s);
   if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 8>(A, s);
