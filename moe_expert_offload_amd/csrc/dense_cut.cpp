@@ -113,11 +113,97 @@ size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward) {
   return part_bound(T, [&](int64_t t) { return gated_ffn_part_bytes(t, d, d_ff, backward); });
 }
 
-size_t i8_part_bytes(int64_t T, int64_t n, int K) {
-  return T <= kSkinnyRows ? 0 : cut_of(T, n, i8_stages(K)).part_bytes;
+// Products in 8-bit integers.  Each way's time in us, by what was measured from 17 to 8192 rows at (N, K) of (2048, 2048),
+// (5632, 2048), (4096, 4096), (11008, 4096) and (4096, 11008): 3 for the launch, and for each round of blocks
+//   64 x 128 tiles, two to a unit, three stages in LDS: 0.45 a stage while there is one to a unit, 0.78 for two, + 1.5
+//   128 x 128 tiles, two to a unit: 0.85 to 1.1, + 2.5; one to a unit, three stages: 0.64, + 2.2
+//   128 x 256 tiles, one to a unit: 0.88, with more than 192 of them up to 1.05, + 2
+//   256 x 256 tiles, one to a unit: 1.2, with more than 140 of them up to 1.85 (power), + 3
+//   joining shared tiles: 4.5, and what the pieces write and the join reads
+// against 3 us and the weights at 2.8 (up to 32 rows) or 1.5 TB/s where they stream (up to 64 rows; each 16 channels
+// read all tokens' codes, which is what bounds that way).  The best of all ways that were timed is within 10 % of the
+// one chosen at three sizes in four.
+I8Cut i8_cut_of(int64_t M, int64_t n, int K) {
+  const int stages = i8_stages(K);
+  I8Cut best{};
+  double cost = 1e30;
+  if (M <= 16) return best;
+  if (M <= kSkinnyRows) cost = 3 + (double)n * K * (M <= 32 ? 0.36e-6 : 0.66e-6);
+  auto up = [](double v) { return v > 0 ? v : 0.0; };
+  // all tiles shared alike by k blocks, `slots` blocks at once; us(blocks): a stage of a round of so many
+  auto even = [&](int tile, bool deep, int bm, int slots, double fixed, double piece, int most, auto us) {
+    const int64_t tm = (M + bm - 1) / bm, tn = (n + 127) / 128, tiles = tm * tn;
+    for (int k = 1; k <= most; k *= 2) {
+      const int per = (stages + k - 1) / k, blocks = (stages + per - 1) / per;
+      if (k > 1 && (blocks < k || per < 2 || tiles * blocks > slots)) break;
+      const int64_t b = tiles * blocks, last = b % slots;
+      double t = 3 + (double)(b / slots) * (us(slots) * per + fixed);
+      if (last) t += us((double)last) * per + fixed;
+      if (k > 1) t += 4.5 + piece * (double)b;
+      if (t >= cost) continue;
+      cost = t;
+      best = I8Cut{};
+      best.tile = tile;
+      best.deep = deep;
+      best.tiles_m = (int)tm;
+      best.tiles_n = (int)tn;
+      best.whole = best.parts = (int)b;
+      best.blocks = blocks;
+      best.per = per;
+      if (k > 1) {
+        best.rest = (int)tiles;
+        best.part_bytes = (size_t)b * bm * 128 * 4;
+      }
+    }
+  };
+  even(64, false, 64, 2 * kUnits, 1.5, 0.01, 8, [&](double b) { return b <= 256 ? 0.45 : 0.5 + 0.28 * (b - 256) / 256; });
+  even(128, true, 128, kUnits, 2.2, 0.012, 4, [&](double) { return 0.64; });
+  even(128, false, 128, 2 * kUnits, 2.5, 0.012, 1, [&](double b) { return 0.85 + 0.25 * up(b - 256) / 256; });
+  for (int mh = 1; mh <= 2; ++mh) {
+    I8Cut d{};
+    d.tile = mh == 2 ? 256 : 384;
+    d.tiles_m = (int)((M + 128 * mh - 1) / (128 * mh));
+    d.tiles_n = (int)((n + 255) / 256);
+    const int64_t tiles = (int64_t)d.tiles_m * d.tiles_n;
+    d.whole = (int)tiles;
+    const double fixed = mh == 2 ? 3 : 2, piece = mh == 2 ? 0.045 : 0.02;
+    auto us = [&](double b) { return mh == 2 ? 1.2 + 0.65 * up(b - 140) / 116 : 0.88 + 0.17 * up(b - 192) / 64; };
+    double t = 3 + (double)(tiles / kUnits) * (us(kUnits) * stages + fixed);
+    const int rest = (int)(tiles % kUnits);
+    if (rest) {
+      double last = us(rest) * stages + fixed;
+      auto offer = [&](int group, int blocks) {
+        const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
+        if (groups * blocks > kUnits || per < 4 || per >= stages) return;
+        const double u = us(groups * blocks) * per + fixed + 4.5 + piece * (groups * blocks);
+        if (u >= last) return;
+        last = u;
+        d.rest = rest;
+        d.whole = (int)tiles - rest;
+        d.group = group;
+        d.blocks = blocks;
+        d.per = per;
+        d.parts = groups * blocks;
+        d.part_bytes = (size_t)(d.parts + rest) * mh * 128 * 256 * 4;
+      };
+      for (int k = 2; k <= 8; ++k) offer(1, k);
+      offer(2, 3);
+      offer(3, 4);
+      t += last;
+    }
+    if (t < cost) {
+      cost = t;
+      best = d;
+    }
+  }
+  return best;
 }
+
+size_t i8_part_bytes(int64_t T, int64_t n, int K) { return i8_cut_of(T, n, K).part_bytes; }
+// (between 17 and 64 rows the cut changes at 33 alone)
 size_t i8_part_bound(int64_t T, int64_t n, int K) {
-  return part_bound(T, [&](int64_t t) { return i8_part_bytes(t, n, K); });
+  const size_t few = T > 16 ? i8_part_bytes(32, n, K) : 0, all = part_bound(T, [&](int64_t t) { return i8_part_bytes(t, n, K); });
+  return few > all ? few : all;
 }
 
 }  // namespace ft

@@ -265,8 +265,8 @@ __device__ __forceinline__ void load_scales(const I8Args& p, uint32_t lds, int m
 
 // What becomes of one 32-row piece of a wave's sums: c0 and c1 are its 32x32 results at channels n0 + b0 and
 // n0 + b1 (kGateUp: gate and up of the same ones).  The lane holds row `r` of the tile, and in quad q the
-// channels 8 q + 4 hi + 0..3 of each.  ts: the tile's scales, of BM tokens first.
-template <int MODE, bool H, int BM, int BN>
+// channels 8 q + 4 hi + 0..3 of each.  scales: the tile's, of BM tokens first.  QH >= 0: quads 2 QH and 2 QH + 1 alone.
+template <int MODE, bool H, int BM, int BN, int QH = -1>
 __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0, const i32x16_t& c1, const float* scales,
                                             int m0, int r, int n0, int b0, int b1, int hi) {
   const int m = m0 + r;
@@ -275,7 +275,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
   const float4* cs = reinterpret_cast<const float4*>(scales + BM);
   if constexpr (MODE == kGateUp) {
 #pragma unroll
-    for (int q = 0; q < 4; q += 2) {
+    for (int q = QH > 0 ? 2 : 0; q < (QH == 0 ? 2 : 4); q += 2) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -299,7 +299,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
       const int b = j ? b1 : b0;
       const i32x16_t& c = j ? c1 : c0;
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
+      for (int q = QH > 0 ? 2 : 0; q < (QH == 0 ? 2 : 4); q += 2) {
         float v[8];  // after the exchange: channels b + 8 (q + hi) .. + 7
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -370,19 +370,26 @@ __device__ __forceinline__ void store_part(int* at, const i32x16_t (&c)[2], int 
 #pragma unroll
     for (int q = 0; q < 4; ++q) d[(j * 4 + q) * 64] = i32x4_t{c[j][4 * q], c[j][4 * q + 1], c[j][4 * q + 2], c[j][4 * q + 3]};
 }
-__device__ __forceinline__ void add_part(i32x16_t (&c)[2], const int* at, int lane) {
-  const i32x4_t* d = reinterpret_cast<const i32x4_t*>(at) + lane;
-  i32x4_t v[2][4];
+// The sums of `n` pieces, `stride` numbers apart: quads 2 QH and 2 QH + 1 of both results, four pieces' loads at once.
+template <int QH>
+__device__ __forceinline__ void sum_parts(i32x16_t (&c)[2], const int* at, size_t stride, int n, int lane) {
+  c[0] = c[1] = i32x16_t{};
+  for (int b0 = 0; b0 < n; b0 += 4) {
+    i32x4_t v[4][4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+    for (int b = 0; b < 4; ++b) {
+      const i32x4_t* d = reinterpret_cast<const i32x4_t*>(at + (size_t)min(b0 + b, n - 1) * stride) + lane;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[j][q] = d[(j * 4 + q) * 64];
+      for (int e = 0; e < 4; ++e) v[b][e] = d[((e >> 1) * 4 + 2 * QH + (e & 1)) * 64];
+    }
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+    for (int b = 0; b < 4; ++b)
+      if (b0 + b < n)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[j][4 * q + e] += v[j][q][e];
+          for (int i = 0; i < 4; ++i) c[e >> 1][4 * (2 * QH + (e & 1)) + i] += v[b][e][i];
+  }
 }
 
 // The places of operands in LDS, the walk over k and the cut into shared tiles are those of the 16-bit
@@ -390,13 +397,15 @@ __device__ __forceinline__ void add_part(i32x16_t (&c)[2], const int* at, int la
 // here 128 k, and an MFMA of 32 k takes the cycles of one of 16 there, so the same bytes are
 // loaded and read in the same time for twice the operations.
 
-// 128 x 128 tiles, 4 waves of 64 x 64: both operands straight into one of two LDS buffers, a stage ahead.
-template <int MODE, bool H>
+// BM x 128 tiles, BM 128 or 64: 4 waves of BM / 2 x 64, both operands straight into one of S LDS buffers, S - 1 stages
+// ahead.  Loads past the last stage are masked (they write zeros nobody reads), which keeps the count of the wait.
+template <int MODE, bool H, int BM, int S>
 __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   constexpr bool GU = MODE == kGateUp;
-  constexpr int SBYTES = 32768;
-  __shared__ __attribute__((aligned(1024))) uint8_t sm[2 * SBYTES];
-  __shared__ __attribute__((aligned(16))) float scales[256];
+  constexpr int MT = BM / 64, ABYTES = BM * 128, SBYTES = ABYTES + 16384;
+  constexpr int LA = BM / 32, LB = 4;  // 1 KB loads a wave issues a stage
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];  // S * SBYTES
+  __shared__ __attribute__((aligned(16))) float scales[BM + 128];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, hi = lane >> 5, l31 = lane & 31;
   const int stages = (p.K + 127) >> 7;
@@ -406,89 +415,106 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   const int s_begin = p.rest ? (lb - tile * p.blocks) * p.per : 0;
   const int s_end = p.rest ? min(stages, s_begin + p.per) : stages;
   const TilePos tp = tile_pos(p, tile);
-  const int m0 = tp.m * 128, n0 = tp.n * (GU ? 64 : 128);
+  const int m0 = tp.m * BM, n0 = tp.n * (GU ? 64 : 128);
 
-  uint32_t offA[4], offB[4];
-  int kq[4];  // first k of the piece within the stage
+  uint32_t offA[LA], offB[LB];
+  int kA[LA], kB[LB];  // first k of the piece within the stage
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = (wave * 4 + j) * 8 + (lane >> 3), pc = (lane & 7) ^ ((r >> 1) & 7);
-    const int n = GU ? (r >> 6) * 32 + (r & 31) : r;  // blocks of 32 rows alternate between gate and up
-    kq[j] = pc * 16;
+  for (int j = 0; j < LA; ++j) {
+    const int r = (wave * LA + j) * 8 + (lane >> 3), pc = (lane & 7) ^ ((r >> 1) & 7);
+    kA[j] = pc * 16;
     offA[j] = m0 + r < p.M ? (uint32_t)(r * p.lda + pc * 16) : kOOB;
+  }
+#pragma unroll
+  for (int j = 0; j < LB; ++j) {
+    const int r = (wave * LB + j) * 8 + (lane >> 3), pc = (lane & 7) ^ ((r >> 1) & 7);
+    const int n = GU ? (r >> 6) * 32 + (r & 31) : r;  // blocks of 32 rows alternate between gate and up
+    kB[j] = pc * 16;
     offB[j] = n0 + n < p.N ? (uint32_t)(n * p.K + pc * 16) : kOOB;
   }
   const uint32_t sm0 = lds_addr(sm);
-  auto load_stage = [&](int s) {
-    const int k0 = s << 7, left = p.K - k0;
-    const uint32_t dst = sm0 + (s & 1) * SBYTES;
+  auto load_stage = [&](int s, int place) {
+    const int k0 = s << 7, left = s < s_end ? p.K - k0 : 0;
+    const uint32_t dst = sm0 + place * SBYTES;
     const auto ra = rsrc_of(p.a + m0 * p.lda + k0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) lds_load16(ra, kq[j] < left ? offA[j] : kOOB, 0, dst + (wave * 4 + j) * 1024);
+    for (int j = 0; j < LA; ++j) lds_load16(ra, kA[j] < left ? offA[j] : kOOB, 0, dst + (wave * LA + j) * 1024);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int8_t* w = GU && ((wave * 4 + j) & 4) ? p.b2 : p.b;
-      lds_load16(rsrc_of(w + (int64_t)n0 * p.K + k0), kq[j] < left ? offB[j] : kOOB, 0, dst + 16384 + (wave * 4 + j) * 1024);
+    for (int j = 0; j < LB; ++j) {
+      const int8_t* w = GU && ((wave * LB + j) & 4) ? p.b2 : p.b;
+      lds_load16(rsrc_of(w + (int64_t)n0 * p.K + k0), kB[j] < left ? offB[j] : kOOB, 0, dst + ABYTES + (wave * LB + j) * 1024);
     }
   };
   auto frag = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
     return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
   };
-  i32x16_t acc[2][2];
+  i32x16_t acc[MT][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
-  load_scales<MODE, 128, 128>(p, lds_addr(scales), m0, n0, wave, lane);
-  if (s_begin < s_end) load_stage(s_begin);
+  for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
+  load_scales<MODE, BM, 128>(p, lds_addr(scales), m0, n0, wave, lane);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) load_stage(s_begin + i, i);
+  int here = 0;
   for (int s = s_begin; s < s_end; ++s) {
     // this wave's loads of stage s have landed; past the barrier everyone's have, and nobody
-    // reads the other buffer any more
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // reads the buffer before it any more
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * (LA + LB)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + 1 < s_end) load_stage(s + 1);
-    const uint8_t *sa = sm + (s & 1) * SBYTES, *sb = sa + 16384;
+    load_stage(s + S - 1, here == 0 ? S - 1 : here - 1);
+    const uint8_t *sa = sm + here * SBYTES, *sb = sa + ABYTES;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      i32x4_t fa[2], fb[2];
+      i32x4_t fa[MT], fb[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) fb[j] = frag(sb, wn * 64 + j * 32, k);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) fa[i] = frag(sa, wm * 64 + i * 32, k);
+      for (int i = 0; i < MT; ++i) fa[i] = frag(sa, wm * (BM / 2) + i * 32, k);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(fb[j], fa[i], acc[i][j]);
     }
     // the reads above are done before anyone passes the next barrier
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    here = here == S - 1 ? 0 : here + 1;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the masked loads too: LDS is another block's afterwards
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < MT; ++i) {
     if (p.rest) {
-      store_part(p.part + (size_t)lb * (128 * 128) + (wave * 2 + i) * 2048, acc[i], lane);
+      store_part(p.part + (size_t)lb * (BM * 128) + (wave * MT + i) * 2048, acc[i], lane);
     } else {
       const int b = wn * (GU ? 32 : 64);
-      i8_epilogue<MODE, H, 128, 128>(p, acc[i][0], acc[i][1], scales, m0, wm * 64 + i * 32 + l31, n0, b, b + 32, hi);
+      i8_epilogue<MODE, H, BM, 128>(p, acc[i][0], acc[i][1], scales, m0, wm * (BM / 2) + i * 32 + l31, n0, b, b + 32, hi);
     }
   }
 }
 
-// The shared tiles of the kernel above: a block per tile and 32-row piece of the waves.
-template <int MODE, bool H>
+// The shared tiles of the kernel above: a block per tile, 32-row piece of the waves and half of their quads.
+template <int MODE, bool H, int BM>
 __global__ __launch_bounds__(256) void i8_join128_kernel(I8Args p) {
+  constexpr int MT = BM / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1, t = blockIdx.x >> 1, i = blockIdx.x & 1;
-  __shared__ __attribute__((aligned(16))) float scales[256];
+  const int wm = wave >> 1, wn = wave & 1, t = blockIdx.x / (2 * MT), i = (blockIdx.x >> 1) % MT;
+  __shared__ __attribute__((aligned(16))) float scales[BM + 128];
   const TilePos tp = tile_pos(p, t);
-  const int m0 = tp.m * 128, n0 = tp.n * (MODE == kGateUp ? 64 : 128), r = wm * 64 + i * 32;
-  stage_scales<MODE, 128, 128, 256>(p, scales, m0, n0);
+  const int m0 = tp.m * BM, n0 = tp.n * (MODE == kGateUp ? 64 : 128), r = wm * (BM / 2) + i * 32;
+  stage_scales<MODE, BM, 128, 256>(p, scales, m0, n0);
   __syncthreads();
   if (m0 + r >= p.M) return;
-  i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
-  for (int b = 0; b < p.blocks; ++b)
-    add_part(acc, p.part + (size_t)(t * p.blocks + b) * (128 * 128) + (wave * 2 + i) * 2048, lane);
+  const int* at = p.part + (size_t)t * p.blocks * (BM * 128) + (wave * MT + i) * 2048;
   const int c = wn * (MODE == kGateUp ? 32 : 64);
-  i8_epilogue<MODE, H, 128, 128>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, c, c + 32, lane >> 5);
+  auto half = [&](auto h) {
+    constexpr int QH = decltype(h)::value;
+    i32x16_t acc[2];
+    sum_parts<QH>(acc, at, BM * 128, p.blocks, lane);
+    i8_epilogue<MODE, H, BM, 128, QH>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, c, c + 32, lane >> 5);
+  };
+  if (blockIdx.x & 1)
+    half(std::integral_constant<int, 1>{});
+  else
+    half(std::integral_constant<int, 0>{});
 }
 
 // 128 MH x 256 tiles, 8 waves, each 64 rows and 32 channels of every 128 x 128 quarter.  A stage is regions of
@@ -687,11 +713,12 @@ __global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
   }
 }
 
-// The tiles whose stages several blocks shared: a block per tile and 32-row piece of the waves; bound by memory.
+// The tiles whose stages several blocks shared: a block per tile, 32-row piece of the waves and half of their quads;
+// bound by memory.
 template <int MODE, bool H, int MH>
 __global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, i = blockIdx.x % (2 * MH), t = blockIdx.x / (2 * MH);
+  const int wm = wave >> 2, wn = wave & 3, i = (blockIdx.x >> 1) % (2 * MH), t = blockIdx.x / (4 * MH);
   const int stages = (p.K + 127) >> 7;
   const int g = t / p.group, from = (t - g * p.group) * stages;
   const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
@@ -702,9 +729,18 @@ __global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
   stage_scales<MODE, MH * 128, 256, 512>(p, scales, m0, n0);
   __syncthreads();
   if (m0 + r >= p.M) return;
-  i32x16_t acc[2] = {i32x16_t{}, i32x16_t{}};
-  for (int b = first; b <= last; ++b) add_part(acc, p.part + (size_t)(b + t) * (MH * 128 * 256) + (wave * 2 * MH + i) * 2048, lane);
-  i8_epilogue<MODE, H, MH * 128, 256>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, wn * 32, wn * 32 + 128, lane >> 5);
+  constexpr int PART = MH * 128 * 256;
+  const int* at = p.part + (size_t)(first + t) * PART + (wave * 2 * MH + i) * 2048;
+  auto half = [&](auto h) {
+    constexpr int QH = decltype(h)::value;
+    i32x16_t acc[2];
+    sum_parts<QH>(acc, at, PART, last - first + 1, lane);
+    i8_epilogue<MODE, H, MH * 128, 256, QH>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, wn * 32, wn * 32 + 128, lane >> 5);
+  };
+  if (blockIdx.x & 1)
+    half(std::integral_constant<int, 1>{});
+  else
+    half(std::integral_constant<int, 0>{});
 }
 
 // ---- launches -------------------------------------------------------------------------
@@ -713,7 +749,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 
 template <int MODE, bool H>
 int i8_go(I8Args& A, hipStream_t s) {
-  if (A.M <= kSkinnyRows) {
+  const I8Cut c = i8_cut_of(A.M, MODE == kGateUp ? 2 * (int64_t)A.N : A.N, A.K);
+  if (c.tile == 0) {
     constexpr int RB = MODE == kGateUp ? 8 : 16;
     const unsigned nb = (unsigned)((A.N + RB - 1) / RB);
     // 16 waves a block where there are few blocks (one token, K = N = 4096: 7.6 us, with 8 waves 9.0), else 8 (K = 4096,
@@ -739,7 +776,6 @@ int i8_go(I8Args& A, hipStream_t s) {
   }
   const size_t es = A.c_f32 ? 4 : 2;
   A.wide = A.N % 8 == 0 && aligned(A.c, 16) && aligned(A.res, 16) && A.ldc * es % 16 == 0 && (!A.res || A.ldr * es % 16 == 0);
-  const Cut c = cut_of(A.M, MODE == kGateUp ? 2 * (int64_t)A.N : A.N, i8_stages(A.K));
   A.tiles_m = c.tiles_m;
   A.tiles_n = c.tiles_n;
   A.whole = c.whole;
@@ -750,13 +786,21 @@ int i8_go(I8Args& A, hipStream_t s) {
   A.parts = c.parts;
   if (c.tile == 256) {
     hipLaunchKernelGGL((i8_tile256_kernel<MODE, H, 2>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
-    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 2>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 2>), dim3((unsigned)c.rest * 8), dim3(512), 0, s, A);
   } else if (c.tile == 384) {
     hipLaunchKernelGGL((i8_tile256_kernel<MODE, H, 1>), dim3((unsigned)(c.whole + c.parts)), dim3(512), 0, s, A);
-    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 1>), dim3((unsigned)c.rest * 2), dim3(512), 0, s, A);
+    if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 1>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
   } else {
-    hipLaunchKernelGGL((i8_tile128_kernel<MODE, H>), dim3((unsigned)c.parts), dim3(256), 0, s, A);
-    if (c.rest) hipLaunchKernelGGL((i8_join128_kernel<MODE, H>), dim3((unsigned)c.rest * 2), dim3(256), 0, s, A);
+    auto go = [&](auto tile, size_t stage, int deep, auto join, unsigned pieces) {
+      hipLaunchKernelGGL(tile, dim3((unsigned)c.parts), dim3(256), deep * stage, s, A);
+      if (c.rest) hipLaunchKernelGGL(join, dim3((unsigned)c.rest * pieces), dim3(256), 0, s, A);
+    };
+    if (c.tile == 64)
+      go(i8_tile128_kernel<MODE, H, 64, 3>, 24576, 3, i8_join128_kernel<MODE, H, 64>, 2);
+    else if (c.deep)
+      go(i8_tile128_kernel<MODE, H, 128, 3>, 32768, 3, i8_join128_kernel<MODE, H, 128>, 4);
+    else
+      go(i8_tile128_kernel<MODE, H, 128, 2>, 32768, 2, i8_join128_kernel<MODE, H, 128>, 4);
   }
   return launched("i8_tile_kernel");
 }
