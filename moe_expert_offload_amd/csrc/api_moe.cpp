@@ -43,7 +43,7 @@ Layout layout(const ft_shape* s, int32_t T) {
     l.h = take(P * s->d_ff * 2);
   } else {
     if (s->fmt == FT_W_MXFP4) l.xv = take((size_t)T * s->d * 2);
-    l.h = take(P * s->d_ff * 4);
+    l.h = take(P * s->d_ff * 6);  // fp32, or three bf16 numbers
   }
   l.total = at + 256;
   return l;

@@ -244,7 +244,7 @@ struct MoeLayer {
   void* xv;        // MXFP4: x [T, d] in another order; 8-bit records: codes of x, of h [T k, d_ff], and their scales
   int8_t* hq;
   float *xs, *hs;
-  void* h;  // [T k, d_ff] fp32, 8-bit records bf16
+  void* h;  // [T k, d_ff], 6 bytes an element; 8-bit records bf16
 };
 int launch_moe_layer(const MoeLayer& L, void* stream);
 

@@ -3,7 +3,7 @@
 //   logits = x W_r^T; the k largest of the allowed experts; gates = softmax over those
 //   y[t] = sum over j of gates[t, j] * Wd_e (silu(Wg_e x[t]) * (Wu_e x[t])), e = idx[t, j] (+ residual[t])
 //
-// Three launches: the logits, gate/up and down.  The second does the top-k of every token and groups
+// Three launches (8-bit records of more than a few pairs: a fourth for h's codes): the logits, gate/up and down.  The second does the top-k of every token and groups
 // the routed pairs by expert, every block by itself (in LDS; a layer of 64 tokens has 512 pairs at most),
 // so that no launch and no wait across blocks lies between; the third sums a token's experts where they
 // leave their product, so there is no combine.  Both stream the routed experts' rows once, whatever
@@ -15,6 +15,8 @@
 // x and the fp32 h.  8-bit records: x and h in 8 bits as ft_i8_quant gives them (h rounded to bf16 before),
 // whole-number sums, as the blocks of kernels_i8.hip.
 #include <climits>
+#include <cmath>
+#include <type_traits>
 
 #include "i8_common.h"
 #include "router_device.h"
@@ -230,7 +232,7 @@ __device__ __forceinline__ int row_bytes(int n) {
 struct Plan : Grouped {
   int32_t id[FT_PLAN_CAP];  // expert of a pair
   int32_t first[FT_E_MAX];  // an expert's first pair, then its group
-  int32_t count[FT_PLAN_CAP];
+  unsigned long long tokens[FT_PLAN_CAP];  // a group's, a bit each: a token takes an expert once
   int32_t wave_sum[NW];
 };
 
@@ -263,8 +265,8 @@ __device__ __forceinline__ int slot_of(const MoeArgs& p, int id) {
   return slot >= 0 && slot < p.n_slots ? slot : -1;
 }
 
-// Groups in the order of their first pair; pairs within a group in any order (each one's results are its own).
-// id and gate are set.  Up to 64 pairs, by one wavefront: a lane a pair.
+// Groups in the order of their first pair, pairs within a group in theirs (every block makes the same plan).  id and
+// gate are set.  Up to 64 pairs, by one wavefront: a lane a pair.
 __device__ void plan_of_a_wave(Plan& P, const MoeArgs& p, int lane) {
   const int n = p.T * p.k;
   const int id = lane < n ? P.id[lane] : -1, slot = slot_of(p, id);
@@ -299,7 +301,7 @@ __device__ void plan_of_a_wave(Plan& P, const MoeArgs& p, int lane) {
 __device__ void plan_of_a_block(Plan& P, const MoeArgs& p) {
   const int n = p.T * p.k, i = threadIdx.x;
   for (int e = i; e < p.E; e += NT) P.first[e] = INT_MAX;
-  if (i < FT_PLAN_CAP) P.count[i] = 0;
+  if (i < FT_PLAN_CAP) P.tokens[i] = 0;
   __syncthreads();
   const int id = i < n ? P.id[i] : -1, slot = slot_of(p, id);
   if (slot >= 0) atomicMin(&P.first[id], i);
@@ -312,13 +314,13 @@ __device__ void plan_of_a_block(Plan& P, const MoeArgs& p) {
     P.slot[rank] = slot;
   }
   __syncthreads();
-  int at = 0;
-  const int grp = slot >= 0 ? P.first[id] : -1;
+  const int grp = slot >= 0 ? P.first[id] : -1, token = i / p.k;
   if (i < n) P.grp[i] = grp;
-  if (grp >= 0) at = atomicAdd(&P.count[grp], 1);
+  if (grp >= 0) atomicOr(&P.tokens[grp], 1ull << token);
   __syncthreads();
+  const int at = grp >= 0 ? __popcll(P.tokens[grp] & ((1ull << token) - 1)) : 0;
   int pairs;
-  const int off = block_prefix(i < groups ? P.count[i] : 0, P.wave_sum, pairs);
+  const int off = block_prefix(i < groups ? __popcll(P.tokens[i]) : 0, P.wave_sum, pairs);
   if (i <= groups) P.off[i] = off;
   __syncthreads();
   if (grp >= 0) P.pair[P.off[grp] + at] = i;
@@ -457,17 +459,9 @@ __device__ __forceinline__ void up_units(const MoeArgs& p, const Plan& P, const 
   }
 }
 
-template <int FMT, int JC, int RG>
-__global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
-  __shared__ Plan P;
-  extern __shared__ uint4 vec[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = p.T * p.k;
-  if (p.lds_vec) {
-    // with few tokens, by the wavefronts that have none to rank
-    const int skip = p.T <= NW / 2 ? p.T * 64 : 0;
-    if ((int)threadIdx.x >= skip)
-      stage_rows(vec, static_cast<const uint4*>(p.xv), p.T * (p.d / Fmt<FMT>::E) * Fmt<FMT>::NU, threadIdx.x - skip, NT - skip);
-  }
+// The top-k of all tokens and their grouping, by every block for itself; the first one leaves both in memory.
+__device__ __forceinline__ void routes(const MoeArgs& p, Plan& P, int lane, int wave) {
+  const int n = p.T * p.k;
   if (p.E <= 64)
     topk_rows<1>(p, P, lane, wave);
   else if (p.E <= 128)
@@ -496,6 +490,20 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
     if (i <= n) p.grouped->off[i] = P.off[i];
     if (i == 0) p.grouped->groups = P.groups;
   }
+}
+
+template <int FMT, int JC, int RG>
+__global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
+  __shared__ Plan P;
+  extern __shared__ uint4 vec[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (p.lds_vec) {
+    // with few tokens, by the wavefronts that have none to rank
+    const int skip = p.T <= NW / 2 ? p.T * 64 : 0;
+    if ((int)threadIdx.x >= skip)
+      stage_rows(vec, static_cast<const uint4*>(p.xv), p.T * (p.d / Fmt<FMT>::E) * Fmt<FMT>::NU, threadIdx.x - skip, NT - skip);
+  }
+  routes(p, P, lane, wave);
   if (p.lds_vec)
     up_units<FMT, JC, RG, true>(p, P, vec);
   else
@@ -506,6 +514,39 @@ __global__ __launch_bounds__(NT) void moe_up_kernel(MoeArgs p) {
 // A block owns p.rows rows of every expert's W_down and so of y; its wavefronts take units of RR rows of one
 // group.  A pair's results wait in LDS until all are there, then each token's are added in the order of j.
 constexpr int kDownRows = 16;
+
+__device__ __forceinline__ void grouped_to_lds(const MoeArgs& p, Grouped& P) {
+  const Grouped& G = *p.grouped;
+  const int n = p.T * p.k, i = threadIdx.x;
+  if (i < n) {
+    P.grp[i] = G.grp[i];
+    P.gate[i] = G.gate[i];
+    P.pair[i] = G.pair[i];
+    P.slot[i] = G.slot[i];
+  }
+  if (i <= n) P.off[i] = G.off[i];
+  if (i == 0) P.groups = G.groups;
+}
+// y of the block's rows from all pairs' results.
+__device__ __forceinline__ void sum_experts(const MoeArgs& p, const Grouped& P, const float* out) {
+  const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
+  for (int e = threadIdx.x; e < p.T * nr; e += NT) {
+    const int t = e / nr, r = e - t * nr;
+    const size_t at = (size_t)t * p.d + b0 + r;
+    float s = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const int q = t * p.k + j;
+      if (P.grp[q] >= 0) s = fmaf(P.gate[q], out[q * kDownRows + r], s);
+    }
+    if (p.y_f32) {
+      if (p.res) s += static_cast<const float*>(p.res)[at];
+      static_cast<float*>(p.y)[at] = s;
+    } else {
+      if (p.res) s += to_f32<false>(static_cast<const uint16_t*>(p.res)[at]);
+      static_cast<uint16_t*>(p.y)[at] = (uint16_t)pack2<false>(s, 0.0f);
+    }
+  }
+}
 
 template <int FMT, int JC, int RR, bool LV, class Stage>
 __device__ __forceinline__ void down_units(const MoeArgs& p, const Grouped& P, const uint4* sh, const float* hs, float* out,
@@ -598,16 +639,8 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
   const int n = p.T * p.k, i = threadIdx.x;
   float* out = reinterpret_cast<float*>(vec);
   uint4* sh = vec + n * kDownRows / 4;
-  const Grouped& G = *p.grouped;
-  if (i < n) {
-    P.grp[i] = G.grp[i];
-    P.gate[i] = G.gate[i];
-    P.pair[i] = G.pair[i];
-    P.slot[i] = G.slot[i];
-    if (FMT == FT_W_I8 && p.hq) s_hs[i] = p.hs[i];
-  }
-  if (i <= n) P.off[i] = G.off[i];
-  if (i == 0) P.groups = G.groups;
+  grouped_to_lds(p, P);
+  if (FMT == FT_W_I8 && p.hq && i < n) s_hs[i] = p.hs[i];
   __syncthreads();
   if (p.lds_vec)
     down_units<FMT, JC, RR, true>(p, P, sh, s_hs, out, [&]() {
@@ -623,30 +656,305 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
   else
     down_units<FMT, JC, RR, false>(p, P, nullptr, s_hs, out, []() {});
   __syncthreads();
-  const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
-  for (int e = i; e < p.T * nr; e += NT) {
-    const int t = e / nr, r = e - t * nr;
-    const size_t at = (size_t)t * p.d + b0 + r;
-    float s = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-      const int q = t * p.k + j;
-      if (P.grp[q] >= 0) s = fmaf(P.gate[q], out[q * kDownRows + r], s);
+  sum_experts(p, P, out);
+}
+
+// ---- many tokens an expert: matrix instructions ----------------------------------------------------
+// The same products for groups of several tokens, cut into parts of up to 16: a tile is 16 rows of an expert (gate/up: 8
+// of each) and the tokens of a part, weights as the MFMA's second operand, so that each is loaded and converted
+// once a part.  Lane l: row (and token) l % 16, in a step the k of its quarter l / 16.  KW wavefronts share a tile's
+// chunks and add their sums in LDS; the block's others take further tiles, and the next chunk, of this tile or the
+// next one, is on its way while one is multiplied.
+//   bf16   v_mfma_f32_16x16x32_bf16
+//   MXFP4  the same on codes turned into bf16 exactly; a step is one block of 32, whose scale multiplies its
+//          fp32 sum; exchanges across the wave bring a lane's block to the quarters
+//   8-bit  v_mfma_i32_16x16x64_i8
+// h stays fp32 for bf16 and MXFP4: it is three bf16 numbers whose sum it is (8 + 8 + 8 bits), each with its own MFMA; the
+// matrix cores have room for that.
+template <int FMT>
+struct Many {
+  static constexpr int KS = FMT == FT_W_I8 ? 64 : 32;   // k of a step
+  static constexpr int EB = FMT == FT_W_I8 ? 1 : 2;     // bytes of an element of x
+  static constexpr int PARTS = FMT == FT_W_I8 ? 1 : 3;  // of h
+  typedef typename std::conditional<FMT == FT_W_I8, int, float>::type One;
+  typedef typename std::conditional<FMT == FT_W_I8, i32x4_t, f32x4_t>::type Acc;
+};
+// A lane's share of a chunk of ST steps: weights, and the tokens' operands (PARTS of each).
+template <int FMT, int PARTS, int ST>
+struct ManyChunk {
+  static constexpr int WL = FMT == FT_W_MXFP4 ? ST / 4 : ST;  // loads: one of MXFP4 codes is four steps
+  uint4 w[WL];
+  uint32_t sc[FMT == FT_W_MXFP4 ? WL : 1];
+  i32x4_t x[ST][PARTS];
+  // Weights: a row of n elements at byte `base` (scales at sbase).  Tokens: a row at `row`, its further parts `plane` bytes
+  // apart.  Past the row's end zeros, of both: x may be an infinity there.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rec, uint32_t base, uint32_t sbase, const uint8_t* row, size_t plane,
+                                       int n, int chunk, int g, bool in) {
+    constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS;
+    if constexpr (FMT == FT_W_MXFP4) {
+#pragma unroll
+      for (int l = 0; l < WL; ++l) {
+        const int k = (chunk * WL + l) * 128;  // n is a multiple of 128
+        w[l] = buf_ld16(rec, in && k < n ? base + (uint32_t)((k + g * 32) >> 1) : kOOB);
+        sc[l] = __builtin_amdgcn_raw_buffer_load_b32(rec, (int)(in && k < n ? sbase + (uint32_t)(k >> 5) : kOOB), 0, 0);
+      }
     }
-    if (p.y_f32) {
-      if (p.res) s += static_cast<const float*>(p.res)[at];
-      static_cast<float*>(p.y)[at] = s;
-    } else {
-      if (p.res) s += to_f32<false>(static_cast<const uint16_t*>(p.res)[at]);
-      static_cast<uint16_t*>(p.y)[at] = (uint16_t)pack2<false>(s, 0.0f);
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+      const int k = (chunk * ST + j) * KS + g * (16 / EB);
+      if constexpr (FMT != FT_W_MXFP4) w[j] = buf_ld16(rec, in && k < n ? base + (uint32_t)(k * EB) : kOOB);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        x[j][q] = *reinterpret_cast<const i32x4_t*>(row + q * plane + (k < n ? k * EB : 0));
+        if (k >= n) x[j][q] = i32x4_t{};
+      }
     }
   }
+  __device__ __forceinline__ void multiply(typename Many<FMT>::Acc& acc) const {
+    if constexpr (FMT == FT_W_I8) {
+#pragma unroll
+      for (int j = 0; j < ST; ++j) acc = mfma16(x[j][0], __builtin_bit_cast(i32x4_t, w[j]), acc);
+    } else if constexpr (FMT == FT_W_BF16) {
+#pragma unroll
+      for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int q = PARTS - 1; q >= 0; --q) acc = mfma16<false>(x[j][q], __builtin_bit_cast(i32x4_t, w[j]), acc);
+    } else {
+#pragma unroll
+      for (int l = 0; l < WL; ++l) {
+        // word j of quarter g to quarter j, word g
+        uint32_t v[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
+        auto s32 = [](uint32_t& a, uint32_t& b) {
+          const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+          a = r.x;
+          b = r.y;
+        };
+        auto s16 = [](uint32_t& a, uint32_t& b) {
+          const u32x2_t r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+          a = r.x;
+          b = r.y;
+        };
+        s32(v[0], v[2]);
+        s32(v[1], v[3]);
+        s16(v[0], v[1]);
+        s16(v[2], v[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const i32x4_t wj = {__builtin_bit_cast(int, mx_pair<0>(v[j])), __builtin_bit_cast(int, mx_pair<1>(v[j])),
+                              __builtin_bit_cast(int, mx_pair<2>(v[j])), __builtin_bit_cast(int, mx_pair<3>(v[j]))};
+          f32x4_t s = {};
+#pragma unroll
+          for (int q = PARTS - 1; q >= 0; --q) s = mfma16<false>(x[4 * l + j][q], wj, s);
+          const float scale = e8m0((sc[l] >> (8 * j)) & 255u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(scale, s[i], acc[i]);
+        }
+      }
+    }
+  }
+};
+
+// The groups in parts of up to 16 pairs.
+struct Parts {
+  int32_t n;
+  int32_t slot[FT_PLAN_CAP], first[FT_PLAN_CAP], pairs[FT_PLAN_CAP];
+  int32_t wave_sum[NW];
+};
+// All threads of the block, a barrier behind the groups' last change; barriers within and behind.
+__device__ void cut_groups(Parts& Q, const Grouped& P) {
+  const int i = threadIdx.x, n = i < P.groups ? P.off[i + 1] - P.off[i] : 0;
+  int total;
+  const int at = block_prefix((n + 15) >> 4, Q.wave_sum, total);
+  for (int t = 0; t * 16 < n; ++t) {
+    Q.slot[at + t] = P.slot[i];
+    Q.first[at + t] = P.off[i] + t * 16;
+    Q.pairs[at + t] = min(16, n - t * 16);
+  }
+  if (i == 0) Q.n = total;
+  __syncthreads();
+}
+
+// Where a tile's operands are, for one lane.
+struct ManyTile {
+  const uint8_t* rp;
+  uint32_t base, sbase;
+  const uint8_t* row;
+  bool in;
+};
+// All tiles of a block, `tile(i)` giving the i-th of `tiles`, its sums left to `done(i, sums)` with sums[(token * 16 + row)]
+// of the KW wavefronts 256 apart.  KW chunks or more.
+template <int FMT, int PARTS, int ST, class Tile, class Done>
+__device__ __forceinline__ void many_tiles(const MoeArgs& p, int tiles, int first, int stride, int kw_log, int n, size_t plane,
+                                           typename Many<FMT>::One (&red)[2][NW * 256], Tile tile, Done done) {
+  constexpr int CK = ST * Many<FMT>::KS;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+  const int KW = 1 << kw_log, kw = wave & (KW - 1), per = NW >> kw_log, chunks = (n + CK - 1) / CK;
+  const int mine = wave >> kw_log;  // of a batch of `per` tiles
+  ManyChunk<FMT, PARTS, ST> next;
+  ManyTile t = tile(first * per + mine);
+  auto load = [&](int c) { next.load(buf_rsrc(t.rp, (uint32_t)p.S), t.base, t.sbase, t.row, plane, n, c, g, t.in); };
+  if (first * per < tiles) load(kw);
+  int buf = 0;
+  for (int b = first; b * per < tiles; b += stride) {
+    typename Many<FMT>::Acc acc = {};
+    for (int c = kw; c < chunks; c += KW) {
+      const ManyChunk<FMT, PARTS, ST> cur = next;
+      if (c + KW < chunks) {
+        load(c + KW);
+      } else if ((b + stride) * per < tiles) {
+        t = tile((b + stride) * per + mine);
+        load(kw);
+      }
+      cur.multiply(acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[buf][wave * 256 + (4 * g + i) * 16 + (lane & 15)] = acc[i];
+    __syncthreads();  // (the other buffer's sums were read before everyone came here)
+    done(b * per, red[buf], KW, per);
+    buf ^= 1;
+  }
+}
+// The wavefronts that share a tile of n elements a row: two chunks each, where there are as many.
+template <int FMT, int ST>
+__device__ __forceinline__ int kw_log_of(int n) {
+  constexpr int CK = ST * Many<FMT>::KS;
+  const int chunks = (n + CK - 1) / CK;
+  return chunks >= 32 ? 4 : chunks >= 16 ? 3 : chunks >= 8 ? 2 : chunks >= 4 ? 1 : 0;
+}
+
+constexpr int kManyPad = 16;  // bytes between rows of x in LDS: 16 tokens' pieces start on different banks
+
+template <int FMT>
+__global__ __launch_bounds__(NT) void moe_up_many_kernel(MoeArgs p) {
+  constexpr int EB = Many<FMT>::EB, ST = FMT == FT_W_MXFP4 ? 8 : 4;
+  typedef typename Many<FMT>::One One;
+  __shared__ Plan P;
+  __shared__ Parts Q;
+  __shared__ One red[2][NW * 256];
+  extern __shared__ uint4 vec[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint8_t* x = static_cast<const uint8_t*>(FMT == FT_W_I8 ? p.xv : (const void*)p.x);
+  if (p.lds_vec) {
+    const int per = p.d * EB / 16;
+    const uint4* src = reinterpret_cast<const uint4*>(x);
+    for (int i = threadIdx.x; i < p.T * per; i += NT) vec[i + i / per * (kManyPad / 16)] = src[i];
+  }
+  routes(p, P, lane, wave);
+  cut_groups(Q, P);
+  const int n16 = lane & 15;
+  const Rec R = rec_of<FMT>(p.d, p.f);
+  const int per_part = p.f / 8, tiles = Q.n * per_part, rb = row_bytes<FMT>(p.d);  // f % 8 == 0
+  many_tiles<FMT, 1, ST>(
+      p, tiles, blockIdx.x, gridDim.x, kw_log_of<FMT, ST>(p.d), p.d, 0, red,
+      [&](int i) {
+        ManyTile t;
+        t.in = i < tiles;
+        const int q = t.in ? i / per_part : 0, row = (t.in ? i - q * per_part : 0) * 8 + (n16 & 7);
+        t.rp = p.rec + (t.in ? (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S : 0);
+        const int tok = t.in ? P.pair[Q.first[q] + min(n16, Q.pairs[q] - 1)] / p.k : 0;
+        t.row = p.lds_vec ? reinterpret_cast<const uint8_t*>(vec) + tok * (p.d * EB + kManyPad) : x + (size_t)tok * p.d * EB;
+        t.base = (n16 < 8 ? 0u : R.up) + (uint32_t)row * (uint32_t)rb;
+        t.sbase = (n16 < 8 ? R.gs : R.us) + (uint32_t)row * (uint32_t)(p.d / 32);
+        return t;
+      },
+      [&](int i0, const One* sums, int KW, int per) {
+        for (int e = threadIdx.x; e < per * 128; e += NT) {
+          const int i = i0 + (e >> 7), tk = (e >> 3) & 15, r = e & 7;
+          if (i >= tiles) continue;
+          const int q = i / per_part;
+          if (tk >= Q.pairs[q]) continue;
+          const One* s = sums + (e >> 7) * KW * 256 + tk * 16 + r;
+          One a = 0, u = 0;
+          for (int w = 0; w < KW; ++w) {
+            a += s[w * 256];
+            u += s[w * 256 + 8];
+          }
+          const int pair = P.pair[Q.first[q] + tk], row = (i - q * per_part) * 8 + r;
+          const size_t at = (size_t)pair * p.f + row;
+          if constexpr (FMT == FT_W_I8) {
+            const float* gs = reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.gs) + row;
+            const float ts = p.xs[pair / p.k], v = act_f(i8_value(a, gs[0], ts), FT_ACT_SILU) * i8_value(u, gs[p.f], ts);
+            static_cast<uint16_t*>(p.h)[at] = (uint16_t)pack2<false>(v, 0.0f);
+          } else {
+            const float v = silu(a) * u;
+            uint16_t* h = static_cast<uint16_t*>(p.h);
+            const size_t plane = (size_t)p.T * p.k * p.f;
+            const uint32_t hi = pack2<false>(v, 0.0f) & 0xffffu;
+            float rest = v - bf_lo(hi);
+            if (!(fabsf(rest) < INFINITY)) rest = 0.0f;  // v not finite, or next to it
+            const uint32_t mid = pack2<false>(rest, 0.0f) & 0xffffu;
+            h[at] = (uint16_t)hi;
+            h[at + plane] = (uint16_t)mid;
+            h[at + 2 * plane] = (uint16_t)pack2<false>(rest - bf_lo(mid), 0.0f);
+          }
+        }
+      });
+}
+
+template <int FMT>
+__global__ __launch_bounds__(NT) void moe_down_many_kernel(MoeArgs p) {
+  constexpr int EB = Many<FMT>::EB, PARTS = Many<FMT>::PARTS, ST = FMT == FT_W_BF16 ? 2 : 4;
+  typedef typename Many<FMT>::One One;
+  __shared__ Grouped P;
+  __shared__ Parts Q;
+  __shared__ One red[2][NW * 256];
+  extern __shared__ uint4 vec[];  // results [pairs][kDownRows]
+  float* out = reinterpret_cast<float*>(vec);
+  const int n_pairs = p.T * p.k, n16 = threadIdx.x & 15;
+  grouped_to_lds(p, P);
+  __syncthreads();
+  cut_groups(Q, P);
+  const Rec R = rec_of<FMT>(p.d, p.f);
+  const int rb = row_bytes<FMT>(p.f);
+  const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
+  const uint8_t* h = static_cast<const uint8_t*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h);
+  many_tiles<FMT, PARTS, ST>(
+      p, Q.n, 0, 1, kw_log_of<FMT, ST>(p.f), p.f, (size_t)n_pairs * p.f * EB, red,
+      [&](int i) {
+        ManyTile t;
+        const bool any = i < Q.n;
+        t.in = any && n16 < nr;
+        const int q = any ? i : 0;
+        t.rp = p.rec + (any ? (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S : 0);
+        t.row = h + (any ? (size_t)P.pair[Q.first[q] + min(n16, Q.pairs[q] - 1)] * p.f * EB : 0);
+        t.base = R.down + (uint32_t)(b0 + n16) * (uint32_t)rb;
+        t.sbase = R.ds + (uint32_t)(b0 + n16) * (uint32_t)(p.f / 32);
+        return t;
+      },
+      [&](int i0, const One* sums, int KW, int per) {
+        for (int e = threadIdx.x; e < per * 256; e += NT) {
+          const int q = i0 + (e >> 8), tk = (e >> 4) & 15, r = e & 15;
+          if (q >= Q.n || tk >= Q.pairs[q] || r >= nr) continue;
+          const One* s = sums + (e >> 8) * KW * 256 + tk * 16 + r;
+          One a = 0;
+          for (int w = 0; w < KW; ++w) a += s[w * 256];
+          const int pair = P.pair[Q.first[q] + tk];
+          if constexpr (FMT == FT_W_I8)
+            out[pair * kDownRows + r] =
+                i8_value(a, reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.ds)[b0 + r], p.hs[pair]);
+          else
+            out[pair * kDownRows + r] = a;
+        }
+      });
+  __syncthreads();
+  sum_experts(p, P, out);
 }
 
 // ---- launches -----------------------------------------------------------------------------------
 constexpr int kUnits = 256;           // compute units
 constexpr size_t kVecLds = 136 << 10;  // most of a block's LDS for rows of x, or for results and rows of h
+constexpr size_t kManyLds = 96 << 10;
 // Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
 constexpr size_t kOwnRows = 32 << 10;
+
+// Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
+// meet if all are equally likely.  us at 4, 6, 8 and 16 tokens an expert, rows against matrix form: bf16 51 / 70, 92 / 131,
+// 86 / 51, 90 / 72; MXFP4 77 / 63, 170 / 127, 192 / 56, 117 / 72 (4 with wider rows: 259 / 355); 8-bit 52 / 43, 87 / 67,
+// 83 / 47, 66 / 46 (3: 101 / 101).
+bool many_tokens(const MoeArgs& A, double least) {
+  const double pairs = (double)A.T * A.k, met = A.E * (1.0 - pow(1.0 - (double)A.k / A.E, A.T));
+  return pairs > least * met;
+}
 
 // A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
 template <int FMT, int W>
@@ -654,6 +962,19 @@ int moe_go(MoeArgs A, hipStream_t s) {
   const size_t P = (size_t)A.T * A.k;
   const size_t xb = (size_t)A.T * A.d * (FMT == FT_W_I8 ? 1 : 2);
   constexpr int E = Fmt<FMT>::E;
+  A.rows = (A.d + kUnits - 1) / kUnits;
+  if (A.rows > kDownRows) A.rows = kDownRows;
+  const unsigned down_blocks = (unsigned)((A.d + A.rows - 1) / A.rows);
+  if (many_tokens(A, FMT == FT_W_BF16 ? 7 : FMT == FT_W_MXFP4 ? 5 : 4)) {
+    const size_t lds = xb + (size_t)A.T * kManyPad;
+    A.lds_vec = lds <= kManyLds;
+    hipLaunchKernelGGL(moe_up_many_kernel<FMT>, dim3(kUnits), dim3(NT), A.lds_vec ? lds : 0, s, A);
+    if (int st = launched("moe_up_many_kernel")) return st;
+    if (FMT == FT_W_I8)
+      if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s)) return st;
+    hipLaunchKernelGGL(moe_down_many_kernel<FMT>, dim3(down_blocks), dim3(NT), P * kDownRows * 4, s, A);
+    return launched("moe_down_many_kernel");
+  }
   A.lds_vec = xb <= kVecLds;
   auto up = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(kUnits), dim3(NT), A.lds_vec ? xb : 0, s, A); };
   const int ju = (A.d / E + 63) / 64;
@@ -674,10 +995,8 @@ int moe_go(MoeArgs A, hipStream_t s) {
     else if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s))
       return st;
   }
-  A.rows = (A.d + kUnits - 1) / kUnits;
-  if (A.rows > kDownRows) A.rows = kDownRows;
   auto down = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((A.d + A.rows - 1) / A.rows)), dim3(NT), ob + (A.lds_vec ? hb : 0), s, A);
+    hipLaunchKernelGGL(kernel, dim3(down_blocks), dim3(NT), ob + (A.lds_vec ? hb : 0), s, A);
   };
   const int jd = (A.f / E + 63) / 64;
   if constexpr (FMT == FT_W_MXFP4)
