@@ -147,13 +147,15 @@ I8Cut i8_cut_of(int64_t M, int64_t n, int K) {
       best.deep = deep;
       best.tiles_m = (int)tm;
       best.tiles_n = (int)tn;
-      best.whole = best.parts = (int)b;
+      if (k == 1) {
+        best.whole = (int)b;
+        continue;
+      }
+      best.rest = (int)tiles;
       best.blocks = blocks;
       best.per = per;
-      if (k > 1) {
-        best.rest = (int)tiles;
-        best.part_bytes = (size_t)b * bm * 128 * 4;
-      }
+      best.parts = (int)b;
+      best.part_bytes = (size_t)b * bm * 128 * 4;
     }
   };
   even(64, false, 64, 2 * kUnits, 1.5, 0.01, 8, [&](double b) { return b <= 256 ? 0.45 : 0.5 + 0.28 * (b - 256) / 256; });
@@ -172,23 +174,19 @@ I8Cut i8_cut_of(int64_t M, int64_t n, int K) {
     const int rest = (int)(tiles % kUnits);
     if (rest) {
       double last = us(rest) * stages + fixed;
-      auto offer = [&](int group, int blocks) {
-        const int groups = (rest + group - 1) / group, per = (group * stages + blocks - 1) / blocks;
-        if (groups * blocks > kUnits || per < 4 || per >= stages) return;
-        const double u = us(groups * blocks) * per + fixed + 4.5 + piece * (groups * blocks);
-        if (u >= last) return;
+      for (int k = 2; k <= 8; ++k) {
+        const int per = (stages + k - 1) / k, blocks = (stages + per - 1) / per;
+        if (blocks < k || per < 4 || rest * k > kUnits) continue;
+        const double u = us(rest * k) * per + fixed + 4.5 + piece * (rest * k);
+        if (u >= last) continue;
         last = u;
         d.rest = rest;
         d.whole = (int)tiles - rest;
-        d.group = group;
-        d.blocks = blocks;
+        d.blocks = k;
         d.per = per;
-        d.parts = groups * blocks;
-        d.part_bytes = (size_t)(d.parts + rest) * mh * 128 * 256 * 4;
-      };
-      for (int k = 2; k <= 8; ++k) offer(1, k);
-      offer(2, 3);
-      offer(3, 4);
+        d.parts = rest * k;
+        d.part_bytes = (size_t)d.parts * mh * 128 * 256 * 4;
+      }
       t += last;
     }
     if (t < cost) {

@@ -31,8 +31,12 @@ size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward);
 
 // The same for one product in 8-bit integers, whose stages are 128 k (the same bytes as 64 k of 16 bits).
 inline int i8_stages(int K) { return (K + 127) / 128; }
-struct I8Cut : Cut {  // tile: 0: the weights stream (no tiles); 64: 64 x 128; else as in Cut
-  bool deep;          // 128 x 128 with three stages in LDS, one tile to a unit
+struct I8Cut {
+  int tile;   // 0: the weights stream (no tiles); 64: 64 x 128; 128: 128 x 128; 384: 128 x 256; 256: 256 x 256
+  bool deep;  // 128 x 128 with three stages in LDS, one tile to a unit
+  // `whole` blocks compute a tile each, `parts` further ones `per` stages of the other `rest` tiles, `blocks` to a tile
+  int tiles_m, tiles_n, whole, rest, blocks, per, parts;
+  size_t part_bytes;
 };
 I8Cut i8_cut_of(int64_t M, int64_t n, int K);
 size_t i8_part_bytes(int64_t T, int64_t n, int K);

@@ -50,8 +50,8 @@ struct I8Args {
   const void* res;
   int64_t ldr;
   uint16_t* h;  // kGateUp: [M, N]
-  // how tiles are shared: see Cut
-  int tiles_m, tiles_n, whole, rest, group, blocks, per, parts;
+  // how tiles are shared: see I8Cut
+  int tiles_m, tiles_n, whole, rest, blocks, per, parts;
   int* part;  // sums of pieces
 };
 
@@ -362,6 +362,17 @@ __device__ __forceinline__ TilePos tile_pos(const I8Args& p, int t) {
   return {first + in % rows, in / rows};
 }
 
+// A block's work: a whole tile, or (slot >= 0) one of the `blocks` pieces of a tile behind those.  Consecutive ones share
+// an XCD.
+struct Piece {
+  int tile, s_begin, s_end, slot;
+};
+__device__ __forceinline__ Piece piece_of(const I8Args& p, int stages) {
+  if ((int)blockIdx.x < p.whole) return {xcd_logical_block(blockIdx.x, p.whole), 0, stages, -1};
+  const int b = xcd_logical_block(blockIdx.x - p.whole, p.parts), t = b / p.blocks, s = (b - t * p.blocks) * p.per;
+  return {p.whole + t, s, min(stages, s + p.per), b};
+}
+
 // Two 32x32 sums of a wave among a piece's: 2048 whole numbers, quads of 4 channels by lane.
 __device__ __forceinline__ void store_part(int* at, const i32x16_t (&c)[2], int lane) {
   i32x4_t* d = reinterpret_cast<i32x4_t*>(at) + lane;
@@ -409,12 +420,9 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, hi = lane >> 5, l31 = lane & 31;
   const int stages = (p.K + 127) >> 7;
-  // consecutive blocks share an XCD; `blocks` of them share each tile's stages (rest > 0)
-  const int lb = xcd_logical_block(blockIdx.x, gridDim.x);
-  const int tile = p.rest ? lb / p.blocks : lb;
-  const int s_begin = p.rest ? (lb - tile * p.blocks) * p.per : 0;
-  const int s_end = p.rest ? min(stages, s_begin + p.per) : stages;
-  const TilePos tp = tile_pos(p, tile);
+  const Piece w = piece_of(p, stages);
+  const int s_begin = w.s_begin, s_end = w.s_end;
+  const TilePos tp = tile_pos(p, w.tile);
   const int m0 = tp.m * BM, n0 = tp.n * (GU ? 64 : 128);
 
   uint32_t offA[LA], offB[LB];
@@ -482,8 +490,8 @@ __global__ __launch_bounds__(256, 1) void i8_tile128_kernel(I8Args p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the masked loads too: LDS is another block's afterwards
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    if (p.rest) {
-      store_part(p.part + (size_t)lb * (BM * 128) + (wave * MT + i) * 2048, acc[i], lane);
+    if (w.slot >= 0) {
+      store_part(p.part + (size_t)w.slot * (BM * 128) + (wave * MT + i) * 2048, acc[i], lane);
     } else {
       const int b = wn * (GU ? 32 : 64);
       i8_epilogue<MODE, H, BM, 128>(p, acc[i][0], acc[i][1], scales, m0, wm * (BM / 2) + i * 32 + l31, n0, b, b + 32, hi);
@@ -498,7 +506,7 @@ __global__ __launch_bounds__(256) void i8_join128_kernel(I8Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, t = blockIdx.x / (2 * MT), i = (blockIdx.x >> 1) % MT;
   __shared__ __attribute__((aligned(16))) float scales[BM + 128];
-  const TilePos tp = tile_pos(p, t);
+  const TilePos tp = tile_pos(p, p.whole + t);
   const int m0 = tp.m * BM, n0 = tp.n * (MODE == kGateUp ? 64 : 128), r = wm * (BM / 2) + i * 32;
   stage_scales<MODE, BM, 128, 256>(p, scales, m0, n0);
   __syncthreads();
@@ -542,174 +550,149 @@ __global__ __launch_bounds__(512, 2) void i8_tile256_kernel(I8Args p) {
   const int wm = wave >> 2, wn = wave & 3, hi = lane >> 5, l31 = lane & 31;
   const int stages = (p.K + 127) >> 7;
 
-  // This block's piece of work: a whole tile, or stages [at, end) of the rest's, which touch at
-  // most two tiles (per < stages).
-  int tile, at = 0, end = 1, b = 0;
-  const bool piece = (int)blockIdx.x >= p.whole;
-  if (!piece) {
-    tile = xcd_logical_block(blockIdx.x, p.whole);
-  } else {
-    b = xcd_logical_block(blockIdx.x - p.whole, p.parts);
-    const int g = b / p.blocks, line = p.group * stages;
-    at = g * line + (b - g * p.blocks) * p.per;
-    end = min(min(at + p.per, (g + 1) * line), p.rest * stages);
-    tile = p.whole;
+  const Piece w = piece_of(p, stages);
+  const int s_begin = w.s_begin, s_end = w.s_end;
+  const TilePos tp = tile_pos(p, w.tile);
+  const int m0 = tp.m * BM, n0 = tp.n * (GU ? 128 : 256);
+  // rows of a wave in the two halves: those past the end are neither read nor multiplied
+  const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
+
+  // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
+  uint32_t offA[MH][2], offB[2][2];  // [half][chunk]
+  int kq[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = (wave * 2 + j) * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);
+    kq[j] = pk * 16;
+#pragma unroll
+    for (int h = 0; h < MH; ++h) offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda + pk * 16) : kOOB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int nh = n0 + (GU ? 0 : h * 128);
+      offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.K + pk * 16) : kOOB;
+    }
   }
-  while (at < end) {
-    int s_begin = 0, s_end = stages, slot = -1;
-    if (piece) {
-      const int t = at / stages;
-      tile = p.whole + t;
-      s_begin = at - t * stages;
-      s_end = min(stages, end - t * stages);
-      if (s_end - s_begin < stages) slot = b + t;
-      at = t * stages + s_end;
-    } else {
-      at = end;
+  // Each region's source moves on by a stage per load.
+  const uint32_t sm0 = lds_addr(sm) + wave * 2048;
+  const int k0 = s_begin << 7;
+  const int8_t* pa[2] = {p.a + m0 * p.lda + k0, p.a + (m0 + 128) * p.lda + k0};
+  const int8_t* pb[2] = {p.b + (int64_t)n0 * p.K + k0, (GU ? p.b2 + (int64_t)n0 * p.K : p.b + (int64_t)(n0 + 128) * p.K) + k0};
+  auto load = [&](int s, const int8_t*& src, const uint32_t (&off)[2], uint32_t region, int place) {
+    const int left = s < s_end ? p.K - (s << 7) : 0;
+    const auto rs = rsrc_of(src);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) lds_load16(rs, kq[j] < left ? off[j] : kOOB, 0, sm0 + place * STAGE + region + j * 1024);
+    src += 128;
+  };
+  auto load_a = [&](int s, int h, int place) { load(s, pa[h], offA[h], h ? A1 : A0, place); };
+  auto load_b = [&](int s, int h, int place) { load(s, pb[h], offB[h], h ? B1 : B0, place); };
+
+  // ---- fragments of a region: 32 rows from `row`, slice of 32 k ----
+  auto frag = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
+  };
+  i32x16_t acc[2 * MH][2];  // [2 half + 32-row piece][half of the channels]
+#pragma unroll
+  for (int i = 0; i < 2 * MH; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
+  i32x4_t fa[2][4], fb0[4], fb1[4];
+  auto read_a = [&](const uint8_t* base) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i][k] = frag(base, wm * 64 + i * 32, k);
+  };
+  auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = frag(base, wn * 32, k);
+  };
+  auto multiply = [&](int half) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[2 * half + i][0] = mfma32(fb0[k], fa[i][k], acc[2 * half + i][0]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[2 * half + i][1] = mfma32(fb1[k], fa[i][k], acc[2 * half + i][1]);
     }
-    const TilePos tp = tile_pos(p, tile);
-    const int m0 = tp.m * BM, n0 = tp.n * (GU ? 128 : 256);
-    // rows of a wave in the two halves: those past the end are neither read nor multiplied
-    const bool any[2] = {m0 + wm * 64 < p.M, m0 + 128 + wm * 64 < p.M};
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // The end of a section: nothing moves across.
+  auto meet = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
 
-    // ---- loads: a wave brings chunks 2 wave and 2 wave + 1 (1 KB) of every region ----
-    uint32_t offA[MH][2], offB[2][2];  // [half][chunk]
-    int kq[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = (wave * 2 + j) * 8 + (lane >> 3), pk = (lane & 7) ^ ((r >> 1) & 7);
-      kq[j] = pk * 16;
-#pragma unroll
-      for (int h = 0; h < MH; ++h) offA[h][j] = m0 + h * 128 + r < p.M ? (uint32_t)(r * p.lda + pk * 16) : kOOB;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int nh = n0 + (GU ? 0 : h * 128);
-        offB[h][j] = nh + r < p.N ? (uint32_t)(r * p.K + pk * 16) : kOOB;
-      }
-    }
-    // Each region's source moves on by a stage per load.
-    const uint32_t sm0 = lds_addr(sm) + wave * 2048;
-    const int k0 = s_begin << 7;
-    const int8_t* pa[2] = {p.a + m0 * p.lda + k0, p.a + (m0 + 128) * p.lda + k0};
-    const int8_t* pb[2] = {p.b + (int64_t)n0 * p.K + k0, (GU ? p.b2 + (int64_t)n0 * p.K : p.b + (int64_t)(n0 + 128) * p.K) + k0};
-    auto load = [&](int s, const int8_t*& src, const uint32_t (&off)[2], uint32_t region, int place) {
-      const int left = s < s_end ? p.K - (s << 7) : 0;
-      const auto rs = rsrc_of(src);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) lds_load16(rs, kq[j] < left ? off[j] : kOOB, 0, sm0 + place * STAGE + region + j * 1024);
-      src += 128;
-    };
-    auto load_a = [&](int s, int h, int place) { load(s, pa[h], offA[h], h ? A1 : A0, place); };
-    auto load_b = [&](int s, int h, int place) { load(s, pb[h], offB[h], h ? B1 : B0, place); };
-
-    // ---- fragments of a region: 32 rows from `row`, slice of 32 k ----
-    auto frag = [&](const uint8_t* base, int row, int slice) -> i32x4_t {
-      return *reinterpret_cast<const i32x4_t*>(base + (row + l31) * 128 + (((2 * slice + hi) ^ ((l31 >> 1) & 7)) << 4));
-    };
-    i32x16_t acc[2 * MH][2];  // [2 half + 32-row piece][half of the channels]
-#pragma unroll
-    for (int i = 0; i < 2 * MH; ++i) acc[i][0] = acc[i][1] = i32x16_t{};
-    i32x4_t fa[2][4], fb0[4], fb1[4];
-    auto read_a = [&](const uint8_t* base) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) fa[i][k] = frag(base, wm * 64 + i * 32, k);
-    };
-    auto read_b = [&](const uint8_t* base, i32x4_t (&f)[4]) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f[k] = frag(base, wn * 32, k);
-    };
-    auto multiply = [&](int half) {
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[2 * half + i][0] = mfma32(fb0[k], fa[i][k], acc[2 * half + i][0]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[2 * half + i][1] = mfma32(fb1[k], fa[i][k], acc[2 * half + i][1]);
-      }
-      __builtin_amdgcn_s_setprio(0);
-    };
-    // The end of a section: nothing moves across.
-    auto meet = [&]() {
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-
-    if (s_begin < s_end) {
-      load_scales<MODE, BM, 256>(p, lds_addr(scales), m0, n0, wave, lane);  // the oldest: waited for with the first stage
-      load_a(s_begin, 0, 0);
-      load_b(s_begin, 0, 0);
-      load_b(s_begin, 1, 0);
-      if constexpr (MH == 2) load_a(s_begin, 1, 0);
-      load_a(s_begin + 1, 0, 1);
-      load_b(s_begin + 1, 0, 1);
-      load_b(s_begin + 1, 1, 1);
-      constexpr int WAIT = MH == 2 ? 8 : 6;
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(WAIT) : "memory");  // A0, B0 and B1 of the first stage
-      meet();
-      if (wm) meet();
-      // RAGGED: the tile has rows past the end.
-      auto walk = [&](auto ragged) {
-        constexpr bool RAGGED = decltype(ragged)::value;
-        int here = 0;
-        for (int s = s_begin; s < s_end; ++s) {
-          const uint8_t* st = sm + here * STAGE;
-          const int other = here == 0 ? PLACES - 1 : here - 1;
-          if (!RAGGED || any[0]) read_a(st + A0);
-          read_b(st + B0, fb0);
-          read_b(st + B1, fb1);
-          if constexpr (MH == 2) {
-            load_a(s + 1, 1, other);
-            reads_done();
-            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
-          } else {
-            load_a(s + 2, 0, other);
-            load_b(s + 2, 0, other);
-            load_b(s + 2, 1, other);
-            reads_done();
-            asm volatile("s_waitcnt vmcnt(6)" ::: "memory");  // the next stage
-          }
-          meet();
-          if (!RAGGED || any[0]) multiply(0);
-          meet();
-          if constexpr (MH == 2) {
-            if (!RAGGED || any[1]) read_a(st + A1);
-            load_a(s + 2, 0, here);
-            load_b(s + 2, 0, here);
-            load_b(s + 2, 1, here);
-            reads_done();
-            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
-            meet();
-            if (!RAGGED || any[1]) multiply(1);
-            meet();
-          }
-          here = here == PLACES - 1 ? 0 : here + 1;
+  if (s_begin < s_end) {
+    load_scales<MODE, BM, 256>(p, lds_addr(scales), m0, n0, wave, lane);  // the oldest: waited for with the first stage
+    load_a(s_begin, 0, 0);
+    load_b(s_begin, 0, 0);
+    load_b(s_begin, 1, 0);
+    if constexpr (MH == 2) load_a(s_begin, 1, 0);
+    load_a(s_begin + 1, 0, 1);
+    load_b(s_begin + 1, 0, 1);
+    load_b(s_begin + 1, 1, 1);
+    constexpr int WAIT = MH == 2 ? 8 : 6;
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(WAIT) : "memory");  // A0, B0 and B1 of the first stage
+    meet();
+    if (wm) meet();
+    // RAGGED: the tile has rows past the end.
+    auto walk = [&](auto ragged) {
+      constexpr bool RAGGED = decltype(ragged)::value;
+      int here = 0;
+      for (int s = s_begin; s < s_end; ++s) {
+        const uint8_t* st = sm + here * STAGE;
+        const int other = here == 0 ? PLACES - 1 : here - 1;
+        if (!RAGGED || any[0]) read_a(st + A0);
+        read_b(st + B0, fb0);
+        read_b(st + B1, fb1);
+        if constexpr (MH == 2) {
+          load_a(s + 1, 1, other);
+          reads_done();
+          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A1 of this stage
+        } else {
+          load_a(s + 2, 0, other);
+          load_b(s + 2, 0, other);
+          load_b(s + 2, 1, other);
+          reads_done();
+          asm volatile("s_waitcnt vmcnt(6)" ::: "memory");  // the next stage
         }
-      };
-      if (m0 + BM - 64 < p.M)
-        walk(std::false_type{});
-      else
-        walk(std::true_type{});
-      if (!wm) meet();
-      // the masked loads' writes too: a wave's next loads go where its own last ones went
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * MH; ++i) {
-      const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
-      if (slot >= 0) {
-        if (m < p.M) store_part(p.part + (size_t)slot * PART + (wave * 2 * MH + i) * 2048, acc[i], lane);
-      } else {
-        i8_epilogue<MODE, H, BM, 256>(p, acc[i][0], acc[i][1], scales, m0, m - m0 + l31, n0, wn * 32, wn * 32 + 128, hi);
+        meet();
+        if (!RAGGED || any[0]) multiply(0);
+        meet();
+        if constexpr (MH == 2) {
+          if (!RAGGED || any[1]) read_a(st + A1);
+          load_a(s + 2, 0, here);
+          load_b(s + 2, 0, here);
+          load_b(s + 2, 1, here);
+          reads_done();
+          asm volatile("s_waitcnt vmcnt(8)" ::: "memory");  // A0, B0 and B1 of the next stage
+          meet();
+          if (!RAGGED || any[1]) multiply(1);
+          meet();
+        }
+        here = here == PLACES - 1 ? 0 : here + 1;
       }
+    };
+    if (m0 + BM - 64 < p.M)
+      walk(std::false_type{});
+    else
+      walk(std::true_type{});
+    if (!wm) meet();
+    // the masked loads' writes too: a wave's next loads go where its own last ones went
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * MH; ++i) {
+    const int m = m0 + (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
+    if (w.slot >= 0) {
+      if (m < p.M) store_part(p.part + (size_t)w.slot * PART + (wave * 2 * MH + i) * 2048, acc[i], lane);
+    } else {
+      i8_epilogue<MODE, H, BM, 256>(p, acc[i][0], acc[i][1], scales, m0, m - m0 + l31, n0, wn * 32, wn * 32 + 128, hi);
     }
-    if (at < end) __syncthreads();  // the scales are no longer read
   }
 }
 
@@ -719,10 +702,6 @@ template <int MODE, bool H, int MH>
 __global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3, i = (blockIdx.x >> 1) % (2 * MH), t = blockIdx.x / (4 * MH);
-  const int stages = (p.K + 127) >> 7;
-  const int g = t / p.group, from = (t - g * p.group) * stages;
-  const int first = g * p.blocks + from / p.per, last = g * p.blocks + (from + stages - 1) / p.per;
-  if (first == last) return;  // one block had it all
   const TilePos tp = tile_pos(p, p.whole + t);
   __shared__ __attribute__((aligned(16))) float scales[MH * 128 + 256];
   const int m0 = tp.m * 128 * MH, n0 = tp.n * (MODE == kGateUp ? 128 : 256), r = (i >> 1) * 128 + wm * 64 + (i & 1) * 32;
@@ -730,11 +709,11 @@ __global__ __launch_bounds__(512) void i8_join256_kernel(I8Args p) {
   __syncthreads();
   if (m0 + r >= p.M) return;
   constexpr int PART = MH * 128 * 256;
-  const int* at = p.part + (size_t)(first + t) * PART + (wave * 2 * MH + i) * 2048;
+  const int* at = p.part + (size_t)t * p.blocks * PART + (wave * 2 * MH + i) * 2048;
   auto half = [&](auto h) {
     constexpr int QH = decltype(h)::value;
     i32x16_t acc[2];
-    sum_parts<QH>(acc, at, PART, last - first + 1, lane);
+    sum_parts<QH>(acc, at, PART, p.blocks, lane);
     i8_epilogue<MODE, H, MH * 128, 256, QH>(p, acc[0], acc[1], scales, m0, r + (lane & 31), n0, wn * 32, wn * 32 + 128, lane >> 5);
   };
   if (blockIdx.x & 1)
@@ -780,7 +759,6 @@ int i8_go(I8Args& A, hipStream_t s) {
   A.tiles_n = c.tiles_n;
   A.whole = c.whole;
   A.rest = c.rest;
-  A.group = c.group;
   A.blocks = c.blocks;
   A.per = c.per;
   A.parts = c.parts;
@@ -792,7 +770,7 @@ int i8_go(I8Args& A, hipStream_t s) {
     if (c.rest) hipLaunchKernelGGL((i8_join256_kernel<MODE, H, 1>), dim3((unsigned)c.rest * 4), dim3(512), 0, s, A);
   } else {
     auto go = [&](auto tile, size_t stage, int deep, auto join, unsigned pieces) {
-      hipLaunchKernelGGL(tile, dim3((unsigned)c.parts), dim3(256), deep * stage, s, A);
+      hipLaunchKernelGGL(tile, dim3((unsigned)(c.whole + c.parts)), dim3(256), deep * stage, s, A);
       if (c.rest) hipLaunchKernelGGL(join, dim3((unsigned)c.rest * pieces), dim3(256), 0, s, A);
     };
     if (c.tile == 64)
