@@ -545,7 +545,7 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
  * Router, top-k, gates, the routed experts and their weighted sum in one call:
  *   y[t] = sum over j of gates[t, j] * W_down (silu(W_gate x_t) * (W_up x_t)) (+ residual[t])
  * over the experts idx[t, j], in the order of j.  shape: E, d, d_ff, k and the records' format (L is not
- * used); d <= 16384, d_ff <= 65536, a record below 2 GiB.  x: device bf16 [T, d], 0 <= T <= 64,
+ * used, but positive); d <= 16384, d_ff <= 65536, a record below 2 GiB.  x: device bf16 [T, d], 0 <= T <= 64,
  * T * k <= FT_PLAN_CAP.  w_router, allowed, idx, gates: as for ft_router_topk, and with its bits (a row
  * that allows fewer than k experts gets idx -1 and gate 0 in the places left).
  * records: n_slots records one after another, 16-byte aligned.  slot_of: device int32 [E], the

@@ -294,12 +294,26 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
       if (mok && n < p.N) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
+    // The residual's pieces leave together, from addresses inside it (those past its ends are not used): one behind the
+    // other each waited for its own round trip (the block of 8192 tokens with a residual, d = 4096, d_ff = 2048: 241 us, so 235).
+    // (Rows through LDS in pieces of 512 bytes instead of 32 took 267: the whole block waits at each pass.)
+    constexpr int Q0 = QH > 0 ? 2 : 0, Q1 = QH == 0 ? 2 : 4;
+    uint4 old[2][2];
+    const bool wide16 = p.wide && !p.c_f32 && p.res;
+    if (wide16) {
+      const uint16_t* r = static_cast<const uint16_t*>(p.res) + (int64_t)min(m, p.M - 1) * p.ldr;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = Q0; q < Q1; q += 2)
+          old[j][q >> 1] = *reinterpret_cast<const uint4*>(r + min(n0 + (j ? b1 : b0) + 8 * q + 8 * hi, p.N - 8));
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int b = j ? b1 : b0;
       const i32x16_t& c = j ? c1 : c0;
 #pragma unroll
-      for (int q = QH > 0 ? 2 : 0; q < (QH == 0 ? 2 : 4); q += 2) {
+      for (int q = Q0; q < Q1; q += 2) {
         float v[8];  // after the exchange: channels b + 8 (q + hi) .. + 7
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -318,25 +332,26 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
           v[4 + e] = __uint_as_float(y);
         }
         const int n = n0 + b + 8 * q + 8 * hi;
-        if (!mok || n >= p.N) continue;
+        const bool ok = mok && n < p.N;
         if (!p.wide) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (n + e < p.N) store1<H>(p, m, n + e, v[e]);
+            if (mok && n + e < p.N) store1<H>(p, m, n + e, v[e]);
         } else if (p.c_f32) {  // wide: N % 8 == 0
-          float* o = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n;
-          if (p.res) {
-            const float* r = static_cast<const float*>(p.res) + (int64_t)m * p.ldr + n;
-            const float4 a = *reinterpret_cast<const float4*>(r), b = *reinterpret_cast<const float4*>(r + 4);
-            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+          if (ok) {
+            float* o = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n;
+            if (p.res) {
+              const float* r = static_cast<const float*>(p.res) + (int64_t)m * p.ldr + n;
+              const float4 a = *reinterpret_cast<const float4*>(r), b = *reinterpret_cast<const float4*>(r + 4);
+              v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+              v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+            }
+            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
           }
-          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-          uint16_t* o = static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc + n;
-          if (p.res) {
-            const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (int64_t)m * p.ldr + n);
+          if (wide16) {
+            const uint4 r = old[j][q >> 1];
             const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -344,8 +359,9 @@ __device__ __forceinline__ void i8_epilogue(const I8Args& p, const i32x16_t& c0,
               v[2 * e + 1] += hi16<H>(rw[e]);
             }
           }
-          *reinterpret_cast<uint4*>(o) =
-              make_uint4(pack2<H>(v[0], v[1]), pack2<H>(v[2], v[3]), pack2<H>(v[4], v[5]), pack2<H>(v[6], v[7]));
+          if (ok)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc + n) =
+                make_uint4(pack2<H>(v[0], v[1]), pack2<H>(v[2], v[3]), pack2<H>(v[4], v[5]), pack2<H>(v[6], v[7]));
         }
       }
     }

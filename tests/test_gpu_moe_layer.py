@@ -100,6 +100,16 @@ CASES = [
     (64, 2056, 104, 1000, 8, "bf16", "fp32", False),
     (64, 1024, 160, 64, 8, "i8", "bf16", True),
     (63, 2048, 768, 12, 7, "bf16", "fp32", True),
+    (36, 2048, 128, 200, 2, "mxfp4", "fp32", False),  # rows of x that LDS does not hold
+    (64, 2304, 32, 300, 2, "i8", "fp32", True),
+    (9, 512, 4224, 60, 4, "mxfp4", "fp32", False),    # rows of h that LDS does not hold, past one chunk
+    (20, 512, 4112, 100, 2, "i8", "bf16", False),
+    (2, 8208, 48, 5, 2, "i8", "fp32", False),
+    (17, 512, 128, 1, 1, "mxfp4", "fp32", True),      # one expert: 16 tokens and one more
+    (32, 264, 72, 2, 2, "bf16", "fp32", False),       # two whole passes of 16
+    (48, 1552, 400, 4, 2, "i8", "fp32", True),
+    (64, 8200, 24, 3, 3, "bf16", "bf16", False),      # the matrix form on more rows of y than 16 a unit
+    (64, 4096, 384, 6, 5, "mxfp4", "fp32", True),
 ]
 
 
