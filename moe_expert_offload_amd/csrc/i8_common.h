@@ -93,9 +93,9 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 
 // One row of n elements to codes and its scale by ROWT threads, 64 or a whole block (`red`: a word of LDS for each wave). The row is
 // held in registers between its largest element and its codes, NP pieces of 8 elements a thread; what is
-// longer is read again.  codes may lie in LDS.
-template <bool H, int ROWT, int NP>
-__device__ __forceinline__ void quant_row(const uint16_t* src, int n, int8_t* codes, float* scale, uint32_t* red) {
+// longer is read again.  place(i): where the codes of 8 elements from 8 i go (a uint2).
+template <bool H, int ROWT, int NP, class Place>
+__device__ __forceinline__ void quant_row(const uint16_t* src, int n, Place place, float* scale, uint32_t* red) {
   const int at = threadIdx.x % ROWT, pieces = n >> 3;
   const uint4* q = reinterpret_cast<const uint4*>(src);
   uint4 v[NP];
@@ -113,16 +113,21 @@ __device__ __forceinline__ void quant_row(const uint16_t* src, int n, int8_t* co
     for (int w = 0; w < ROWT / 64; ++w) m = max(m, red[w]);
   }
   const RowScale r = row_scale<H>(m);
-  uint2* d = reinterpret_cast<uint2*>(codes);
   auto put = [&](int p, const uint4& x) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    d[p] = row_codes8<H>(w, r);
+    *place(p) = row_codes8<H>(w, r);
   };
 #pragma unroll
   for (int i = 0; i < NP; ++i)
     if (at + i * ROWT < pieces) put(at + i * ROWT, v[i]);
   for (int p = at + NP * ROWT; p < pieces; p += ROWT) put(p, q[p]);
   if (at == 0) *scale = r.scale;
+}
+// One after another; codes may lie in LDS.
+template <bool H, int ROWT, int NP>
+__device__ __forceinline__ void quant_row(const uint16_t* src, int n, int8_t* codes, float* scale, uint32_t* red) {
+  uint2* d = reinterpret_cast<uint2*>(codes);
+  quant_row<H, ROWT, NP>(src, n, [=](int i) { return d + i; }, scale, red);
 }
 
 // A product's value: the whole-number sum times the channel's scale, then the token's.

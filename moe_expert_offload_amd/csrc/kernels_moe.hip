@@ -59,7 +59,7 @@ struct MoeArgs {
   const void* res;
   void* y;
   int y_f32;
-  int rows;     // down: rows of a block
+  int rows;     // down: rows of a block; gate/up's matrix form: tokens of a part
   int lds_vec;  // the tokens' rows (gate/up: x, down: h) are staged in LDS
 };
 
@@ -663,14 +663,16 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
 // The same products for groups of several tokens, cut into parts of up to 16: a tile is 16 rows of an expert (gate/up: 8
 // of each) and the tokens of a part, weights as the MFMA's second operand, so that each is loaded and converted
 // once a part.  Lane l: row (and token) l % 16, in a step the k of its quarter l / 16.  KW wavefronts share a tile's
-// chunks and add their sums in LDS; the block's others take further tiles, and the next chunk, of this tile or the
-// next one, is on its way while one is multiplied.
+// chunks and add their sums in LDS; the block's others take further tiles, and the next chunk's weights, of this tile
+// or the next one, are on their way while one is multiplied.
 //   bf16   v_mfma_f32_16x16x32_bf16
 //   MXFP4  the same on codes turned into bf16 exactly; a step is one block of 32, whose scale multiplies its
 //          fp32 sum; exchanges across the wave bring a lane's block to the quarters
 //   8-bit  v_mfma_i32_16x16x64_i8
 // h stays fp32 for bf16 and MXFP4: it is three bf16 numbers whose sum it is (8 + 8 + 8 bits), each with its own MFMA; the
 // matrix cores have room for that.
+// Loads of 64 bytes from each of 16 rows, as the weights', cost the load unit four times what 1 KB in a line does, so the
+// tokens' operands do not come that way: gate/up holds a part's x in LDS, and h lies in memory as down multiplies it (frag_place).
 template <int FMT>
 struct Many {
   static constexpr int KS = FMT == FT_W_I8 ? 64 : 32;   // k of a step
@@ -679,46 +681,38 @@ struct Many {
   typedef typename std::conditional<FMT == FT_W_I8, int, float>::type One;
   typedef typename std::conditional<FMT == FT_W_I8, i32x4_t, f32x4_t>::type Acc;
 };
-// A lane's share of a chunk of ST steps: weights, and the tokens' operands (PARTS of each).
-template <int FMT, int PARTS, int ST>
-struct ManyChunk {
+// A lane's weights of a chunk of ST steps.
+template <int FMT, int ST>
+struct ManyWeights {
   static constexpr int WL = FMT == FT_W_MXFP4 ? ST / 4 : ST;  // loads: one of MXFP4 codes is four steps
   uint4 w[WL];
   uint32_t sc[FMT == FT_W_MXFP4 ? WL : 1];
-  i32x4_t x[ST][PARTS];
-  // Weights: a row of n elements at byte `base` (scales at sbase).  Tokens: a row at `row`, its further parts `plane` bytes
-  // apart.  Past the row's end zeros, of both: x may be an infinity there.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rec, uint32_t base, uint32_t sbase, const uint8_t* row, size_t plane,
-                                       int n, int chunk, int g, bool in) {
+  // A row of n elements at byte `base` (scales at sbase); zeros past its end.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rec, uint32_t base, uint32_t sbase, int n, int chunk, int g, bool in) {
     constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS;
-    if constexpr (FMT == FT_W_MXFP4) {
 #pragma unroll
-      for (int l = 0; l < WL; ++l) {
+    for (int l = 0; l < WL; ++l) {
+      if constexpr (FMT == FT_W_MXFP4) {
         const int k = (chunk * WL + l) * 128;  // n is a multiple of 128
         w[l] = buf_ld16(rec, in && k < n ? base + (uint32_t)((k + g * 32) >> 1) : kOOB);
         sc[l] = __builtin_amdgcn_raw_buffer_load_b32(rec, (int)(in && k < n ? sbase + (uint32_t)(k >> 5) : kOOB), 0, 0);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < ST; ++j) {
-      const int k = (chunk * ST + j) * KS + g * (16 / EB);
-      if constexpr (FMT != FT_W_MXFP4) w[j] = buf_ld16(rec, in && k < n ? base + (uint32_t)(k * EB) : kOOB);
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        x[j][q] = *reinterpret_cast<const i32x4_t*>(row + q * plane + (k < n ? k * EB : 0));
-        if (k >= n) x[j][q] = i32x4_t{};
+      } else {
+        const int k = (chunk * ST + l) * KS + g * (16 / EB);
+        w[l] = buf_ld16(rec, in && k < n ? base + (uint32_t)(k * EB) : kOOB);
       }
     }
   }
-  __device__ __forceinline__ void multiply(typename Many<FMT>::Acc& acc) const {
+  // x(j, q): part q of the tokens' operand of step j.
+  template <int PARTS, class X>
+  __device__ __forceinline__ void multiply(typename Many<FMT>::Acc& acc, X x) const {
     if constexpr (FMT == FT_W_I8) {
 #pragma unroll
-      for (int j = 0; j < ST; ++j) acc = mfma16(x[j][0], __builtin_bit_cast(i32x4_t, w[j]), acc);
+      for (int j = 0; j < ST; ++j) acc = mfma16(x(j, 0), __builtin_bit_cast(i32x4_t, w[j]), acc);
     } else if constexpr (FMT == FT_W_BF16) {
 #pragma unroll
       for (int j = 0; j < ST; ++j)
 #pragma unroll
-        for (int q = PARTS - 1; q >= 0; --q) acc = mfma16<false>(x[j][q], __builtin_bit_cast(i32x4_t, w[j]), acc);
+        for (int q = PARTS - 1; q >= 0; --q) acc = mfma16<false>(x(j, q), __builtin_bit_cast(i32x4_t, w[j]), acc);
     } else {
 #pragma unroll
       for (int l = 0; l < WL; ++l) {
@@ -744,7 +738,7 @@ struct ManyChunk {
                               __builtin_bit_cast(int, mx_pair<2>(v[j])), __builtin_bit_cast(int, mx_pair<3>(v[j]))};
           f32x4_t s = {};
 #pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q) s = mfma16<false>(x[4 * l + j][q], wj, s);
+          for (int q = PARTS - 1; q >= 0; --q) s = mfma16<false>(x(4 * l + j, q), wj, s);
           const float scale = e8m0((sc[l] >> (8 * j)) & 255u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = fmaf(scale, s[i], acc[i]);
@@ -754,66 +748,40 @@ struct ManyChunk {
   }
 };
 
-// The groups in parts of up to 16 pairs.
+// The groups in parts.
 struct Parts {
   int32_t n;
-  int32_t slot[FT_PLAN_CAP], first[FT_PLAN_CAP], pairs[FT_PLAN_CAP];
+  int32_t slot[FT_PLAN_CAP];
+  uint16_t pair[FT_PLAN_CAP];                  // by group
+  uint16_t first[FT_PLAN_CAP], off[FT_PLAN_CAP];  // a part's first place among them, its group's
+  uint8_t pairs[FT_PLAN_CAP], of[FT_PLAN_CAP];    // its pairs, its group's (64 tokens at most)
   int32_t wave_sum[NW];
 };
-// All threads of the block, a barrier behind the groups' last change; barriers within and behind.
-__device__ void cut_groups(Parts& Q, const Grouped& P) {
+// Parts of up to `most` pairs.  All threads of the block, a barrier behind the groups' last change; barriers within and
+// behind.
+__device__ void cut_groups(Parts& Q, const Grouped& P, int most) {
   const int i = threadIdx.x, n = i < P.groups ? P.off[i + 1] - P.off[i] : 0;
   int total;
-  const int at = block_prefix((n + 15) >> 4, Q.wave_sum, total);
-  for (int t = 0; t * 16 < n; ++t) {
+  const int at = block_prefix((n + most - 1) / most, Q.wave_sum, total);
+  for (int t = 0; t * most < n; ++t) {
     Q.slot[at + t] = P.slot[i];
-    Q.first[at + t] = P.off[i] + t * 16;
-    Q.pairs[at + t] = min(16, n - t * 16);
+    Q.first[at + t] = (uint16_t)(P.off[i] + t * most);
+    Q.pairs[at + t] = (uint8_t)min(most, n - t * most);
+    Q.off[at + t] = (uint16_t)P.off[i];
+    Q.of[at + t] = (uint8_t)n;
   }
+  if (i < P.off[P.groups]) Q.pair[i] = (uint16_t)P.pair[i];
   if (i == 0) Q.n = total;
   __syncthreads();
 }
 
-// Where a tile's operands are, for one lane.
-struct ManyTile {
-  const uint8_t* rp;
-  uint32_t base, sbase;
-  const uint8_t* row;
-  bool in;
-};
-// All tiles of a block, `tile(i)` giving the i-th of `tiles`, its sums left to `done(i, sums)` with sums[(token * 16 + row)]
-// of the KW wavefronts 256 apart.  KW chunks or more.
-template <int FMT, int PARTS, int ST, class Tile, class Done>
-__device__ __forceinline__ void many_tiles(const MoeArgs& p, int tiles, int first, int stride, int kw_log, int n, size_t plane,
-                                           typename Many<FMT>::One (&red)[2][NW * 256], Tile tile, Done done) {
-  constexpr int CK = ST * Many<FMT>::KS;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
-  const int KW = 1 << kw_log, kw = wave & (KW - 1), per = NW >> kw_log, chunks = (n + CK - 1) / CK;
-  const int mine = wave >> kw_log;  // of a batch of `per` tiles
-  ManyChunk<FMT, PARTS, ST> next;
-  ManyTile t = tile(first * per + mine);
-  auto load = [&](int c) { next.load(buf_rsrc(t.rp, (uint32_t)p.S), t.base, t.sbase, t.row, plane, n, c, g, t.in); };
-  if (first * per < tiles) load(kw);
-  int buf = 0;
-  for (int b = first; b * per < tiles; b += stride) {
-    typename Many<FMT>::Acc acc = {};
-    for (int c = kw; c < chunks; c += KW) {
-      const ManyChunk<FMT, PARTS, ST> cur = next;
-      if (c + KW < chunks) {
-        load(c + KW);
-      } else if ((b + stride) * per < tiles) {
-        t = tile((b + stride) * per + mine);
-        load(kw);
-      }
-      cur.multiply(acc);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[buf][wave * 256 + (4 * g + i) * 16 + (lane & 15)] = acc[i];
-    __syncthreads();  // (the other buffer's sums were read before everyone came here)
-    done(b * per, red[buf], KW, per);
-    buf ^= 1;
-  }
+// Where h of a group's token i lies (of n, the first of them `off` among the pairs by group), for down: the group's 16 tokens
+// of a part side by side, 16 bytes of each in turn.  Byte `at` of its row of `row` bytes:
+__device__ __forceinline__ size_t frag_place(int off, int n, int i, size_t row, uint32_t at) {
+  const int part = i & ~15, w = min(16, n - part);
+  return (size_t)(off + part) * row + ((size_t)(at >> 4) * w + (i & 15)) * 16 + (at & 15);
 }
+
 // The wavefronts that share a tile of n elements a row: two chunks each, where there are as many.
 template <int FMT, int ST>
 __device__ __forceinline__ int kw_log_of(int n) {
@@ -824,118 +792,195 @@ __device__ __forceinline__ int kw_log_of(int n) {
 
 constexpr int kManyPad = 16;  // bytes between rows of x in LDS: 16 tokens' pieces start on different banks
 
+// p.rows: tokens of a part, as many as LDS holds x of.  A block takes consecutive tiles, `per` of one part at a time: it loads
+// x once or twice.
 template <int FMT>
 __global__ __launch_bounds__(NT) void moe_up_many_kernel(MoeArgs p) {
-  constexpr int EB = Many<FMT>::EB, ST = FMT == FT_W_MXFP4 ? 8 : 4;
+  constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS, ST = FMT == FT_W_MXFP4 ? 8 : 4, CK = ST * KS;
   typedef typename Many<FMT>::One One;
-  __shared__ Plan P;
   __shared__ Parts Q;
-  __shared__ One red[2][NW * 256];
-  extern __shared__ uint4 vec[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ One red[NW * 256];
+  extern __shared__ uint4 vec[];  // the plan, then a part's rows of x
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
   const uint8_t* x = static_cast<const uint8_t*>(FMT == FT_W_I8 ? p.xv : (const void*)p.x);
-  if (p.lds_vec) {
-    const int per = p.d * EB / 16;
-    const uint4* src = reinterpret_cast<const uint4*>(x);
-    for (int i = threadIdx.x; i < p.T * per; i += NT) vec[i + i / per * (kManyPad / 16)] = src[i];
+  {
+    Plan& P = *reinterpret_cast<Plan*>(vec);
+    routes(p, P, lane, wave);
+    cut_groups(Q, P, p.rows);
   }
-  routes(p, P, lane, wave);
-  cut_groups(Q, P);
-  const int n16 = lane & 15;
   const Rec R = rec_of<FMT>(p.d, p.f);
-  const int per_part = p.f / 8, tiles = Q.n * per_part, rb = row_bytes<FMT>(p.d);  // f % 8 == 0
-  many_tiles<FMT, 1, ST>(
-      p, tiles, blockIdx.x, gridDim.x, kw_log_of<FMT, ST>(p.d), p.d, 0, red,
-      [&](int i) {
-        ManyTile t;
-        t.in = i < tiles;
-        const int q = t.in ? i / per_part : 0, row = (t.in ? i - q * per_part : 0) * 8 + (n16 & 7);
-        t.rp = p.rec + (t.in ? (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S : 0);
-        const int tok = t.in ? P.pair[Q.first[q] + min(n16, Q.pairs[q] - 1)] / p.k : 0;
-        t.row = p.lds_vec ? reinterpret_cast<const uint8_t*>(vec) + tok * (p.d * EB + kManyPad) : x + (size_t)tok * p.d * EB;
-        t.base = (n16 < 8 ? 0u : R.up) + (uint32_t)row * (uint32_t)rb;
-        t.sbase = (n16 < 8 ? R.gs : R.us) + (uint32_t)row * (uint32_t)(p.d / 32);
-        return t;
-      },
-      [&](int i0, const One* sums, int KW, int per) {
-        for (int e = threadIdx.x; e < per * 128; e += NT) {
-          const int i = i0 + (e >> 7), tk = (e >> 3) & 15, r = e & 7;
-          if (i >= tiles) continue;
-          const int q = i / per_part;
-          if (tk >= Q.pairs[q]) continue;
-          const One* s = sums + (e >> 7) * KW * 256 + tk * 16 + r;
-          One a = 0, u = 0;
-          for (int w = 0; w < KW; ++w) {
-            a += s[w * 256];
-            u += s[w * 256 + 8];
-          }
-          const int pair = P.pair[Q.first[q] + tk], row = (i - q * per_part) * 8 + r;
-          const size_t at = (size_t)pair * p.f + row;
-          if constexpr (FMT == FT_W_I8) {
-            const float* gs = reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.gs) + row;
-            const float ts = p.xs[pair / p.k], v = act_f(i8_value(a, gs[0], ts), FT_ACT_SILU) * i8_value(u, gs[p.f], ts);
-            static_cast<uint16_t*>(p.h)[at] = (uint16_t)pack2<false>(v, 0.0f);
-          } else {
-            const float v = silu(a) * u;
-            uint16_t* h = static_cast<uint16_t*>(p.h);
-            const size_t plane = (size_t)p.T * p.k * p.f;
-            const uint32_t hi = pack2<false>(v, 0.0f) & 0xffffu;
-            float rest = v - bf_lo(hi);
-            if (!(fabsf(rest) < INFINITY)) rest = 0.0f;  // v not finite, or next to it
-            const uint32_t mid = pack2<false>(rest, 0.0f) & 0xffffu;
-            h[at] = (uint16_t)hi;
-            h[at + plane] = (uint16_t)mid;
-            h[at + 2 * plane] = (uint16_t)pack2<false>(rest - bf_lo(mid), 0.0f);
-          }
+  const int per_part = p.f / 8, rb = row_bytes<FMT>(p.d);  // f % 8 == 0
+  const int kw_log = kw_log_of<FMT, ST>(p.d), KW = 1 << kw_log, kw = wave & (KW - 1), per = NW >> kw_log, mine = wave >> kw_log;
+  const int chunks = (p.d + CK - 1) / CK, batches = (per_part + per - 1) / per, units = Q.n * batches;  // KW chunks or more
+  const int pieces = p.d * EB / 16, xrow = p.d * EB + kManyPad;
+  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  ManyWeights<FMT, ST> next;
+  auto load = [&](int u, int c) {
+    const int q = u / batches, i = (u - q * batches) * per + mine, row = min(i, per_part - 1) * 8 + (n16 & 7);
+    const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S;
+    next.load(buf_rsrc(rp, (uint32_t)p.S), (n16 < 8 ? 0u : R.up) + (uint32_t)row * (uint32_t)rb,
+              (n16 < 8 ? R.gs : R.us) + (uint32_t)row * (uint32_t)(p.d / 32), p.d, c, g, i < per_part);
+  };
+  if (u0 < u1) load(u0, kw);
+  int staged = -1;
+  for (int u = u0; u < u1; ++u) {
+    const int q = u / batches, n = __builtin_amdgcn_readfirstlane((int)Q.pairs[q]), first = __builtin_amdgcn_readfirstlane((int)Q.first[q]);
+    if (q != staged) {  // (nobody reads the rows of the part before: a barrier ended its last unit)
+      staged = q;
+      const int segs = (pieces + 63) >> 6, all = n * segs;
+      for (int s0 = wave; s0 < all; s0 += 4 * NW) {
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = min(s0 + e * NW, all - 1), r = s / segs, i = min((s - r * segs) * 64 + lane, pieces - 1);
+          v[e] = reinterpret_cast<const uint4*>(x + (size_t)(Q.pair[first + r] / p.k) * p.d * EB)[i];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = s0 + e * NW, r = s / segs, i = (s - r * segs) * 64 + lane;
+          if (s < all && i < pieces) vec[r * (xrow / 16) + i] = v[e];
+        }
+      }
+      __syncthreads();
+    }
+    const uint8_t* xr = reinterpret_cast<const uint8_t*>(vec) + min(n16, n - 1) * xrow;
+    typename Many<FMT>::Acc acc = {};
+    for (int c = kw; c < chunks; c += KW) {
+      const ManyWeights<FMT, ST> cur = next;
+      if (c + KW < chunks)
+        load(u, c + KW);
+      else if (u + 1 < u1)
+        load(u + 1, kw);
+      cur.template multiply<1>(acc, [&](int j, int) {
+        const int k = (c * ST + j) * KS + g * (16 / EB);
+        i32x4_t v = *reinterpret_cast<const i32x4_t*>(xr + (k < p.d ? k * EB : 0));
+        if (k >= p.d) v = i32x4_t{};  // x may be an infinity there
+        return v;
       });
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave * 256 + (4 * g + i) * 16 + n16] = acc[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < per * 128; e += NT) {
+      const int i = (u - q * batches) * per + (e >> 7), tk = (e >> 3) & 15, r = e & 7;
+      if (i >= per_part || tk >= n) continue;
+      const One* s = red + (e >> 7) * KW * 256 + tk * 16 + r;
+      One a = 0, b = 0;
+      for (int w = 0; w < KW; ++w) {
+        a += s[w * 256];
+        b += s[w * 256 + 8];
+      }
+      const int pair = Q.pair[first + tk], row = i * 8 + r;
+      if constexpr (FMT == FT_W_I8) {
+        const float* gs = reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.gs) + row;
+        const float ts = p.xs[pair / p.k], v = act_f(i8_value(a, gs[0], ts), FT_ACT_SILU) * i8_value(b, gs[p.f], ts);
+        static_cast<uint16_t*>(p.h)[(size_t)pair * p.f + row] = (uint16_t)pack2<false>(v, 0.0f);
+      } else {
+        const float v = silu(a) * b;
+        const int off = Q.off[q];
+        const size_t at = frag_place(off, Q.of[q], first - off + tk, (size_t)p.f * 2, (uint32_t)row * 2) >> 1;
+        uint16_t* h = static_cast<uint16_t*>(p.h);
+        const size_t plane = (size_t)p.T * p.k * p.f;
+        const uint32_t hi = pack2<false>(v, 0.0f) & 0xffffu;
+        float rest = v - bf_lo(hi);
+        if (!(fabsf(rest) < INFINITY)) rest = 0.0f;  // v not finite, or next to it
+        const uint32_t mid = pack2<false>(rest, 0.0f) & 0xffffu;
+        h[at] = (uint16_t)hi;
+        h[at + plane] = (uint16_t)mid;
+        h[at + 2 * plane] = (uint16_t)pack2<false>(rest - bf_lo(mid), 0.0f);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// 8-bit records: h's codes, a row by each block, where down multiplies them.
+__global__ __launch_bounds__(256) void moe_codes_kernel(MoeArgs p) {
+  __shared__ uint32_t red[4];
+  const Grouped& G = *p.grouped;
+  const int at = blockIdx.x;
+  if (at >= G.off[G.groups]) return;  // the whole block
+  const int pair = G.pair[at], grp = G.grp[pair], off = G.off[grp], n = G.off[grp + 1] - off;
+  quant_row<false, 256, 2>(static_cast<const uint16_t*>(p.h) + (size_t)pair * p.f, p.f,
+                           [&](int i) { return reinterpret_cast<uint2*>(p.hq + frag_place(off, n, at - off, p.f, (uint32_t)i * 8)); },
+                           p.hs + pair, red);
 }
 
 template <int FMT>
 __global__ __launch_bounds__(NT) void moe_down_many_kernel(MoeArgs p) {
-  constexpr int EB = Many<FMT>::EB, PARTS = Many<FMT>::PARTS, ST = FMT == FT_W_BF16 ? 2 : 4;
+  constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS, PARTS = Many<FMT>::PARTS, ST = FMT == FT_W_BF16 ? 2 : 4, CK = ST * KS;
   typedef typename Many<FMT>::One One;
   __shared__ Grouped P;
   __shared__ Parts Q;
   __shared__ One red[2][NW * 256];
   extern __shared__ uint4 vec[];  // results [pairs][kDownRows]
   float* out = reinterpret_cast<float*>(vec);
-  const int n_pairs = p.T * p.k, n16 = threadIdx.x & 15;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n16 = lane & 15, g = lane >> 4;
   grouped_to_lds(p, P);
   __syncthreads();
-  cut_groups(Q, P);
+  cut_groups(Q, P, 16);
   const Rec R = rec_of<FMT>(p.d, p.f);
-  const int rb = row_bytes<FMT>(p.f);
+  const int rb = row_bytes<FMT>(p.f), tiles = Q.n;
   const int b0 = blockIdx.x * p.rows, nr = min(p.rows, p.d - b0);
   const uint8_t* h = static_cast<const uint8_t*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h);
-  many_tiles<FMT, PARTS, ST>(
-      p, Q.n, 0, 1, kw_log_of<FMT, ST>(p.f), p.f, (size_t)n_pairs * p.f * EB, red,
-      [&](int i) {
-        ManyTile t;
-        const bool any = i < Q.n;
-        t.in = any && n16 < nr;
-        const int q = any ? i : 0;
-        t.rp = p.rec + (any ? (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S : 0);
-        t.row = h + (any ? (size_t)P.pair[Q.first[q] + min(n16, Q.pairs[q] - 1)] * p.f * EB : 0);
-        t.base = R.down + (uint32_t)(b0 + n16) * (uint32_t)rb;
-        t.sbase = R.ds + (uint32_t)(b0 + n16) * (uint32_t)(p.f / 32);
-        return t;
-      },
-      [&](int i0, const One* sums, int KW, int per) {
-        for (int e = threadIdx.x; e < per * 256; e += NT) {
-          const int q = i0 + (e >> 8), tk = (e >> 4) & 15, r = e & 15;
-          if (q >= Q.n || tk >= Q.pairs[q] || r >= nr) continue;
-          const One* s = sums + (e >> 8) * KW * 256 + tk * 16 + r;
-          One a = 0;
-          for (int w = 0; w < KW; ++w) a += s[w * 256];
-          const int pair = P.pair[Q.first[q] + tk];
-          if constexpr (FMT == FT_W_I8)
-            out[pair * kDownRows + r] =
-                i8_value(a, reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.ds)[b0 + r], p.hs[pair]);
-          else
-            out[pair * kDownRows + r] = a;
-        }
-      });
+  const size_t plane = (size_t)p.T * p.k * p.f * EB;
+  const int kw_log = kw_log_of<FMT, ST>(p.f), KW = 1 << kw_log, kw = wave & (KW - 1), per = NW >> kw_log, mine = wave >> kw_log;
+  const int chunks = (p.f + CK - 1) / CK;  // KW or more
+  ManyWeights<FMT, ST> next;
+  i32x4_t xn[ST][PARTS];
+  auto load = [&](int i, int c) {
+    const bool any = i < tiles;
+    const int q = any ? i : 0, n = any ? (int)Q.pairs[q] : 1;
+    const uint8_t* rp = p.rec + (any ? (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S : 0);
+    next.load(buf_rsrc(rp, (uint32_t)p.S), R.down + (uint32_t)(b0 + n16) * (uint32_t)rb,
+              R.ds + (uint32_t)(b0 + n16) * (uint32_t)(p.f / 32), p.f, c, g, any && n16 < nr);
+    // places of a part as frag_place has them: piece by piece, of each its n tokens
+    const uint8_t* row = h + (any ? (size_t)Q.first[q] * p.f * EB : 0) + min(n16, n - 1) * 16;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+      const int k = (c * ST + j) * KS + g * (16 / EB);
+#pragma unroll
+      for (int e = 0; e < PARTS; ++e) {
+        xn[j][e] = *reinterpret_cast<const i32x4_t*>(row + e * plane + (k < p.f ? (k * EB >> 4) * n * 16 : 0));
+        if (k >= p.f) xn[j][e] = i32x4_t{};  // h may be an infinity there
+      }
+    }
+  };
+  if (tiles > 0) load(mine, kw);
+  int buf = 0;
+  for (int b = 0; b < tiles; b += per) {
+    typename Many<FMT>::Acc acc = {};
+    for (int c = kw; c < chunks; c += KW) {
+      const ManyWeights<FMT, ST> cur = next;
+      i32x4_t x[ST][PARTS];
+#pragma unroll
+      for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) x[j][e] = xn[j][e];
+      if (c + KW < chunks)
+        load(b + mine, c + KW);
+      else if (b + per < tiles)
+        load(b + per + mine, kw);
+      cur.template multiply<PARTS>(acc, [&](int j, int e) { return x[j][e]; });
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[buf][wave * 256 + (4 * g + i) * 16 + n16] = acc[i];
+    __syncthreads();  // (the other buffer's sums were read before everyone came here)
+    for (int e = threadIdx.x; e < per * 256; e += NT) {
+      const int q = b + (e >> 8), tk = (e >> 4) & 15, r = e & 15;
+      if (q >= tiles || tk >= Q.pairs[q] || r >= nr) continue;
+      const One* s = red[buf] + (e >> 8) * KW * 256 + tk * 16 + r;
+      One a = 0;
+      for (int w = 0; w < KW; ++w) a += s[w * 256];
+      const int pair = Q.pair[Q.first[q] + tk];
+      if constexpr (FMT == FT_W_I8)
+        out[pair * kDownRows + r] =
+            i8_value(a, reinterpret_cast<const float*>(p.rec + (size_t)Q.slot[q] * p.S + R.ds)[b0 + r], p.hs[pair]);
+      else
+        out[pair * kDownRows + r] = a;
+    }
+    buf ^= 1;
+  }
   __syncthreads();
   sum_experts(p, P, out);
 }
@@ -943,7 +988,9 @@ __global__ __launch_bounds__(NT) void moe_down_many_kernel(MoeArgs p) {
 // ---- launches -----------------------------------------------------------------------------------
 constexpr int kUnits = 256;           // compute units
 constexpr size_t kVecLds = 136 << 10;  // most of a block's LDS for rows of x, or for results and rows of h
-constexpr size_t kManyLds = 96 << 10;
+// gate/up's matrix form: a part's x, beside the parts and sums (16 tokens of d = 4096 in bf16 take 128 KB)
+constexpr size_t kManyLds = 136 << 10;
+static_assert(sizeof(Plan) <= kManyLds && kManyLds + sizeof(Parts) + NW * 1024 <= 160 << 10, "");
 // Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
 constexpr size_t kOwnRows = 32 << 10;
 
@@ -966,12 +1013,17 @@ int moe_go(MoeArgs A, hipStream_t s) {
   if (A.rows > kDownRows) A.rows = kDownRows;
   const unsigned down_blocks = (unsigned)((A.d + A.rows - 1) / A.rows);
   if (many_tokens(A, FMT == FT_W_BF16 ? 7 : FMT == FT_W_MXFP4 ? 5 : 4)) {
-    const size_t lds = xb + (size_t)A.T * kManyPad;
-    A.lds_vec = lds <= kManyLds;
-    hipLaunchKernelGGL(moe_up_many_kernel<FMT>, dim3(kUnits), dim3(NT), A.lds_vec ? lds : 0, s, A);
+    const size_t row = (size_t)A.d * (FMT == FT_W_I8 ? 1 : 2) + kManyPad;
+    const size_t fit = kManyLds / row, part = fit < 16 ? fit : 16;  // 4 or more: d <= 16384
+    const size_t lds = (part < (size_t)A.T ? part : A.T) * row;
+    MoeArgs up = A;
+    up.rows = (int)part;
+    hipLaunchKernelGGL(moe_up_many_kernel<FMT>, dim3(kUnits), dim3(NT), lds > sizeof(Plan) ? lds : sizeof(Plan), s, up);
     if (int st = launched("moe_up_many_kernel")) return st;
-    if (FMT == FT_W_I8)
-      if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s)) return st;
+    if (FMT == FT_W_I8) {
+      hipLaunchKernelGGL(moe_codes_kernel, dim3((unsigned)P), dim3(256), 0, s, A);
+      if (int st = launched("moe_codes_kernel")) return st;
+    }
     hipLaunchKernelGGL(moe_down_many_kernel<FMT>, dim3(down_blocks), dim3(NT), P * kDownRows * 4, s, A);
     return launched("moe_down_many_kernel");
   }
