@@ -22,7 +22,7 @@ bool bad_shape(const ft_shape* s) {
 bool bad_tokens(const ft_shape* s, int32_t T) { return T < 0 || T > kMaxTokens || T * s->k > FT_PLAN_CAP; }
 
 struct Layout {
-  size_t logits, grouped, xv, xs, hq, hs, h, total;
+  size_t logits, grouped, xv, xs, hq, hs, h, part, total;
 };
 Layout layout(const ft_shape* s, int32_t T) {
   Layout l{};
@@ -43,8 +43,10 @@ Layout layout(const ft_shape* s, int32_t T) {
     l.h = take(P * s->d_ff * 2);
   } else {
     if (s->fmt == FT_W_MXFP4) l.xv = take((size_t)T * s->d * 2);
-    l.h = take(P * s->d_ff * 6);  // fp32, or three bf16 numbers
+    l.h = take(P * s->d_ff * 4);
   }
+  const int split = moe_down_split(s->d);
+  if (split > 1) l.part = take((size_t)split * T * s->d * 4);
   l.total = at + 256;
   return l;
 }
@@ -102,6 +104,7 @@ int ft_moe_layer(const ft_shape* shape, const void* x, int32_t T, const void* w_
   L.hq = reinterpret_cast<int8_t*>(ws + l.hq);
   L.hs = reinterpret_cast<float*>(ws + l.hs);
   L.h = ws + l.h;
+  L.part = reinterpret_cast<float*>(ws + l.part);
   return launch_moe_layer(L, stream);
 }
 

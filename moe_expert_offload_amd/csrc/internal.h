@@ -244,8 +244,14 @@ struct MoeLayer {
   void* xv;        // MXFP4: x [T, d] in another order; 8-bit records: codes of x, of h [T k, d_ff], and their scales
   int8_t* hq;
   float *xs, *hs;
-  void* h;  // [T k, d_ff], 6 bytes an element; 8-bit records bf16
+  void* h;      // [T k, d_ff] fp32; 8-bit records bf16
+  float* part;  // [moe_down_split(d), T, d] where that is above 1
 };
+// Matrix form of down: blocks that share 16 rows of y, so that a narrow d has blocks for every compute unit.
+inline int moe_down_split(int d) {
+  const int n = 256 / ((d + 15) / 16);
+  return n < 1 ? 1 : n > 16 ? 16 : n;
+}
 int launch_moe_layer(const MoeLayer& L, void* stream);
 
 // ---- host expert kernel (cpu_exec.cpp) ----------------------------------------
