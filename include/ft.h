@@ -544,7 +544,7 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
  *
  * Router, top-k, gates, the routed experts and their weighted sum in one call:
  *   y[t] = sum over j of gates[t, j] * W_down (silu(W_gate x_t) * (W_up x_t)) (+ residual[t])
- * over the experts idx[t, j], in the order of j.  shape: E, d, d_ff, k and the records' format (L is not
+ * over the experts idx[t, j].  shape: E, d, d_ff, k and the records' format (L is not
  * used, but positive); d <= 16384, d_ff <= 65536, a record below 2 GiB.  x: device bf16 [T, d], 0 <= T <= 64,
  * T * k <= FT_PLAN_CAP.  w_router, allowed, idx, gates: as for ft_router_topk, and with its bits (a row
  * that allows fewer than k experts gets idx -1 and gate 0 in the places left).
@@ -555,7 +555,8 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
  * y [T, d] and residual (may be NULL, may be y) of y_dtype, FT_T_BF16 or FT_T_FP32.
  * Arithmetic: FT_W_BF16 and FT_W_MXFP4 (weights dequantised exactly) apply to the bf16 x and to h in
  * fp32, fp32 sums.  FT_W_I8: x, and h rounded to bf16, are quantised as ft_i8_quant does, a product is
- * that of ft_i8_gemm.  The gates' sum and the residual are fp32, rounded once to y's type.
+ * that of ft_i8_gemm.  The gates' sum and the residual are fp32, rounded once to y's type; the order of sums in
+ * fp32 goes by the shape and T alone.
  * x, w_router, records 16-byte aligned; workspace: ft_moe_layer_workspace_bytes(shape, T),
  * 256-byte aligned; one for the most tokens serves fewer. */
 size_t ft_moe_layer_workspace_bytes(const ft_shape* shape, int32_t T);

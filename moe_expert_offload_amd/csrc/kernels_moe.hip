@@ -3,17 +3,22 @@
 //   logits = x W_r^T; the k largest of the allowed experts; gates = softmax over those
 //   y[t] = sum over j of gates[t, j] * Wd_e (silu(Wg_e x[t]) * (Wu_e x[t])), e = idx[t, j] (+ residual[t])
 //
-// Three launches (8-bit records of more than a few pairs: a fourth for h's codes): the logits, gate/up and down.  The second does the top-k of every token and groups
-// the routed pairs by expert, every block by itself (in LDS; a layer of 64 tokens has 512 pairs at most),
-// so that no launch and no wait across blocks lies between; the third sums a token's experts where they
-// leave their product, so there is no combine.  Both stream the routed experts' rows once, whatever
-// number of tokens takes them: a wavefront holds a few rows in registers and applies each token of
-// the expert to them (lane l takes the 16-byte pieces l, l + 64, ... of a row, 1 KB a load).  Bound by
-// memory.
+// Launches: the logits; the experts' gate and up products; 8-bit records of more than a few pairs: h's codes; the down
+// product.  More than 24 tokens: the top-k behind the logits.  The second does the top-k of every token otherwise, and groups
+// the routed pairs by expert, every block by itself (in LDS; a layer of 64 tokens has 512 pairs at most), so
+// that no launch and no wait across blocks lies between; the down product sums a token's experts where they leave
+// it, so there is no combine.  (Both products in one launch, down's blocks waiting for the parts of h that they need:
+// 77 us against 65 for one token, d = 4096, d_ff = 2048, top-6, bf16; a wait across XCDs costs more than a launch.)
+//
+// Both stream the routed experts' rows once, whatever number of tokens takes them: a wavefront holds a few rows in registers
+// and applies each token of the expert to them (lane l takes the 16-byte pieces l, l + 64, ... of a row, 1 KB a load).
+// Bound by memory: one token as above 64 us, 302 MB at 4.7 TB/s; 16 tokens in MXFP4 214 us, 5 TB/s.  From about 4
+// tokens an expert on by the vector instructions that apply each: there the matrix instructions take over (below).
 //
 // Records (bf16, MXFP4) as in include/ft.h; MXFP4 weights are dequantised exactly and applied to the bf16
 // x and the fp32 h.  8-bit records: x and h in 8 bits as ft_i8_quant gives them (h rounded to bf16 before),
 // whole-number sums, as the blocks of kernels_i8.hip.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -1059,12 +1064,14 @@ static_assert(sizeof(Plan) <= kManyLds && kManyLds + sizeof(Parts) + NW * 1024 <
 constexpr size_t kOwnRows = 32 << 10;
 
 // Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
-// meet if all are equally likely.  us at 4, 6, 8 and 16 tokens an expert, rows against matrix form: bf16 51 / 70, 92 / 131,
-// 86 / 51, 90 / 72; MXFP4 77 / 63, 170 / 127, 192 / 56, 117 / 72 (4 with wider rows: 259 / 355); 8-bit 52 / 43, 87 / 67,
-// 83 / 47, 66 / 46 (3: 101 / 101).
-bool many_tokens(const MoeArgs& A, double least) {
+// meet if all are equally likely.  The rows' form gains with their length, which fills its loads (not for bf16, whose rows
+// are long in bytes).  us of rows against matrix form (d x d_ff, tokens an expert):
+//   bf16    1024 x 512: 2.3 43 / 49, 4 52 / 50, 6 89 / 74   2048 x 768: 2.3 215 / 254, 4 292 / 291   4096 x 2048: 3 709 / 710, 6 1030 / 750
+//   MXFP4   1024 x 512: 2.1 38 / 35, 4 76 / 39, 6 167 / 55   2048 x 768: 2.3 147 / 164, 4 253 / 181   4096 x 2048: 4 74 / 77, 6 541 / 443
+//   8-bit   1024 x 512: 2.3 44 / 40, 4 53 / 40, 6 84 / 55   2048 x 768: 2.3 129 / 144, 4 170 / 158   4096 x 2048: 4 69 / 69, 6 430 / 358
+bool many_tokens(const MoeArgs& A, bool bf16) {
   const double pairs = (double)A.T * A.k, met = A.E * (1.0 - pow(1.0 - (double)A.k / A.E, A.T));
-  return pairs > least * met;
+  return pairs > (bf16 ? 4.5 : std::min(4.5, 1.0 + (A.d + A.f) / 1400.0)) * met;
 }
 
 // A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
@@ -1076,7 +1083,7 @@ int moe_go(MoeArgs A, hipStream_t s) {
   A.rows = (A.d + kUnits - 1) / kUnits;
   if (A.rows > kDownRows) A.rows = kDownRows;
   const unsigned down_blocks = (unsigned)((A.d + A.rows - 1) / A.rows);
-  if (many_tokens(A, FMT == FT_W_BF16 ? 7 : FMT == FT_W_MXFP4 ? 5 : 4)) {
+  if (many_tokens(A, FMT == FT_W_BF16)) {
     const size_t row = (size_t)A.d * (FMT == FT_W_I8 ? 1 : 2) + kManyPad;
     const size_t fit = kManyLds / row, part = fit < 16 ? fit : 16;  // 4 or more: d <= 16384
     const size_t lds = (part < (size_t)A.T ? part : A.T) * row;
