@@ -273,6 +273,29 @@ def test_rows_not_finite():
         R.check(b["y"][ok], want, "y")
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4", "i8"])
+def test_rows_not_finite_among_many(fmt):
+    """The same where experts have several tokens: a NaN, an infinity, and an x whose h passes the range."""
+    torch = torch_mod()
+    _say("moe not finite, many", fmt)
+    T, d, f = 40, 512, 128
+    L = Layer(T, d, f, 3, 2, fmt, 13)
+    L.x[3, 7] = float("nan")
+    L.x[17, 500] = float("inf")
+    L.x[33] = L.x[33] * 1e30  # products near 1e31, h past 1e60
+    L.dx.copy_(L.x)
+    b = L.buffers("fp32")
+    L.call(b, "fp32")
+    torch.cuda.synchronize()
+    bad = [3, 17, 33]
+    ok = [t for t in range(T) if t not in bad]
+    assert not torch.isfinite(b["y"][bad]).any()
+    idx, gates = L.routed()
+    assert torch.equal(b["idx"][ok], idx[ok]) and torch.equal(b["gates"][ok], gates[ok])
+    want = M.layer(L.x[ok], L.recs, L.slots(), idx[ok].cpu(), gates[ok].cpu(), d, f, fmt, torch.float32)
+    R.check(b["y"][ok], want, "y")
+
+
 def test_records_past_32_bits():
     """A record array of more than 2^32 bytes; the last experts are taken."""
     torch = torch_mod()
