@@ -708,43 +708,51 @@ struct Many {
   typedef typename std::conditional<FMT == FT_W_I8, int, float>::type One;
   typedef typename std::conditional<FMT == FT_W_I8, i32x4_t, f32x4_t>::type Acc;
 };
-// A lane's weights of a chunk of ST steps.
+// Where a lane's weights of a chunk are: a row of n elements at byte `base` of a record (scales at sbase), chunk `chunk` of it.
+struct ManyAt {
+  __amdgpu_buffer_rsrc_t rec;
+  uint32_t base, sbase;
+  int n, chunk, g;
+  bool in;
+};
+// A lane's weights of a chunk of ST steps; zeros past a row's end.
 template <int FMT, int ST>
 struct ManyWeights {
-  static constexpr int WL = FMT == FT_W_MXFP4 ? ST / 4 : ST;  // loads: one of MXFP4 codes is four steps
+  static constexpr int KS = Many<FMT>::KS, PER = FMT == FT_W_MXFP4 ? 4 : 1, WL = ST / PER;  // steps a load has, loads
   uint4 w[WL];
   uint32_t sc[FMT == FT_W_MXFP4 ? WL : 1];
-  // A row of n elements at byte `base` (scales at sbase); zeros past its end.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rec, uint32_t base, uint32_t sbase, int n, int chunk, int g, bool in) {
-    constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS;
-#pragma unroll
-    for (int l = 0; l < WL; ++l) {
-      if constexpr (FMT == FT_W_MXFP4) {
-        const int k = (chunk * WL + l) * 128;  // n is a multiple of 128
-        w[l] = buf_ld16(rec, in && k < n ? base + (uint32_t)((k + g * 32) >> 1) : kOOB);
-        sc[l] = __builtin_amdgcn_raw_buffer_load_b32(rec, (int)(in && k < n ? sbase + (uint32_t)(k >> 5) : kOOB), 0, 0);
-      } else {
-        const int k = (chunk * ST + l) * KS + g * (16 / EB);
-        w[l] = buf_ld16(rec, in && k < n ? base + (uint32_t)(k * EB) : kOOB);
-      }
+  __device__ __forceinline__ void load(const ManyAt& a, int l) {
+    if constexpr (FMT == FT_W_MXFP4) {
+      const int k = (a.chunk * WL + l) * 128;  // n is a multiple of 128
+      const bool in = a.in && k < a.n;
+      w[l] = buf_ld16(a.rec, in ? a.base + (uint32_t)((k + a.g * 32) >> 1) : kOOB);
+      sc[l] = __builtin_amdgcn_raw_buffer_load_b32(a.rec, (int)(in ? a.sbase + (uint32_t)(k >> 5) : kOOB), 0, 0);
+    } else {
+      const int k = (a.chunk * ST + l) * KS + a.g * (KS / 4);
+      w[l] = buf_ld16(a.rec, a.in && k < a.n ? a.base + (uint32_t)(k * Many<FMT>::EB) : kOOB);
     }
   }
-  // x(j, q): part q of the tokens' operand of step j.
-  template <int PARTS, class X>
-  __device__ __forceinline__ void multiply(typename Many<FMT>::Acc& acc, X x) const {
-    if constexpr (FMT == FT_W_I8) {
+  // Each load's steps, and in its place that of `next`: the chunk's loads stay on their way all the time.  x(j, q): part q of
+  // the tokens' operand of step j; used(j): x(j, .) is not asked for any more.
+  template <int PARTS, class X, class Used>
+  __device__ __forceinline__ void multiply(typename Many<FMT>::Acc& acc, const ManyAt& next, X x, Used used) {
 #pragma unroll
-      for (int j = 0; j < ST; ++j) acc = mfma16(x(j, 0), __builtin_bit_cast(i32x4_t, w[j]), acc);
-    } else if constexpr (FMT == FT_W_BF16) {
+    for (int l = 0; l < WL; ++l) {
+      if constexpr (FMT != FT_W_MXFP4) {
+        const i32x4_t wl = __builtin_bit_cast(i32x4_t, w[l]);
 #pragma unroll
-      for (int j = 0; j < ST; ++j)
-#pragma unroll
-        for (int q = PARTS - 1; q >= 0; --q) acc = mfma16<false>(x(j, q), __builtin_bit_cast(i32x4_t, w[j]), acc);
-    } else {
-#pragma unroll
-      for (int l = 0; l < WL; ++l) {
+        for (int q = PARTS - 1; q >= 0; --q) {
+          if constexpr (FMT == FT_W_I8)
+            acc = mfma16(x(l, q), wl, acc);
+          else
+            acc = mfma16<false>(x(l, q), wl, acc);
+        }
+        load(next, l);
+        used(l);
+      } else {
         // word j of quarter g to quarter j, word g
         uint32_t v[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
+        const uint32_t s4 = sc[l];
         auto s32 = [](uint32_t& a, uint32_t& b) {
           const u32x2_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
           a = r.x;
@@ -759,6 +767,7 @@ struct ManyWeights {
         s32(v[1], v[3]);
         s16(v[0], v[1]);
         s16(v[2], v[3]);
+        load(next, l);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const i32x4_t wj = {__builtin_bit_cast(int, mx_pair<0>(v[j])), __builtin_bit_cast(int, mx_pair<1>(v[j])),
@@ -766,11 +775,13 @@ struct ManyWeights {
           f32x4_t s = {};
 #pragma unroll
           for (int q = PARTS - 1; q >= 0; --q) s = mfma16<false>(x(4 * l + j, q), wj, s);
-          const float scale = e8m0((sc[l] >> (8 * j)) & 255u);
+          const float scale = e8m0((s4 >> (8 * j)) & 255u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = fmaf(scale, s[i], acc[i]);
+          used(4 * l + j);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
@@ -823,7 +834,7 @@ constexpr int kManyPad = 16;  // bytes between rows of x in LDS: 16 tokens' piec
 // x once or twice.
 template <int FMT>
 __global__ __launch_bounds__(NT) void moe_up_many_kernel(MoeArgs p) {
-  constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS, ST = FMT == FT_W_MXFP4 ? 8 : 4, CK = ST * KS;
+  constexpr int EB = Many<FMT>::EB, KS = Many<FMT>::KS, ST = 8, CK = ST * KS;
   typedef typename Many<FMT>::One One;
   __shared__ Parts Q;
   __shared__ One red[NW * 256];
@@ -841,14 +852,18 @@ __global__ __launch_bounds__(NT) void moe_up_many_kernel(MoeArgs p) {
   const int chunks = (p.d + CK - 1) / CK, batches = (per_part + per - 1) / per, units = Q.n * batches;  // KW chunks or more
   const int pieces = p.d * EB / 16, xrow = p.d * EB + kManyPad;
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
-  ManyWeights<FMT, ST> next;
-  auto load = [&](int u, int c) {
+  ManyWeights<FMT, ST> w;
+  auto place = [&](int u, int c, bool any) {
     const int q = u / batches, i = (u - q * batches) * per + mine, row = min(i, per_part - 1) * 8 + (n16 & 7);
     const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S;
-    next.load(buf_rsrc(rp, (uint32_t)p.S), (n16 < 8 ? 0u : R.up) + (uint32_t)row * (uint32_t)rb,
-              (n16 < 8 ? R.gs : R.us) + (uint32_t)row * (uint32_t)(p.d / 32), p.d, c, g, i < per_part);
+    return ManyAt{buf_rsrc(rp, (uint32_t)p.S), (n16 < 8 ? 0u : R.up) + (uint32_t)row * (uint32_t)rb,
+                  (n16 < 8 ? R.gs : R.us) + (uint32_t)row * (uint32_t)(p.d / 32), p.d, c, g, any && i < per_part};
   };
-  if (u0 < u1) load(u0, kw);
+  if (u0 < u1) {
+    const ManyAt at = place(u0, kw, true);
+#pragma unroll
+    for (int l = 0; l < ManyWeights<FMT, ST>::WL; ++l) w.load(at, l);
+  }
   int staged = -1;
   for (int u = u0; u < u1; ++u) {
     const int q = u / batches, n = __builtin_amdgcn_readfirstlane((int)Q.pairs[q]), first = __builtin_amdgcn_readfirstlane((int)Q.first[q]);
@@ -873,17 +888,14 @@ __global__ __launch_bounds__(NT) void moe_up_many_kernel(MoeArgs p) {
     const uint8_t* xr = reinterpret_cast<const uint8_t*>(vec) + min(n16, n - 1) * xrow;
     typename Many<FMT>::Acc acc = {};
     for (int c = kw; c < chunks; c += KW) {
-      const ManyWeights<FMT, ST> cur = next;
-      if (c + KW < chunks)
-        load(u, c + KW);
-      else if (u + 1 < u1)
-        load(u + 1, kw);
-      cur.template multiply<1>(acc, [&](int j, int) {
+      const bool here = c + KW < chunks, more = here || u + 1 < u1;
+      const ManyAt next = place(here || !more ? u : u + 1, here ? c + KW : kw, more);
+      w.template multiply<1>(acc, next, [&](int j, int) {
         const int k = (c * ST + j) * KS + g * (16 / EB);
         i32x4_t v = *reinterpret_cast<const i32x4_t*>(xr + (k < p.d ? k * EB : 0));
         if (k >= p.d) v = i32x4_t{};  // x may be an infinity there
         return v;
-      });
+      }, [](int) {});
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave * 256 + (4 * g + i) * 16 + n16] = acc[i];
@@ -953,7 +965,7 @@ __device__ __forceinline__ void cut3(const i32x4_t (&v)[2], i32x4_t (&x)[3]) {
 template <int FMT>
 __global__ __launch_bounds__(NT) void moe_down_many_kernel(MoeArgs p) {
   constexpr int EB = FMT == FT_W_I8 ? 1 : 4;  // bytes of an element of h
-  constexpr int KS = Many<FMT>::KS, PARTS = Many<FMT>::PARTS, HL = Many<FMT>::HL, ST = FMT == FT_W_BF16 ? 2 : 4, CK = ST * KS;
+  constexpr int KS = Many<FMT>::KS, PARTS = Many<FMT>::PARTS, HL = Many<FMT>::HL, ST = FMT == FT_W_I8 ? 8 : 4, CK = ST * KS;
   typedef typename Many<FMT>::One One;
   __shared__ Grouped P;
   __shared__ Parts Q;
@@ -974,50 +986,55 @@ __global__ __launch_bounds__(NT) void moe_down_many_kernel(MoeArgs p) {
   const uint8_t* h = static_cast<const uint8_t*>(FMT == FT_W_I8 ? (const void*)p.hq : p.h);
   const int kw_log = kw_log_of<FMT, ST>(p.f), KW = 1 << kw_log, kw = wave & (KW - 1), per = NW >> kw_log, mine = wave >> kw_log;
   const int chunks = (p.f + CK - 1) / CK;  // KW or more
-  ManyWeights<FMT, ST> next;
-  i32x4_t xn[ST][HL];
-  auto load = [&](int i, int c) {
+  ManyWeights<FMT, ST> w;
+  i32x4_t x[ST][HL];
+  struct Place {
+    ManyAt w;
+    const uint8_t* row;
+    int step;  // bytes from piece to piece
+  };
+  auto place = [&](int i, int c) {
     const bool any = i < tile1;
     const int q = any ? i : tile0, n = Q.pairs[q];
     const uint8_t* rp = p.rec + (size_t)__builtin_amdgcn_readfirstlane(Q.slot[q]) * p.S;
-    next.load(buf_rsrc(rp, (uint32_t)p.S), R.down + (uint32_t)(b0 + n16) * (uint32_t)rb,
-              R.ds + (uint32_t)(b0 + n16) * (uint32_t)(p.f / 32), p.f, c, g, any && n16 < nr);
-    // places of a part as frag_place has them: piece by piece, of each its n tokens
-    const uint8_t* row = h + (size_t)Q.first[q] * p.f * EB + min(n16, n - 1) * 16;
-#pragma unroll
-    for (int j = 0; j < ST; ++j) {
-      const int k = (c * ST + j) * KS + g * (KS / 4);
-#pragma unroll
-      for (int e = 0; e < HL; ++e) {
-        xn[j][e] = *reinterpret_cast<const i32x4_t*>(row + ((k < p.f ? k * EB >> 4 : 0) + e) * n * 16);
-        if (k >= p.f) xn[j][e] = i32x4_t{};  // h may be an infinity there
-      }
-    }
+    return Place{ManyAt{buf_rsrc(rp, (uint32_t)p.S), R.down + (uint32_t)(b0 + n16) * (uint32_t)rb,
+                        R.ds + (uint32_t)(b0 + n16) * (uint32_t)(p.f / 32), p.f, c, g, any && n16 < nr},
+                 // a part as frag_place has it: piece by piece, of each its n tokens
+                 h + (size_t)Q.first[q] * p.f * EB + min(n16, n - 1) * 16, n * 16};
   };
-  if (tile0 < tile1) load(tile0 + mine, kw);
+  auto load_x = [&](const Place& a, int j) {
+    const int k = (a.w.chunk * ST + j) * KS + g * (KS / 4);
+#pragma unroll
+    for (int e = 0; e < HL; ++e) x[j][e] = *reinterpret_cast<const i32x4_t*>(a.row + ((k < p.f ? k * EB >> 4 : 0) + e) * a.step);
+  };
+  if (tile0 < tile1) {
+    const Place at = place(tile0 + mine, kw);
+#pragma unroll
+    for (int l = 0; l < ManyWeights<FMT, ST>::WL; ++l) w.load(at.w, l);
+#pragma unroll
+    for (int j = 0; j < ST; ++j) load_x(at, j);
+  }
   int buf = 0;
   for (int b = tile0; b < tile1; b += per) {
     typename Many<FMT>::Acc acc = {};
     for (int c = kw; c < chunks; c += KW) {
-      const ManyWeights<FMT, ST> cur = next;
-      i32x4_t x[ST][HL];
-#pragma unroll
-      for (int j = 0; j < ST; ++j)
-#pragma unroll
-        for (int e = 0; e < HL; ++e) x[j][e] = xn[j][e];
-      if (c + KW < chunks)
-        load(b + mine, c + KW);
-      else if (b + per < tile1)
-        load(b + per + mine, kw);
+      const bool here = c + KW < chunks;
+      const Place next = place(here ? b + mine : b + per < tile1 ? b + per + mine : tile1, here ? c + KW : kw);
       i32x4_t x3[3];
-      cur.template multiply<PARTS>(acc, [&](int j, int e) {
-        if constexpr (FMT == FT_W_I8) {
-          return x[j][0];
-        } else {
-          if (e == PARTS - 1) cut3(x[j], x3);  // asked for first
-          return x3[e];
-        }
-      });
+      w.template multiply<PARTS>(
+          acc, next.w,
+          [&](int j, int e) {
+            if constexpr (FMT == FT_W_I8) {
+              return x[j][0];
+            } else {
+              if (e == PARTS - 1) {  // asked for first
+                if ((c * ST + j) * KS + g * (KS / 4) >= p.f) x[j][0] = x[j][1] = i32x4_t{};  // h may be an infinity there
+                cut3(x[j], x3);
+              }
+              return x3[e];
+            }
+          },
+          [&](int j) { load_x(next, j); });
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[buf][wave * 256 + (4 * g + i) * 16 + n16] = acc[i];
