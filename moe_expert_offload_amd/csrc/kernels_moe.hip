@@ -1081,14 +1081,24 @@ static_assert(sizeof(Plan) <= kManyLds && kManyLds + sizeof(Parts) + NW * 1024 <
 constexpr size_t kOwnRows = 32 << 10;
 
 // Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
-// meet if all are equally likely.  The rows' form gains with their length, which fills its loads (not for bf16, whose rows
-// are long in bytes).  us of rows against matrix form (d x d_ff, tokens an expert):
-//   bf16    1024 x 512: 2.3 43 / 49, 4 52 / 50, 6 89 / 74   2048 x 768: 2.3 215 / 254, 4 292 / 291   4096 x 2048: 3 709 / 710, 6 1030 / 750
-//   MXFP4   1024 x 512: 2.1 38 / 35, 4 76 / 39, 6 167 / 55   2048 x 768: 2.3 147 / 164, 4 253 / 181   4096 x 2048: 4 74 / 77, 6 541 / 443
-//   8-bit   1024 x 512: 2.3 44 / 40, 4 53 / 40, 6 84 / 55   2048 x 768: 2.3 129 / 144, 4 170 / 158   4096 x 2048: 4 69 / 69, 6 430 / 358
-bool many_tokens(const MoeArgs& A, bool bf16) {
-  const double pairs = (double)A.T * A.k, met = A.E * (1.0 - pow(1.0 - (double)A.k / A.E, A.T));
-  return pairs > (bf16 ? 4.5 : std::min(4.5, 1.0 + (A.d + A.f) / 1400.0)) * met;
+// meet if all are equally likely.  How many are enough goes by the rows' length (d + d_ff), which fills the rows' form's loads
+// and not the other's, and by the elements that the layer reads, against the matrix form's longer way to its first
+// product (MXFP4, whose conversions it saves, gains all the same).  us of rows against matrix form at so many tokens an expert:
+//                        bf16                         MXFP4                                8-bit
+//   1024 x 512 of 16..128  2.3 43 / 46, 4 52 / 47     2.2 38 / 34, 3.2 171 / 74              2.3 56 / 51, 4 53 / 44
+//   2048 x 768 of 128    2.7 240 / 251, 4.1 291 / 260   2.3 146 / 147, 2.7 178 / 158, 4.1 255 / 162   2.7 140 / 141, 4.1 170 / 145
+//   2048 x 768 of 8      4 43 / 47, 8 61 / 51         4 48 / 38                            4 36 / 41, 8 49 / 42
+//   4096 x 2048 of 64    3.1 714 / 634, 6 1030 / 669   3.1 326 / 369, 3.8 378 / 371         3.1 315 / 307, 6 430 / 307
+//   256 x 128 of 64      8 82 / 38                    8 - / 35                             8 79 / 41
+//   4096 x 14336 of 8    4 752 / 546                  3.1 265 / 321, 4 336 / 323             3.1 302 / 275, 4 368 / 277
+template <int FMT>
+bool many_tokens(const MoeArgs& A) {
+  const double pairs = (double)A.T * A.k, met = A.E * (1.0 - pow(1.0 - (double)A.k / A.E, A.T)), row = A.d + A.f;
+  const double read = met * A.d * A.f, start = std::min(1.5, 16.7e6 / read);
+  const double least = FMT == FT_W_BF16    ? 2.8 + start
+                       : FMT == FT_W_MXFP4 ? std::min(3.9, 1.55 + row / 2700)
+                                           : std::min(2.7, 0.1 + row / 1000) + start;
+  return pairs > least * met;
 }
 
 // A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
@@ -1100,7 +1110,7 @@ int moe_go(MoeArgs A, hipStream_t s) {
   A.rows = (A.d + kUnits - 1) / kUnits;
   if (A.rows > kDownRows) A.rows = kDownRows;
   const unsigned down_blocks = (unsigned)((A.d + A.rows - 1) / A.rows);
-  if (many_tokens(A, FMT == FT_W_BF16)) {
+  if (many_tokens<FMT>(A)) {
     const size_t row = (size_t)A.d * (FMT == FT_W_I8 ? 1 : 2) + kManyPad;
     const size_t fit = kManyLds / row, part = fit < 16 ? fit : 16;  // 4 or more: d <= 16384
     const size_t lds = (part < (size_t)A.T ? part : A.T) * row;
