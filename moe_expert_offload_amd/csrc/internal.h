@@ -247,7 +247,8 @@ struct MoeLayer {
   void* h;      // [T k, d_ff] fp32; 8-bit records bf16
   float* part;  // [moe_down_split(d), T, d] where that is above 1
 };
-// Matrix form of down: blocks that share 16 rows of y, so that a narrow d has blocks for every compute unit.
+// Matrix form of down: blocks that share 16 rows of y, so that a narrow d has blocks for every compute unit (64 tokens, E = 64,
+// k = 6, d = 1024, d_ff = 512: MXFP4 92 us with rows dealt to all units instead, so 55).
 inline int moe_down_split(int d) {
   const int n = 256 / ((d + 15) / 16);
   return n < 1 ? 1 : n > 16 ? 16 : n;

@@ -12,7 +12,7 @@
 //
 // Both stream the routed experts' rows once, whatever number of tokens takes them: a wavefront holds a few rows in registers
 // and applies each token of the expert to them (lane l takes the 16-byte pieces l, l + 64, ... of a row, 1 KB a load).
-// Bound by memory: one token as above 64 us, 302 MB at 4.7 TB/s; 16 tokens in MXFP4 214 us, 5 TB/s.  From about 4
+// Bound by memory: one token as above 64 us, 302 MB at 4.7 TB/s; 16 tokens in MXFP4 214 us, 5 TB/s.  From about 3
 // tokens an expert on by the vector instructions that apply each: there the matrix instructions take over (below).
 //
 // Records (bf16, MXFP4) as in include/ft.h; MXFP4 weights are dequantised exactly and applied to the bf16
@@ -689,8 +689,8 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
 // The same products for groups of several tokens, cut into parts of up to 16: a tile is 16 rows of an expert (gate/up: 8
 // of each) and the tokens of a part, weights as the MFMA's second operand, so that each is loaded and converted
 // once a part.  Lane l: row (and token) l % 16, in a step the k of its quarter l / 16.  KW wavefronts share a tile's
-// chunks and add their sums in LDS; the block's others take further tiles, and the next chunk's weights, of this tile
-// or the next one, are on their way while one is multiplied.
+// chunks and add their sums in LDS; the block's others take further tiles.  The next chunk, of this tile or the next one,
+// is on its way while one is multiplied, each load leaving as its registers are used up.
 //   bf16   v_mfma_f32_16x16x32_bf16
 //   MXFP4  the same on codes turned into bf16 exactly; a step is one block of 32, whose scale multiplies its
 //          fp32 sum; exchanges across the wave bring a lane's block to the quarters
@@ -699,6 +699,8 @@ __global__ __launch_bounds__(NT) void moe_down_kernel(MoeArgs p) {
 // MFMA; the matrix cores have room for that.
 // Loads of 64 bytes from each of 16 rows, as the weights', cost the load unit four times what 1 KB in a line does, so the
 // tokens' operands do not come that way: gate/up holds a part's x in LDS, and h lies in memory as down multiplies it (frag_place).
+// 64 tokens, 32 an expert, d = 2048, d_ff = 768 in bf16: with both gathered 185 us, so 107 (gate/up 48, 100 MB of weights read
+// once per 16 tokens; down 43, each block reading all of h).
 template <int FMT>
 struct Many {
   static constexpr int KS = FMT == FT_W_I8 ? 64 : 32;   // k of a step
@@ -1077,8 +1079,10 @@ constexpr size_t kVecLds = 136 << 10;  // most of a block's LDS for rows of x, o
 // gate/up's matrix form: a part's x, beside the parts and sums (16 tokens of d = 4096 in bf16 take 128 KB)
 constexpr size_t kManyLds = 136 << 10;
 static_assert(sizeof(Plan) <= kManyLds && kManyLds + sizeof(Parts) + NW * 1024 <= 160 << 10, "");
-// Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all.
-constexpr size_t kOwnRows = 32 << 10;
+// Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all (us itself
+// against the launch: 6144 elements 20.9 / 22.6, 12288 37.4 / 40.5, 24576 46.1 / 46.2 and 61.6 / 65.6, 36864 58.9 / 57.2, 79872
+// 88.7 / 83.1; two rows of 14336 92.4 / 83.3, a wavefront each).
+constexpr size_t kOwnRows = 24 << 10;
 
 // Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
 // meet if all are equally likely.  How many are enough goes by the rows' length (d + d_ff), which fills the rows' form's loads
