@@ -45,7 +45,7 @@ Layout layout(const ft_shape* s, int32_t T) {
     if (s->fmt == FT_W_MXFP4) l.xv = take((size_t)T * s->d * 2);
     l.h = take(P * s->d_ff * 4);
   }
-  const int split = moe_down_split(s->d);
+  const int split = moe_down_split(s->d, s->E);
   if (split > 1) l.part = take((size_t)split * T * s->d * 4);
   l.total = at + 256;
   return l;

@@ -245,13 +245,13 @@ struct MoeLayer {
   int8_t* hq;
   float *xs, *hs;
   void* h;      // [T k, d_ff] fp32; 8-bit records bf16
-  float* part;  // [moe_down_split(d), T, d] where that is above 1
+  float* part;  // [moe_down_split(d, E), T, d] where that is above 1
 };
 // Matrix form of down: blocks that share 16 rows of y, so that a narrow d has blocks for every compute unit (64 tokens, E = 64,
-// k = 6, d = 1024, d_ff = 512: MXFP4 92 us with rows dealt to all units instead, so 55).
-inline int moe_down_split(int d) {
-  const int n = 256 / ((d + 15) / 16);
-  return n < 1 ? 1 : n > 16 ? 16 : n;
+// k = 6, d = 1024, d_ff = 512: MXFP4 92 us with rows dealt to all units instead, so 55).  Each takes some of the experts.
+inline int moe_down_split(int d, int E) {
+  const int n = 256 / ((d + 15) / 16), most = E < 16 ? E : 16;
+  return n < 1 ? 1 : n > most ? most : n;
 }
 int launch_moe_layer(const MoeLayer& L, void* stream);
 
