@@ -57,7 +57,7 @@ struct MoeArgs {
   float* gates;
   int ranked;  // both are there
   Grouped* grouped;
-  void* xv;    // x as it is multiplied: bf16 x itself, MXFP4 in planes, 8-bit records codes (scales xs)
+  void* xv;    // x as it is multiplied: bf16 x itself, MXFP4 in planes (the matrix form: x itself), 8-bit records codes (scales xs)
   float* xs;
   int8_t* hq;  // 8-bit records: h in 8 bits (scales hs)
   float* hs;
@@ -352,7 +352,7 @@ __device__ __forceinline__ void load_parts(uint4 (&v)[NV], const uint4* row, int
   for (int q = 0; q < NV; ++q) v[q] = row[q * pieces + i];
 }
 
-// ---- logits; MXFP4: and x in planes, 8-bit records: and x in 8 bits, a row by each of the last blocks ------
+// ---- logits; and by each of the last blocks, where a form multiplies it so, a row of x in planes (MXFP4) or in 8 bits ------
 template <int FMT, int TT, int TE>
 __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs p, const uint16_t* __restrict__ w, float* logits, int eb,
                                                          int blocks) {
@@ -1109,14 +1109,14 @@ bool many_tokens(const MoeArgs& A) {
 
 // A lane holds W pieces of weights at once: rows of up to 64 JC pieces in one go, the longer the fewer of them.
 template <int FMT, int W>
-int moe_go(MoeArgs A, hipStream_t s) {
+int moe_go(MoeArgs A, bool many, hipStream_t s) {
   const size_t P = (size_t)A.T * A.k;
   const size_t xb = (size_t)A.T * A.d * (FMT == FT_W_I8 ? 1 : 2);
   constexpr int E = Fmt<FMT>::E;
   A.rows = (A.d + kUnits - 1) / kUnits;
   if (A.rows > kDownRows) A.rows = kDownRows;
   const unsigned down_blocks = (unsigned)((A.d + A.rows - 1) / A.rows);
-  if (many_tokens<FMT>(A)) {
+  if (many) {
     const size_t row = (size_t)A.d * (FMT == FT_W_I8 ? 1 : 2) + kManyPad;
     const size_t fit = kManyLds / row, part = fit < 16 ? fit : 16;  // 4 or more: d <= 16384
     const size_t lds = (part < (size_t)A.T ? part : A.T) * row;
@@ -1202,7 +1202,9 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
   // few logits a wavefront: their sums run in a fixed order and so one behind the other
   const int tt = L.T == 1 ? 1 : L.T <= 16 ? 2 : 4, te = L.T == 1 ? 1 : 2;
   const int eb = (L.E + 4 * te - 1) / (4 * te), blocks = eb * ((L.T + tt - 1) / tt);
-  const dim3 grid((unsigned)(blocks + (L.fmt == FT_W_BF16 ? 0 : L.T)));
+  const bool many = L.fmt == FT_W_BF16 ? many_tokens<FT_W_BF16>(A) : L.fmt == FT_W_MXFP4 ? many_tokens<FT_W_MXFP4>(A) : many_tokens<FT_W_I8>(A);
+  const bool rows = L.fmt == FT_W_I8 || (L.fmt == FT_W_MXFP4 && !many);  // the matrix form reads 16-bit x as it is
+  const dim3 grid((unsigned)(blocks + (rows ? L.T : 0)));
   auto logits = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, A, L.w_router, L.logits, eb, blocks); };
   auto by_format = [&](auto bf16, auto mx, auto i8) { L.fmt == FT_W_BF16 ? logits(bf16) : L.fmt == FT_W_MXFP4 ? logits(mx) : logits(i8); };
   if (tt == 1)
@@ -1216,9 +1218,9 @@ int launch_moe_layer(const MoeLayer& L, void* stream) {
     hipLaunchKernelGGL(moe_topk_kernel, dim3((unsigned)A.T), dim3(64), 0, s, A);
     if (int st = launched("moe_topk_kernel")) return st;
   }
-  if (L.fmt == FT_W_I8) return moe_go<FT_W_I8, 16>(A, s);
-  if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 8>(A, s);
-  return moe_go<FT_W_BF16, 16>(A, s);
+  if (L.fmt == FT_W_I8) return moe_go<FT_W_I8, 16>(A, many, s);
+  if (L.fmt == FT_W_MXFP4) return moe_go<FT_W_MXFP4, 8>(A, many, s);
+  return moe_go<FT_W_BF16, 16>(A, many, s);
 }
 
 }  // namespace ft
