@@ -10,7 +10,7 @@ using namespace ft;
 
 namespace {
 
-constexpr int32_t kMaxK = 1 << 16;  // sums of K products of 8-bit integers stay below 2^30
+constexpr int32_t kMaxK = 1 << 16;  // sums of K products of 8-bit integers: at most 2^30 in magnitude
 constexpr int32_t kMaxN = (1 << 26) - 256;  // a grid of 1024 threads for 16 channels has fewer than 2^32
 
 // Tiles of 128 x 128 whose grid has fewer than 2^32 threads.

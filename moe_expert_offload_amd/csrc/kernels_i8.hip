@@ -5,7 +5,7 @@
 //   y[t, n] = (sum over k of q[t, k] c[n, k]) * scale[n] * s[t] (+ residual)
 //   block: h = act(a) * u rounded to the activations' type, quantised as x is, then the down product
 //
-// The sums are whole numbers in 32 bits, exact in any order (K <= 65536: below 2^30); the two scales
+// The sums are whole numbers in 32 bits, exact in any order (K <= 65536: at most 2^30 in magnitude); the two scales
 // and the residual are applied in fp32.  h is rounded to 16 bits on its way to its codes: its row's
 // largest element is known only when all of its product's tiles are done, so h goes through
 // memory, and half the bytes cost less than 1/127 of the largest does.
