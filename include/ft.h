@@ -48,7 +48,10 @@
  * layer l, expert e reads record (l mod L_phys)*E + e.
  *
  * MXFP4 arithmetic: decode (the row-streaming form) and the CPU branch apply the
- * exactly dequantised weights to the bf16 activations.  Prefill (the MFMA form)
+ * exactly dequantised weights to the bf16 activations.  The device sums a block's 32
+ * products in fp32 before it applies the scale: x or h for which 6 * sum |v| over a block
+ * passes fp32's largest value (32 equal ones past 1.7e36) may give infinities or NaN
+ * where the scale would have brought the sum back.  Prefill (the MFMA form)
  * runs on gfx950's scaled MFMA with E4M3 x E2M1 operands: x and the SwiGLU output
  * h are converted to MXFP8 (E4M3 elements, one E8M0 scale per 32 consecutive
  * elements along the reduction axis, shared exponent floor(log2 max|v|) - 8,
@@ -553,8 +556,8 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
  * outside [0, n_slots) is left out of the sum (its gate stands): with the cache's residency as slot_of,
  * y is the device's part of the layer.
  * y [T, d] and residual (may be NULL, may be y) of y_dtype, FT_T_BF16 or FT_T_FP32.
- * Arithmetic: FT_W_BF16 and FT_W_MXFP4 (weights dequantised exactly) apply to the bf16 x and to h in
- * fp32, fp32 sums.  FT_W_I8: x, and h rounded to bf16, are quantised as ft_i8_quant does, a product is
+ * Arithmetic: FT_W_BF16 and FT_W_MXFP4 (weights dequantised exactly, range as under "MXFP4 arithmetic"
+ * above) apply to the bf16 x and to h in fp32, fp32 sums.  FT_W_I8: x, and h rounded to bf16, are quantised as ft_i8_quant does, a product is
  * that of ft_i8_gemm.  The gates' sum and the residual are fp32, rounded once to y's type; the order of sums in
  * fp32 goes by the shape and T alone.
  * x, w_router, records 16-byte aligned; workspace: ft_moe_layer_workspace_bytes(shape, T),
