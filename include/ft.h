@@ -499,8 +499,7 @@ int ft_w4_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- products in 8-bit integers ---------------------------------------------------
- * As the dense operators above: stateless, asynchronous, to be captured, nothing
- * allocated; equal calls give equal bits.
+ * Streams, captured graphs, workspaces, overlaps and equal bits as for the dense operators above.
  *
  * Rows in 8 bits.  src: `dtype` (bf16 or fp16) [rows, n], n a multiple of 16 up to 2^16, ld as
  * for the dense operators; codes int8 [rows, n], contiguous; scales fp32 [rows] (4-byte
@@ -543,7 +542,7 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- a routed layer for a few tokens, its experts on the device -------------------
- * Stateless, asynchronous, to be captured, nothing allocated; equal calls give equal bits.
+ * Streams, captured graphs, workspaces, overlaps and equal bits as for the dense operators above.
  *
  * Router, top-k, gates, the routed experts and their weighted sum in one call:
  *   y[t] = sum over j of gates[t, j] * W_down (silu(W_gate x_t) * (W_up x_t)) (+ residual[t])
@@ -553,8 +552,10 @@ int ft_i8_gated_ffn(const void* x, int64_t ldx, int32_t T, int32_t dtype, int32_
  * that allows fewer than k experts gets idx -1 and gate 0 in the places left).
  * records: n_slots records one after another, 16-byte aligned.  slot_of: device int32 [E], the
  * record of each expert, or NULL: record e is expert e's (n_slots >= E).  An expert whose slot is
- * outside [0, n_slots) is left out of the sum (its gate stands): with the cache's residency as slot_of,
- * y is the device's part of the layer.
+ * outside [0, n_slots) is left out of the sum (its gate stands).  On an expert cache: records its
+ * slots, slot_of what ft_expert_cache_where gives for each expert of the layer, copied to the device by
+ * the caller; y is then the sum over the resident experts, as long as no call changes the cache before
+ * this one has run, and behind the fills that the table counts on.
  * y [T, d] and residual (may be NULL, may be y) of y_dtype, FT_T_BF16 or FT_T_FP32.
  * Arithmetic: FT_W_BF16 and FT_W_MXFP4 (weights dequantised exactly, range as under "MXFP4 arithmetic"
  * above) apply to the bf16 x and to h in fp32, fp32 sums.  FT_W_I8: x, and h rounded to bf16, are quantised as ft_i8_quant does, a product is
