@@ -51,7 +51,7 @@ struct I8Args {
   int64_t ldr;
   uint16_t* h;  // kGateUp: [M, N]
   // how tiles are shared: see I8Cut
-  int tiles_m, tiles_n, whole, rest, blocks, per, parts;
+  int tiles_m, tiles_n, whole, blocks, per, parts;
   int* part;  // sums of pieces
 };
 
@@ -774,7 +774,6 @@ int i8_go(I8Args& A, hipStream_t s) {
   A.tiles_m = c.tiles_m;
   A.tiles_n = c.tiles_n;
   A.whole = c.whole;
-  A.rest = c.rest;
   A.blocks = c.blocks;
   A.per = c.per;
   A.parts = c.parts;
