@@ -1081,9 +1081,13 @@ constexpr size_t kVecLds = 136 << 10;  // most of a block's LDS for rows of x, o
 // gate/up's matrix form: a part's x, beside the parts and sums (16 tokens of d = 4096 in bf16 take 128 KB)
 constexpr size_t kManyLds = 136 << 10;
 static_assert(sizeof(Plan) <= kManyLds && kManyLds + sizeof(Parts) + NW * 1024 <= 160 << 10, "");
-// Elements of h up to which each block of the down product makes h's codes itself, in place of a launch for all (us itself
-// against the launch: 6144 elements 20.9 / 22.6, 12288 37.4 / 40.5, 24576 46.1 / 46.2 and 61.6 / 65.6, 36864 58.9 / 57.2, 79872
-// 88.7 / 83.1; two rows of 14336 92.4 / 83.3, a wavefront each).
+// Elements of a row of h, and of all of h, up to which each block of the down product makes h's codes itself, in place of a launch
+// for all.  A row goes to one wavefront, which holds 2048 elements and reads the rest twice (us of a layer, itself against the
+// launch, d = 4096, one token, 1 / 2 / 4 rows: of 2048 19.2 / 20.7, 24.8 / 26.8, 32.3 / 35.6; of 4096 24.6 / 24.6, 35.4 / 36.0,
+// 52.9 / 54.1; of 6144 30.4 / 28.4, 46.4 / 45.5, 72.1 / 72.3; one of 8192 35.6 / 32.4, of 14336 51.6 / 42.7, of 24576 85.3 / 67.2;
+// rows of 768 and 2048: 6144 elements 20.9 / 22.6, 12288 37.4 / 40.5, 24576 46.1 / 46.2 and 61.6 / 65.6, 36864 58.9 / 57.2,
+// 79872 88.7 / 83.1).
+constexpr int kOwnRow = 4096;
 constexpr size_t kOwnRows = 24 << 10;
 
 // Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
@@ -1150,7 +1154,7 @@ int moe_go(MoeArgs A, bool many, hipStream_t s) {
   const size_t hb = P * A.f * (FMT == FT_W_I8 ? 1 : 4), ob = P * kDownRows * 4;
   A.lds_vec = hb <= kVecLds - ob;
   if (FMT == FT_W_I8) {
-    if (P * A.f <= kOwnRows && A.lds_vec)
+    if (A.f <= kOwnRow && P * A.f <= kOwnRows && A.lds_vec)
       A.hq = nullptr;
     else if (int st = launch_i8_quant(static_cast<const uint16_t*>(A.h), A.f, (int)P, A.f, false, A.hq, A.hs, s))
       return st;
