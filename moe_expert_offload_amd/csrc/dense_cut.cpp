@@ -118,7 +118,7 @@ size_t gated_ffn_part_bound(int64_t T, int d, int d_ff, bool backward) {
 //   64 x 128 tiles, two to a unit, three stages in LDS: 0.45 a stage while there is one to a unit, 0.78 for two, + 1.5
 //   128 x 128 tiles, two to a unit: 0.85 to 1.1, + 2.5; one to a unit, three stages: 0.64, + 2.2
 //   128 x 256 tiles, one to a unit: 0.88, with more than 192 of them up to 1.05, + 2
-//   256 x 256 tiles, one to a unit: 1.2, with more than 140 of them up to 1.85 (power), + 3
+//   256 x 256 tiles, one to a unit: 1.2, with more than 140 of them up to 1.85 (the clock falls, among other things), + 3
 //   joining shared tiles: 4.5, and what the pieces write and the join reads
 // against 3 us and the weights at 2.8 (up to 32 rows) or 1.5 TB/s where they stream (up to 64 rows; each 16 channels
 // read all tokens' codes, which is what bounds that way).  The best of all ways that were timed is within 10 % of the

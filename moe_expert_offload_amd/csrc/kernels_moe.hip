@@ -1091,7 +1091,8 @@ constexpr int kOwnRow = 4096;
 constexpr size_t kOwnRows = 24 << 10;
 
 // Whether the experts that are taken are taken by enough tokens for the matrix forms: as many as T tokens with k of E each
-// meet if all are equally likely.  How many are enough goes by the rows' length (d + d_ff), which fills the rows' form's loads
+// meet if all are equally likely, allowed and given a record (by the shape and T alone, as the order of sums is; where a few experts take
+// most tokens, the rows' form runs past the point where the other is faster).  How many are enough goes by the rows' length (d + d_ff), which fills the rows' form's loads
 // and not the other's, and by the elements that the layer reads, against the matrix form's longer way to its first
 // product (MXFP4, whose conversions it saves, gains all the same).  us of rows against matrix form at so many tokens an expert:
 //                        bf16                         MXFP4                                8-bit
